@@ -9,6 +9,7 @@ The library must have been built (``python allgather_gemm_amd/build.py`` or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -74,6 +75,20 @@ def lib() -> ctypes.CDLL:
         L.tgather_ex.argtypes = [_vp, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
                                  _i32, _i32, _vp]
         L.tgather_ex.restype = ctypes.c_int
+        for name, n in (("gemm_bias_act_workspace", 3), ("gemm_xent_workspace", 3), ("gemm_xent_bwd_workspace", 3)):
+            getattr(L, name).argtypes = [_i64] * n
+            getattr(L, name).restype = _i64
+        L.gemm_bias_act_bwd_workspace.argtypes = [_i64, _i64, _i64, _i32]
+        L.gemm_bias_act_bwd_workspace.restype = _i64
+        L.gemm_bias_act.argtypes = [_vp] * 4 + [_i64] * 3 + [_i32, _vp, _vp, _vp, _i64, _vp]
+        L.gemm_bias_act_bwd.argtypes = [_vp] * 4 + [_i64] * 3 + [_i32] + [_vp] * 4 + [_i64, _vp]
+        L.gemm_grouped.argtypes = [_vp] * 3 + [_i32] + [_i64] * 3 + [_vp, _vp]
+        L.gemm_grouped_bwd.argtypes = [_vp] * 4 + [_i32] + [_i64] * 3 + [_vp, _vp, _vp]
+        L.gemm_xent.argtypes = [_vp] * 3 + [_i64] * 3 + [_vp] * 3 + [_i64, _vp]
+        L.gemm_xent_bwd.argtypes = [_vp] * 5 + [_i64] * 3 + [_vp] * 3 + [_i64, _vp]
+        for name in ("gemm_bias_act", "gemm_bias_act_bwd", "gemm_grouped", "gemm_grouped_bwd", "gemm_xent",
+                     "gemm_xent_bwd"):
+            getattr(L, name).restype = ctypes.c_int
         L.ag_check.argtypes = [_vp, ctypes.POINTER(_i64)]
         L.ag_check.restype = ctypes.c_int
         L.ag_status_str.argtypes = [ctypes.c_int]
@@ -282,6 +297,190 @@ def tgather(shards, valid_rows: int, valid_cols: int, dst: torch.Tensor | None =
     if rc != AG_OK:
         raise AgError(rc, "tgather_ex")
     return dst
+
+
+# ------------------------------------------------------------------------ language-model operators
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+
+
+def _need(t, name: str, shape: tuple, dtype=torch.bfloat16, device=None):
+    """Checks a tensor argument; returns its device pointer (None for an absent one)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s must be %s %s, not %s %s" % (name, shape, dtype, tuple(t.shape), t.dtype))
+    _check_dev(t, name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, device))
+    return t.data_ptr()
+
+
+def _dims(t, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError("%s must have %d dimensions" % (name, n))
+    return t.shape
+
+
+class _on:
+    """The stream a call runs on: outputs and scratch memory are allocated on it, so that they are not
+    handed to other work before the call's kernels are done with them."""
+
+    def __init__(self, stream, device):
+        self.device = device
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+        self.guard = None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+@functools.lru_cache(maxsize=4096)
+def _work_bytes(entry: str, device: int, *extents) -> int:
+    return getattr(lib(), entry + "_workspace")(*extents)
+
+
+def _work(entry: str, device, *extents):
+    """(tensor, bytes) of the scratch memory that a call asks for."""
+    n = _work_bytes(entry, device.index, *extents)
+    return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
+
+
+def _done(rc: int, entry: str):
+    if rc != AG_OK:
+        raise AgError(rc, entry)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                  residual: torch.Tensor | None = None, C: torch.Tensor | None = None,
+                  pre: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """C (M, Nc) = act(A @ B^T + bias) + residual, all bf16, sums in fp32.  A (M, K), B (Nc, K), bias (Nc),
+    residual (M, Nc); act: "none" | "relu" | "silu" | "gelu" (erf) | "gelu_tanh".  pre: optional (M, Nc)
+    output that receives A @ B^T + bias, which gemm_bias_act_bwd needs.  residual may be C itself."""
+    M, K = _dims(A, "A", 2)
+    Nc = _dims(B, "B", 2)[0]
+    dev = A.device
+    a, b = _need(A, "A", (M, K)), _need(B, "B", (Nc, K), device=dev)
+    bi, r = _need(bias, "bias", (Nc,), device=dev), _need(residual, "residual", (M, Nc), device=dev)
+    pr = _need(pre, "pre", (M, Nc), device=dev)
+    with _on(stream, dev) as s:
+        if C is None:
+            C = torch.empty((M, Nc), dtype=torch.bfloat16, device=dev)
+        c = _need(C, "C", (M, Nc), device=dev)
+        w, n = _work("gemm_bias_act", dev, M, Nc, K)
+        _done(lib().gemm_bias_act(a, b, bi, r, M, Nc, K, _ACTS[act], c, pr, _p(w), n, s), "gemm_bias_act")
+    return C
+
+
+def gemm_bias_act_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, act: str = "none",
+                      pre: torch.Tensor | None = None, need_dA: bool = True, need_dB: bool = True,
+                      need_dbias: bool = True, stream=None):
+    """Gradients of gemm_bias_act: (dA (M, K), dB (Nc, K), dbias (Nc)) for dC (M, Nc), None where not
+    needed.  pre: what gemm_bias_act stored (act "none" needs none).  The residual's gradient is dC."""
+    M, K = _dims(A, "A", 2)
+    Nc = _dims(B, "B", 2)[0]
+    dev = A.device
+    d, a = _need(dC, "dC", (M, Nc), device=dev), _need(A, "A", (M, K))
+    b, pr = _need(B, "B", (Nc, K), device=dev), _need(pre, "pre", (M, Nc), device=dev)
+    code = _ACTS[act]
+    if code != ACT_NONE and pre is None:
+        raise ValueError("act %r needs pre" % act)
+    with _on(stream, dev) as s:
+        dA = torch.empty_like(A) if need_dA else None
+        dB = torch.empty_like(B) if need_dB else None
+        dbias = torch.empty((Nc,), dtype=torch.bfloat16, device=dev) if need_dbias else None
+        w, n = _work("gemm_bias_act_bwd", dev, M, Nc, K, code)
+        _done(lib().gemm_bias_act_bwd(d, a, b, pr, M, Nc, K, code, _p(dA), _p(dB), _p(dbias), _p(w), n, s),
+              "gemm_bias_act_bwd")
+    return dA, dB, dbias
+
+
+def gemm_grouped(A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, C: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Rows [ends[e-1], ends[e]) of C (M, Nc) = the same rows of A (M, K) @ B[e]^T, B (E, Nc, K), all bf16;
+    rows past ends[-1] are zero.  ends: (E,) int32 on the device, the running sums of the experts' row
+    counts; it is not read on the host."""
+    M, K = _dims(A, "A", 2)
+    E, Nc, _ = _dims(B, "B", 3)
+    dev = A.device
+    a, b = _need(A, "A", (M, K)), _need(B, "B", (E, Nc, K), device=dev)
+    en = _need(ends, "ends", (E,), torch.int32, dev)
+    with _on(stream, dev) as s:
+        if C is None:
+            C = torch.empty((M, Nc), dtype=torch.bfloat16, device=dev)
+        c = _need(C, "C", (M, Nc), device=dev)
+        _done(lib().gemm_grouped(a, b, en, E, M, Nc, K, c, s), "gemm_grouped")
+    return C
+
+
+def gemm_grouped_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, need_dA: bool = True,
+                     need_dB: bool = True, stream=None):
+    """Gradients of gemm_grouped: (dA (M, K), dB (E, Nc, K)) for dC (M, Nc), None where not needed."""
+    M, K = _dims(A, "A", 2)
+    E, Nc, _ = _dims(B, "B", 3)
+    dev = A.device
+    d, a = _need(dC, "dC", (M, Nc), device=dev), _need(A, "A", (M, K))
+    b, en = _need(B, "B", (E, Nc, K), device=dev), _need(ends, "ends", (E,), torch.int32, dev)
+    with _on(stream, dev) as s:
+        dA = torch.empty_like(A) if need_dA else None
+        dB = torch.empty_like(B) if need_dB else None
+        _done(lib().gemm_grouped_bwd(d, a, b, en, E, M, Nc, K, _p(dA), _p(dB), s), "gemm_grouped_bwd")
+    return dA, dB
+
+
+def gemm_xent(A: torch.Tensor, B: torch.Tensor, targets: torch.Tensor, stream=None):
+    """Cross entropy of the logits A @ B^T, which are never stored: (loss, lse), both (T,) fp32, for A (T, K),
+    B (V, K) bf16 and targets (T,) int64.  A target outside [0, V) marks a row without one: loss 0, no
+    gradient."""
+    T, K = _dims(A, "A", 2)
+    V = _dims(B, "B", 2)[0]
+    dev = A.device
+    a, b = _need(A, "A", (T, K)), _need(B, "B", (V, K), device=dev)
+    y = _need(targets, "targets", (T,), torch.int64, dev)
+    with _on(stream, dev) as s:
+        loss = torch.empty((T,), dtype=torch.float32, device=dev)
+        lse = torch.empty((T,), dtype=torch.float32, device=dev)
+        w, n = _work("gemm_xent", dev, T, V, K)
+        _done(lib().gemm_xent(a, b, y, T, V, K, loss.data_ptr(), lse.data_ptr(), _p(w), n, s), "gemm_xent")
+    return loss, lse
+
+
+def gemm_xent_bwd(dloss: torch.Tensor, A: torch.Tensor, B: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                  need_dA: bool = True, need_dB: bool = True, work_bytes: int | None = None, stream=None):
+    """Gradients of gemm_xent: (dA (T, K), dB (V, K)) for dloss (T,) fp32 and gemm_xent's lse, None where not
+    needed.  work_bytes: scratch memory to use, where the default (d logits in pieces of up to 512 MiB) is
+    too much; fewer bytes make more, narrower pieces of the vocabulary."""
+    T, K = _dims(A, "A", 2)
+    V = _dims(B, "B", 2)[0]
+    dev = A.device
+    a, b = _need(A, "A", (T, K)), _need(B, "B", (V, K), device=dev)
+    y, g = _need(targets, "targets", (T,), torch.int64, dev), _need(dloss, "dloss", (T,), torch.float32, dev)
+    ls = _need(lse, "lse", (T,), torch.float32, dev)
+    with _on(stream, dev) as s:
+        dA = torch.empty_like(A) if need_dA else None
+        dB = torch.empty_like(B) if need_dB else None
+        if work_bytes is None:
+            w, n = _work("gemm_xent_bwd", dev, T, V, K)
+        else:
+            n = work_bytes
+            w = torch.empty(n, dtype=torch.uint8, device=dev)
+        _done(lib().gemm_xent_bwd(g, a, b, y, ls, T, V, K, _p(dA), _p(dB), _p(w), n, s), "gemm_xent_bwd")
+    return dA, dB
 
 
 def check(stream=None) -> tuple[int, list[int]]:

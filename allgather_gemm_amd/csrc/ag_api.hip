@@ -47,6 +47,20 @@ int hip_fail(hipError_t e, const char* what)
             return hip_fail(e_, what);         \
     } while (0)
 
+}  // namespace
+
+// For the entry points of other files: no exception leaves it, also when the text cannot be stored.
+int hip_error(hipError_t e, const char* what) noexcept
+{
+    try {
+        return hip_fail(e, what);
+    } catch (...) {
+        return AG_EHIP;
+    }
+}
+
+namespace {
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int current_ws(Workspace** out)

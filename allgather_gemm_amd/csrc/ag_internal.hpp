@@ -112,6 +112,9 @@ hipError_t launch_producer(const GemmArgs& a, const FusedPlan& f, hipStream_t st
 
 hipError_t device_cus(int* out);
 
+// Records a HIP error for ag_last_error() and returns AG_EHIP (ag_api.hip).
+int hip_error(hipError_t e, const char* what) noexcept;
+
 // Small helper kernel: p[0..n) = value (flag epochs, GEMM-only flags).
 hipError_t launch_fill_u32(uint32_t* p, int64_t n, uint32_t value, hipStream_t stream);
 

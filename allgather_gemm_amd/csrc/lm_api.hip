@@ -1,0 +1,405 @@
+// lm_api.hip -- entry points of the language-model operators declared in include/aggemm.h: argument
+// checks, the plan of each product (tile, splits, workspace layout) and the launches.  They keep no
+// state: the workspace is the caller's, so calls on different streams are independent and a call can
+// be captured into a graph.
+#include "../../include/aggemm.h"
+#include "ag_internal.hpp"
+#include "lm_internal.hpp"
+
+#include <algorithm>
+
+namespace ag {
+namespace lm {
+namespace {
+
+constexpr int64_t kMaxDim = 1 << 21;              // columns of any operand: 32-bit tile offsets
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kPieceBytes = 512 << 20;        // d logits held at a time
+
+#define LM_HIP(call, what)               \
+    do {                                 \
+        hipError_t e_ = (call);          \
+        if (e_ != hipSuccess)            \
+            return hip_error(e_, what);  \
+    } while (0)
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// a tensor that must be there when it has elements
+bool bad(const void* p, int64_t elements, uintptr_t n = 16) { return (elements > 0 && !p) || !aligned(p, n); }
+int64_t up(int64_t x, int64_t n) { return (x + n - 1) / n * n; }
+int64_t region(int64_t bytes) { return up(bytes, 256); }
+
+int cus()
+{
+    int n = 0;
+    if (device_cus(&n) != hipSuccess || n <= 0)
+        n = 256;
+    return n;
+}
+
+// One product (M, N, K): its tile and how many parts the reduction is split into.
+struct Plan {
+    Tile tile;
+    int splits;
+    int64_t split_steps;
+    int64_t part_bytes(int64_t M, int64_t N) const { return splits > 1 ? region(splits * M * up(N, 8) * 4) : 0; }
+};
+
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32)
+{
+    Plan p;
+    const int64_t n = cus();
+    auto tiles = [&](Tile t) { return ((M + tile_m(t) - 1) / tile_m(t)) * ((N + tile_n(t) - 1) / tile_n(t)); };
+    if (rows32 && M <= 32)
+        p.tile = kTile32;
+    else
+        p.tile = tiles(kTile256) * 2 >= n ? kTile256 : kTile128;
+    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64), t = std::max<int64_t>(1, tiles(p.tile));
+    const int64_t room = p.tile == kTile128 ? 2 * n : n;
+    int64_t s = std::max<int64_t>(1, std::min(room / t, steps / 4));
+    p.split_steps = (steps + s - 1) / s;
+    p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
+    return p;
+}
+
+TileArgs product(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M, int64_t N, int64_t K, void* C,
+                 int64_t ldc)
+{
+    TileArgs a = {};
+    a.A = static_cast<const __bf16*>(A);
+    a.B = static_cast<const __bf16*>(B);
+    a.lda = lda;
+    a.ldb = ldb;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.k_valid = K;
+    a.splits = 1;
+    a.vec = ldc % 8 == 0;
+    a.out.C = static_cast<__bf16*>(C);
+    a.out.ldc = ldc;
+    return a;
+}
+
+// Launches a product by its plan; a split one is joined through `part`.
+template <typename Launch>
+hipError_t run_product(Launch launch, const Plan& p, TileArgs a, void* part, hipStream_t s)
+{
+    if (p.splits > 1) {
+        a.splits = p.splits;
+        a.split_steps = p.split_steps;
+        a.part = static_cast<float*>(part);
+        a.ldp = up(a.N, 8);
+    }
+    hipError_t e = launch(p.tile, a, s);
+    if (e == hipSuccess && p.splits > 1)
+        e = launch_join(a.part, p.splits, a.M, a.N, a.ldp, a.out, a.vec, s);
+    return e;
+}
+
+hipError_t nt_linear(Tile t, const TileArgs& a, hipStream_t s) { return launch_nt(t, kEpiLinear, a, s); }
+
+struct LinearBwd {
+    bool own_d;              // d = dC act'(pre) is written to the workspace
+    int64_t ldd;
+    Plan da, db;
+    int64_t d_bytes, sum_bytes, part_bytes;
+    int64_t bytes() const { return d_bytes + sum_bytes + part_bytes; }
+};
+
+LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
+{
+    LinearBwd w;
+    w.own_d = act != kActNone || Nc % 8 != 0;
+    w.ldd = up(Nc, 8);
+    w.da = plan_product(M, K, w.ldd, true);
+    w.db = plan_product(Nc, K, M, false);
+    w.d_bytes = w.own_d ? region(M * w.ldd * 2) : 0;
+    w.sum_bytes = region(colsum_rows(M) * Nc * 4);
+    w.part_bytes = std::max(w.da.part_bytes(M, K), w.db.part_bytes(Nc, K));
+    return w;
+}
+
+Tile xent_tile(int64_t T) { return T <= 32 ? kTile32 : T <= 128 ? kTile128 : kTile256; }
+
+int64_t stat_pairs(Tile t, int64_t V) { return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t)); }
+
+struct XentBwd {
+    int64_t piece;           // columns of the vocabulary at a time, a multiple of 256
+    int64_t pieces;
+    Plan da;
+    bool part;               // dA is summed in fp32 in the workspace
+    int64_t part_bytes, db_part_bytes;
+    int64_t bytes(int64_t T) const { return region(T * piece * 2) + part_bytes + db_part_bytes; }
+};
+
+XentBwd plan_xent_bwd(int64_t T, int64_t V, int64_t K, int64_t piece)
+{
+    XentBwd w;
+    w.piece = piece;
+    w.pieces = (V + piece - 1) / piece;
+    w.da = plan_product(T, K, std::min(up(V, 8), piece), true);
+    w.part = w.pieces > 1 || w.da.splits > 1;
+    w.part_bytes = w.part ? region((int64_t)w.da.splits * T * K * 4) : 0;
+    w.db_part_bytes = 0;
+    return w;
+}
+
+// Equal pieces of at most kPieceBytes of d logits; fewer columns, down to 256, where the workspace is
+// smaller than that.
+XentBwd plan_xent_bwd_in(int64_t T, int64_t V, int64_t K, int64_t room)
+{
+    const int64_t most = std::max<int64_t>(256, kPieceBytes / std::max<int64_t>(1, T * 2) / 256 * 256);
+    for (int64_t n = (V + most - 1) / most;; ++n) {
+        const XentBwd w = plan_xent_bwd(T, V, K, up((V + n - 1) / n, 256));
+        if (w.piece == 256 || w.bytes(T) <= room)
+            return w;
+    }
+}
+
+bool shapes_ok(int64_t M, int64_t Nc, int64_t K)
+{
+    return M >= 0 && Nc >= 0 && K >= 0 && K % 8 == 0;
+}
+
+bool too_large(int64_t M, int64_t Nc, int64_t K) { return K > kMaxDim || Nc > kMaxDim || M > kMaxRows; }
+
+}  // namespace
+}  // namespace lm
+}  // namespace ag
+
+using namespace ag;
+using namespace ag::lm;
+
+extern "C" int64_t gemm_bias_act_workspace(int64_t M, int64_t Nc, int64_t K)
+{
+    if (!shapes_ok(M, Nc, K) || too_large(M, Nc, K))
+        return 0;
+    return plan_product(M, Nc, K, true).part_bytes(M, Nc);
+}
+
+extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, int64_t M, int64_t Nc,
+                             int64_t K, int32_t act, void* C, void* pre, void* work, int64_t work_bytes, void* stream)
+{
+    if (!shapes_ok(M, Nc, K) || act < kActNone || act > kActGeluTanh)
+        return AG_EINVAL;
+    if (M == 0 || Nc == 0)
+        return AG_OK;
+    if (bad(A, K) || bad(B, K) || bad(C, 1) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16))
+        return AG_EINVAL;
+    if (too_large(M, Nc, K))
+        return AG_EUNSUPPORTED;
+    const Plan p = plan_product(M, Nc, K, true);
+    if (work_bytes < p.part_bytes(M, Nc) || bad(work, p.part_bytes(M, Nc)))
+        return AG_EINVAL;
+    TileArgs a = product(A, K, B, K, M, Nc, K, C, Nc);
+    a.out.bias = static_cast<const __bf16*>(bias);
+    a.out.residual = static_cast<const __bf16*>(residual);
+    a.out.pre = static_cast<__bf16*>(pre);
+    a.out.act = act;
+    LM_HIP(run_product(nt_linear, p, a, work, static_cast<hipStream_t>(stream)), "launch gemm_bias_act");
+    return AG_OK;
+}
+
+extern "C" int64_t gemm_bias_act_bwd_workspace(int64_t M, int64_t Nc, int64_t K, int32_t act)
+{
+    if (!shapes_ok(M, Nc, K) || too_large(M, Nc, K))
+        return 0;
+    return plan_linear_bwd(M, Nc, K, act).bytes();
+}
+
+extern "C" int gemm_bias_act_bwd(const void* dC, const void* A, const void* B, const void* pre, int64_t M, int64_t Nc,
+                                 int64_t K, int32_t act, void* dA, void* dB, void* dbias, void* work, int64_t work_bytes,
+                                 void* stream)
+{
+    if (!shapes_ok(M, Nc, K) || act < kActNone || act > kActGeluTanh)
+        return AG_EINVAL;
+    if (bad(dC, M * Nc) || (dB && bad(A, M * K)) || (dA && bad(B, Nc * K)) || (act != kActNone && bad(pre, M * Nc)) ||
+        !aligned(dA, 16) || !aligned(dB, 16) || !aligned(dbias, 16) || !aligned(pre, 16))
+        return AG_EINVAL;
+    if (too_large(M, Nc, K))
+        return AG_EUNSUPPORTED;
+    const LinearBwd w = plan_linear_bwd(M, Nc, K, act);
+    if (work_bytes < w.bytes() || bad(work, w.bytes()))
+        return AG_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(work);
+    const void* d = dC;
+    float* sum = reinterpret_cast<float*>(ws + w.d_bytes);
+    void* part = ws + w.d_bytes + w.sum_bytes;
+    const bool want_d = w.own_d && (dA || dB);
+    if (want_d)
+        d = ws;
+    if (want_d || dbias)
+        LM_HIP(launch_act_bwd(static_cast<const __bf16*>(dC), static_cast<const __bf16*>(pre), act, M, Nc,
+                              want_d ? reinterpret_cast<__bf16*>(ws) : nullptr, w.ldd, dbias ? sum : nullptr, s),
+               "launch act_bwd");
+    if (dbias)
+        LM_HIP(launch_colsum_join(sum, colsum_rows(M), Nc, static_cast<__bf16*>(dbias), s), "launch colsum_join");
+    if (dA) {
+        TileArgs a = product(d, w.ldd, B, K, M, K, w.ldd, dA, K);
+        a.k_valid = Nc;
+        LM_HIP(run_product(launch_nn, w.da, a, part, s), "launch dA");
+    }
+    if (dB)
+        LM_HIP(run_product(launch_tn, w.db, product(d, w.ldd, A, K, Nc, K, M, dB, K), part, s), "launch dB");
+    return AG_OK;
+}
+
+static bool groups_ok(const void* ends, int32_t E, int64_t M, int64_t Nc, int64_t K)
+{
+    return shapes_ok(M, Nc, K) && Nc % 8 == 0 && E >= 1 && !bad(ends, 1, 4);
+}
+
+// Tile of the products whose rows are grouped, by the mean rows of a group.
+static Tile group_tile(int64_t M, int32_t E)
+{
+    const int64_t mean = M / E;
+    return mean <= 32 ? kTile32 : mean < 192 ? kTile128 : kTile256;
+}
+
+extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M, int64_t Nc, int64_t K,
+                            void* C, void* stream)
+{
+    if (!groups_ok(ends, E, M, Nc, K))
+        return AG_EINVAL;
+    if (M == 0 || Nc == 0)
+        return AG_OK;
+    if (bad(A, K) || bad(B, K) || bad(C, 1))
+        return AG_EINVAL;
+    if (too_large(M, Nc, K) || E > kMaxGroups)
+        return AG_EUNSUPPORTED;
+    TileArgs a = product(A, K, B, K, M, Nc, K, C, Nc);
+    a.ends = ends;
+    a.E = E;
+    a.group = kGroupRows;
+    a.strideB = Nc * K;
+    LM_HIP(launch_nt(group_tile(M, E), kEpiLinear, a, static_cast<hipStream_t>(stream)), "launch gemm_grouped");
+    return AG_OK;
+}
+
+extern "C" int gemm_grouped_bwd(const void* dC, const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M,
+                                int64_t Nc, int64_t K, void* dA, void* dB, void* stream)
+{
+    if (!groups_ok(ends, E, M, Nc, K))
+        return AG_EINVAL;
+    if (bad(dC, M * Nc) || (dB && bad(A, M * K)) || (dA && bad(B, Nc * K)) || !aligned(dA, 16) || !aligned(dB, 16))
+        return AG_EINVAL;
+    if (too_large(M, Nc, K) || E > kMaxGroups)
+        return AG_EUNSUPPORTED;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (dA && M > 0 && K > 0) {
+        TileArgs a = product(dC, Nc, B, K, M, K, Nc, dA, K);
+        a.ends = ends;
+        a.E = E;
+        a.group = kGroupRows;
+        a.strideB = Nc * K;
+        LM_HIP(launch_nn(group_tile(M, E), a, s), "launch dA");
+    }
+    if (dB && Nc > 0 && K > 0) {
+        TileArgs a = product(dC, Nc, A, K, Nc, K, M, dB, K);
+        a.ends = ends;
+        a.E = E;
+        a.group = kGroupK;
+        LM_HIP(launch_tn(((Nc + 255) / 256) * ((K + 255) / 256) * E * 2 >= cus() ? kTile256 : kTile128, a, s), "launch dB");
+    }
+    return AG_OK;
+}
+
+static bool xent_shapes_ok(int64_t T, int64_t V, int64_t K) { return shapes_ok(T, V, K) && V >= 1; }
+
+extern "C" int64_t gemm_xent_workspace(int64_t T, int64_t V, int64_t K)
+{
+    if (!xent_shapes_ok(T, V, K) || too_large(T, V, K))
+        return 0;
+    return region(T * stat_pairs(xent_tile(T), V) * 8) + region(T * 4);
+}
+
+extern "C" int gemm_xent(const void* A, const void* B, const int64_t* targets, int64_t T, int64_t V, int64_t K, float* loss,
+                         float* lse, void* work, int64_t work_bytes, void* stream)
+{
+    if (!xent_shapes_ok(T, V, K))
+        return AG_EINVAL;
+    if (T == 0)
+        return AG_OK;
+    if (bad(A, K) || bad(B, K) || bad(targets, 1, 8) || bad(loss, 1, 4) || bad(lse, 1, 4) || bad(work, 1))
+        return AG_EINVAL;
+    if (too_large(T, V, K))
+        return AG_EUNSUPPORTED;
+    if (work_bytes < gemm_xent_workspace(T, V, K))
+        return AG_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Tile t = xent_tile(T);
+    TileArgs a = product(A, K, B, K, T, V, K, nullptr, 0);
+    a.stat_n = stat_pairs(t, V);
+    a.stat = static_cast<float*>(work);
+    a.hit = reinterpret_cast<float*>(static_cast<char*>(work) + region(T * a.stat_n * 8));
+    a.targets = targets;
+    LM_HIP(launch_nt(t, kEpiStat, a, s), "launch gemm_xent");
+    LM_HIP(launch_xent_join(a.stat, a.stat_n, a.hit, targets, T, V, loss, lse, s), "launch xent_join");
+    return AG_OK;
+}
+
+extern "C" int64_t gemm_xent_bwd_workspace(int64_t T, int64_t V, int64_t K)
+{
+    if (!xent_shapes_ok(T, V, K) || too_large(T, V, K))
+        return 0;
+    return plan_xent_bwd_in(T, V, K, INT64_MAX).bytes(T);
+}
+
+extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, const int64_t* targets, const float* lse,
+                             int64_t T, int64_t V, int64_t K, void* dA, void* dB, void* work, int64_t work_bytes,
+                             void* stream)
+{
+    if (!xent_shapes_ok(T, V, K))
+        return AG_EINVAL;
+    if (bad(A, T * K) || bad(B, K) || bad(targets, T, 8) || bad(dloss, T, 4) || bad(lse, T, 4) || !aligned(dA, 16) ||
+        !aligned(dB, 16))
+        return AG_EINVAL;
+    if (too_large(T, V, K))
+        return AG_EUNSUPPORTED;
+    if (K == 0 || (!dA && !dB))
+        return AG_OK;
+    const XentBwd w = plan_xent_bwd_in(T, V, K, work_bytes);
+    if (work_bytes < w.bytes(T) || bad(work, w.bytes(T)))
+        return AG_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(work);
+    float* part = reinterpret_cast<float*>(ws + region(T * w.piece * 2));
+    const int64_t ldd = w.piece;
+    for (int64_t i = 0; i < w.pieces; ++i) {
+        const int64_t v0 = i * w.piece, n = std::min(w.piece, V - v0);
+        const char* Bp = static_cast<const char*>(B) + v0 * K * 2;
+        TileArgs a = product(A, K, Bp, K, T, n, K, ws, ldd);
+        a.targets = targets;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.vocab = V;
+        a.col0 = v0;
+        LM_HIP(launch_nt(xent_tile(T), kEpiGrad, a, s), "launch d logits");
+        if (dA) {
+            a = product(ws, ldd, Bp, K, T, K, up(n, 8), dA, K);
+            a.k_valid = n;
+            if (w.part) {
+                a.splits = w.da.splits;
+                a.split_steps = w.da.split_steps;
+                a.part = part;
+                a.ldp = K;
+                a.accumulate = i > 0;
+            }
+            LM_HIP(launch_nn(w.da.tile, a, s), "launch dA");
+        }
+        if (dB) {
+            a = product(ws, ldd, A, K, n, K, T, static_cast<char*>(dB) + v0 * K * 2, K);
+            const Plan p = plan_product(n, K, T, false);
+            LM_HIP(launch_tn(p.tile, a, s), "launch dB");
+        }
+    }
+    if (dA && w.part) {
+        LinearOut out = {};
+        out.C = static_cast<__bf16*>(dA);
+        out.ldc = K;
+        LM_HIP(launch_join(part, w.da.splits, T, K, K, out, true, s), "launch dA join");
+    }
+    return AG_OK;
+}

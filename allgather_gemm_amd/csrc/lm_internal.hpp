@@ -1,0 +1,85 @@
+// lm_internal.hpp -- host-side interface between the entry points of the language-model operators
+// (lm_api.hip) and their kernels (lm_nt.hip, lm_nn.hip, lm_tn.hip, lm_small.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ag {
+
+namespace lm {
+
+constexpr int kMaxGroups = 1024;
+
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+enum Group { kGroupNone = 0, kGroupRows = 1, kGroupK = 2 };
+enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2 };
+enum Tile { kTile256 = 0, kTile128 = 1, kTile32 = 2 };
+
+// C = act(sum + bias) + residual, pre = sum + bias (pre, bias, residual may be null)
+struct LinearOut {
+    __bf16* C;
+    const __bf16* bias;
+    const __bf16* residual;
+    __bf16* pre;
+    int64_t ldc;
+    int act;
+};
+
+struct TileArgs {
+    const __bf16 *A, *B;
+    int64_t lda, ldb;        // row strides in elements, multiples of 8
+    int64_t M, N, K;
+    int64_t k_valid;         // rows that a (K, N) B has where X's rows are zero-padded to K (launch_nn)
+    int64_t tiles_m, tiles_n;
+    // groups: rows [ends[e-1], ends[e]) of A (kGroupRows), or of the reduction (kGroupK; out.C of
+    // group e starts at e * M * ldc)
+    const int32_t* ends;
+    int E, group;
+    int64_t strideB;         // elements from one group's B to the next
+    // split reduction: split s takes K steps [s * split_steps, ...) and writes its fp32 sums to
+    // part + s * M * ldp
+    int splits;
+    int64_t split_steps;
+    float* part;
+    int64_t ldp;             // multiple of 8
+    int accumulate;          // add to part instead of writing it
+    bool vec;                // rows of C, pre and residual start at 16-byte boundaries
+    LinearOut out;
+    // softmax statistics of each row's columns: stat[row][stat_n][2] = (maximum, sum of exponentials)
+    float* stat;
+    int64_t stat_n;
+    float* hit;              // the target's logit
+    const int64_t* targets;
+    // d logits into out.C
+    const float* lse;
+    const float* dloss;
+    int64_t vocab, col0;     // size of the vocabulary; its first column in this piece
+};
+
+int tile_m(Tile t);
+int tile_n(Tile t);
+int stat_cols(Tile t);       // columns that one statistics pair covers
+
+// X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_m and tiles_n are filled in here.
+hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream);
+hipError_t launch_nn(Tile t, TileArgs a, hipStream_t stream);
+hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream);
+
+// out = epilogue of the sum over splits of part[s][row][col]
+hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
+                       bool vec, hipStream_t stream);
+
+// d (M, ldd) = dC act'(pre), columns [N, ldd) zero (d may be null); colsum: null or fp32
+// [colsum_rows(M)][N] partial column sums of the unrounded products
+int64_t colsum_rows(int64_t M);
+hipError_t launch_act_bwd(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N, __bf16* d, int64_t ldd,
+                          float* colsum, hipStream_t stream);
+hipError_t launch_colsum_join(const float* colsum, int64_t rows, int64_t N, __bf16* out, hipStream_t stream);
+
+// lse and loss of each row from its statistics
+hipError_t launch_xent_join(const float* stat, int64_t stat_n, const float* hit, const int64_t* targets, int64_t T,
+                            int64_t vocab, float* loss, float* lse, hipStream_t stream);
+
+}  // namespace lm
+}  // namespace ag

@@ -1,0 +1,54 @@
+// lm_nt.hip -- X (M, K) times Y (N, K): the forward products (linear, grouped by expert) and the logits.
+#include "lm_launch.hpp"
+
+namespace ag {
+namespace lm {
+namespace {
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 1) void nt256_kernel(TileArgs a)
+{
+    tile_body<256, 256, 2, 2, 2, false, false, EPI>(a);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 2) void nt128_kernel(TileArgs a)
+{
+    tile_body<128, 128, 2, 2, 2, false, false, EPI>(a);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 1) void nt32_kernel(TileArgs a)
+{
+    tile_body<32, 128, 1, 4, 4, false, false, EPI>(a);
+}
+
+template <int EPI>
+hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
+{
+    switch (t) {
+    case kTile256: return launch_tiles(nt256_kernel<EPI>, 256, 256, 1, a, stream);
+    case kTile128: return launch_tiles(nt128_kernel<EPI>, 128, 128, 2, a, stream);
+    default: return launch_tiles(nt32_kernel<EPI>, 32, 128, 1, a, stream);
+    }
+}
+
+}  // namespace
+
+int tile_m(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 32; }
+int tile_n(Tile t) { return t == kTile256 ? 256 : 128; }
+int stat_cols(Tile t) { return t == kTile256 ? 128 : t == kTile128 ? 64 : 32; }
+
+hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream)
+{
+    switch (epi) {
+    case kEpiStat:
+        a.stat_n = (a.N + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
+        return launch<kEpiStat>(t, a, stream);
+    case kEpiGrad: return launch<kEpiGrad>(t, a, stream);
+    default: return launch<kEpiLinear>(t, a, stream);
+    }
+}
+
+}  // namespace lm
+}  // namespace ag

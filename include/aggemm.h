@@ -197,6 +197,88 @@ int ag_gemm_noalloc(const void *const *shards, int32_t N, int64_t M, int64_t K, 
                     int64_t Nc, void *C, int64_t comm_block_rows, void *a_out, int32_t local_rank,
                     void *stream);
 
+/* ------------------------------------------------------------------ language-model operators
+ *
+ * The products of a language model's block and head around the gathered A, with what follows them
+ * fused in, and their gradients.  All matrices are bf16, every sum and softmax statistic fp32, outputs
+ * rounded once (nearest even).  The conventions above hold, with two additions:
+ *   - They keep nothing in the library.  A call that needs scratch memory takes `work`, a 16-byte
+ *     aligned device buffer of at least `work_bytes`, what the matching ..._workspace() returns for
+ *     the same extents (0: `work` may be NULL).  Calls on different streams with different workspaces
+ *     are independent, and a call may be captured into a graph.
+ *   - Extents of 0 are valid everywhere but V: what remains of the formula is written (K == 0: the
+ *     products are zero; a gradient summed over no rows is zero).
+ * K % 8 == 0; matrices and bias 16-byte aligned.  K, Nc or V > 2^21 or rows > 2^30 return
+ * AG_EUNSUPPORTED. */
+
+/* Activations. */
+#define AG_ACT_NONE       0
+#define AG_ACT_RELU       1
+#define AG_ACT_SILU       2   /* x / (1 + exp(-x)) */
+#define AG_ACT_GELU       3   /* x (1 + erf(x / sqrt 2)) / 2 */
+#define AG_ACT_GELU_TANH  4   /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+
+/*
+ * C = act(A B^T + bias) + residual.
+ *   A (M, K), B (Nc, K), C (M, Nc); bias (Nc) or NULL; residual (M, Nc) or NULL; act AG_ACT_*;
+ *   pre: NULL, or (M, Nc) that receives A B^T + bias in bf16 for gemm_bias_act_bwd.  (C itself uses
+ *   the unrounded sums.)  residual may be the same buffer as C.
+ */
+int64_t gemm_bias_act_workspace(int64_t M, int64_t Nc, int64_t K);
+int gemm_bias_act(const void *A, const void *B, const void *bias, const void *residual, int64_t M,
+                  int64_t Nc, int64_t K, int32_t act, void *C, void *pre, void *work,
+                  int64_t work_bytes, void *stream);
+
+/*
+ * Its gradients, with d = dC * act'(pre):  dA = d B (M, K), dB = d^T A (Nc, K), dbias = column sums of
+ * d (Nc).  The residual's gradient is dC itself.  Each output may be NULL: it is then not computed (and
+ * A, which only dB needs, or B, which only dA needs, may be NULL too).  pre: as gemm_bias_act stored
+ * it; NULL with AG_ACT_NONE.  The products take d rounded to bf16; dbias sums it unrounded.  relu'(0) = 0.
+ */
+int64_t gemm_bias_act_bwd_workspace(int64_t M, int64_t Nc, int64_t K, int32_t act);
+int gemm_bias_act_bwd(const void *dC, const void *A, const void *B, const void *pre, int64_t M,
+                      int64_t Nc, int64_t K, int32_t act, void *dA, void *dB, void *dbias, void *work,
+                      int64_t work_bytes, void *stream);
+
+/*
+ * Products grouped by expert: rows [ends[e-1], ends[e]) of C are the same rows of A times B[e]^T
+ * (ends[-1] = 0); rows at or past ends[E-1] of C are zero.
+ *   A (M, K), B (E, Nc, K), C (M, Nc); ends: E int32 on the DEVICE, the running sums of the experts'
+ *   row counts.  The library never reads them on the host, so a router's output needs no
+ *   synchronisation; an entry below its predecessor or beyond M counts as that bound.
+ * Nc % 8 == 0; E > 1024 returns AG_EUNSUPPORTED.
+ */
+int gemm_grouped(const void *A, const void *B, const int32_t *ends, int32_t E, int64_t M, int64_t Nc,
+                 int64_t K, void *C, void *stream);
+
+/* Its gradients: rows of expert e: dA = dC B[e]; dB[e] = dC_e^T A_e over the expert's rows (zero for an
+ * expert without rows).  Rows of dA past the last end are zero.  dA or dB may be NULL. */
+int gemm_grouped_bwd(const void *dC, const void *A, const void *B, const int32_t *ends, int32_t E,
+                     int64_t M, int64_t Nc, int64_t K, void *dA, void *dB, void *stream);
+
+/*
+ * Softmax cross entropy of the logits A B^T, which are never stored:
+ *   lse[t] = log sum_v exp(a_t . b_v),  loss[t] = lse[t] - a_t . b_y,  y = targets[t].
+ *   A (T, K), B (V, K), targets (T) int64 on the device, loss and lse (T) fp32.
+ * A target outside [0, V) (such as -100) marks a row without one: its loss is 0 and it contributes no
+ * gradient.  V >= 1.
+ */
+int64_t gemm_xent_workspace(int64_t T, int64_t V, int64_t K);
+int gemm_xent(const void *A, const void *B, const int64_t *targets, int64_t T, int64_t V, int64_t K,
+              float *loss, float *lse, void *work, int64_t work_bytes, void *stream);
+
+/*
+ * Its gradients for dloss (T) fp32 and the lse that gemm_xent wrote: with
+ * D[t,v] = dloss[t] (exp(a_t . b_v - lse[t]) - [v = y]),  dA = D B (T, K),  dB = D^T A (V, K).
+ * D is formed a piece of the vocabulary at a time, in bf16; gemm_xent_bwd_workspace() asks for pieces of
+ * up to 512 MiB, and a smaller workspace, down to 256 columns a piece, only makes more of them.  dA or
+ * dB may be NULL.
+ */
+int64_t gemm_xent_bwd_workspace(int64_t T, int64_t V, int64_t K);
+int gemm_xent_bwd(const float *dloss, const void *A, const void *B, const int64_t *targets,
+                  const float *lse, int64_t T, int64_t V, int64_t K, void *dA, void *dB, void *work,
+                  int64_t work_bytes, void *stream);
+
 /* Waits for `stream`, then reads and clears the current device's status words (the workspace's,
  * then ag_gemm_noalloc's).  Returns AG_OK, or AG_ETIMEOUT with info = {code, chunk, tile, epoch}
  * for the first flag wait that gave up since the last ag_check (epoch: the failing call's flag
