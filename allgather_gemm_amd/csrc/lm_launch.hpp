@@ -27,9 +27,7 @@ hipError_t launch_tiles(Kernel kernel, int bm, int bn, int per_cu, TileArgs& a, 
         tiles *= a.E;
     if (tiles <= 0)
         return hipSuccess;
-    int64_t grid = tiles;
-    if (a.group == kGroupRows || grid > (1 << 30))
-        grid = std::min<int64_t>(tiles, (int64_t)cus * per_cu);
+    const int64_t grid = std::min<int64_t>(tiles, (int64_t)cus * per_cu);
     kernel<<<dim3((unsigned)grid), dim3(NT), 0, stream>>>(a);
     return hipGetLastError();
 }

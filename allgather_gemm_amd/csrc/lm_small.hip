@@ -28,8 +28,14 @@ __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits,
     }
     float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
     const int n = (int)min((int64_t)8, N - col);
-    if (n > 0)
-        linear8(out, row, col, n, vec, x);
+    if (n <= 0)
+        return;
+    float b[8] = {}, r[8] = {};
+    if (out.bias)
+        load8(out.bias + col, n, vec, b);
+    if (out.residual)
+        load8(out.residual + row * out.ldc + col, n, vec, r);
+    linear8(out, row, col, n, vec, x, b, r);
 }
 
 constexpr int COLS = 256;      // columns of a workgroup of act_bwd_kernel: 32 lanes of 8
@@ -50,9 +56,7 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
         if (act != kActNone) {
             float z[8];
             load8(pre + row * N + col, n, vec, z);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = e < n ? x[e] * act_slope(z[e], act) : 0.0f;
+            act_slope8(x, z, act);
         }
         if (d && col < ldd) {
             bf16x8 o;

@@ -31,6 +31,16 @@ __device__ __forceinline__ uint32_t swz(uint32_t row) { return (row & 7u) ^ ((ro
 
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
+// Workgroup barrier of the K loop: this wave's LDS reads are done, its loads into LDS are not waited for
+// (__syncthreads() would wait for every one in flight; the loop waits for those it needs itself).
+__device__ __forceinline__ void stage_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // One operand's side of the tile: R rows of the output's extent, T: column operand.
 template <int R, bool T>
 struct Side {
@@ -46,47 +56,67 @@ struct Side {
     }
 
     uint32_t voff;         // this thread's byte offset inside a load
+    int32_t c16;           // row operand: bytes of this thread's chunk into the K step
     uint32_t op_stride;    // bytes between two loads' first rows
-    int32_t klim;          // row operand: this thread's chunk lies inside the row while 128 kb < klim
+    const char* at;        // where the next step's buffer starts
+    int64_t step;          // bytes from one step's buffer to the next
+    int32_t left;          // row operand: bytes of the row from `at` on that are still to be read;
+                           // column operand: rows still to be read
+    int32_t bytes;         // row operand: bytes from `at` to the tile's last; column operand: those of a
+                           // whole step
+    int32_t col2;          // column operand: bytes of the tile's first column into its row
+    int32_t row_bytes;
 
-    __device__ __forceinline__ void init(int tid, int64_t ld, int64_t K)
+    __device__ __forceinline__ void init(int tid, int64_t ld)
     {
-        const uint32_t ldb = (uint32_t)(ld * 2);
+        row_bytes = (int32_t)(ld * 2);
         if (T) {
             const uint32_t k = (uint32_t)(tid * 16) / RB, p = ((uint32_t)(tid * 16) % RB) / 16;
             const uint32_t c = ((p >> 2) ^ ksw(k)) * 4 + (p & 3);
-            voff = k * ldb + c * 16;
-            klim = 0;
+            voff = k * row_bytes + c * 16;
+            c16 = 0;
+            step = (int64_t)BK * row_bytes;
         } else {
             const uint32_t r = tid >> 3, c = (tid & 7) ^ swz(r);
-            voff = r * ldb + c * 16;
-            klim = (int32_t)(K * 2) - (int32_t)c * 16;
+            voff = r * row_bytes + c * 16;
+            c16 = (int32_t)c * 16;
+            step = BK * 2;
         }
-        op_stride = RPO * ldb;
+        op_stride = RPO * row_bytes;
     }
 
-    // Buffer over what step kb of this tile may read: base = first element of the tile at k = 0
-    // (row operand: its first row; column operand: row k = 0 at the tile's first column), `rows` the
-    // valid tile rows (row operand), K the reduction length, col0 the tile's first column.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const __bf16* base, int64_t ld, int64_t rows,
-                                                                  int64_t K, int64_t col0, int64_t kb)
+    // A tile's K steps [kb0, ...) up to reduction index k_end: base = first element of the tile at k = 0
+    // (row operand: its first row; column operand: row k = 0 at the tile's first column, col0), rows =
+    // the valid tile rows (row operand), K = the reduction length.
+    __device__ __forceinline__ void start(const __bf16* base, int64_t rows, int64_t K, int64_t col0, int64_t kb0,
+                                          int64_t k_end)
     {
+        at = reinterpret_cast<const char*>(base) + kb0 * step;
+        const int32_t k_left = (int32_t)(max((int64_t)0, k_end - kb0 * BK));
         if (T) {
-            const int64_t left = K - kb * BK;
-            const int64_t n = left <= 0 ? 0 : (left < BK ? left : (int64_t)BK) * ld * 2 - col0 * 2;
-            return make_rsrc(reinterpret_cast<const char*>(base) + (left <= 0 ? 0 : kb * BK * ld * 2), (uint32_t)n);
+            left = k_left;
+            col2 = (int32_t)(col0 * 2);
+        } else {
+            left = k_left * 2;
+            bytes = (int32_t)(max((int64_t)0, ((rows - 1) * row_bytes + K * 2) - kb0 * BK * 2));
         }
-        const int64_t kbyte = kb * 128;
-        const int64_t n = K * 2 <= kbyte ? 0 : ((rows - 1) * ld + K) * 2 - kbyte;
-        return make_rsrc(reinterpret_cast<const char*>(base) + (n <= 0 ? 0 : kbyte), (uint32_t)(n <= 0 ? 0 : n));
     }
 
-    // This thread's offset in step kb; past the row's end it starts beyond every buffer size.
-    __device__ __forceinline__ uint32_t offset(int64_t kb) const
+    // The buffer over what the next step may read, and this thread's offset in it (past the row's end it
+    // lies beyond every buffer's size, which stays under 2^31).  Steps past the last read nothing.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const
     {
         if (T)
-            return voff;
-        return (int32_t)(kb * 128) < klim ? voff : 0x80000000u;
+            return make_rsrc(at, (uint32_t)max(0, min(left, BK) * row_bytes - col2));
+        return make_rsrc(at, (uint32_t)max(0, bytes));
+    }
+    __device__ __forceinline__ uint32_t offset() const { return T || c16 < left ? voff : 0x80000000u; }
+    __device__ __forceinline__ void advance()
+    {
+        at += step;
+        left -= T ? BK : BK * 2;
+        if (!T)
+            bytes -= BK * 2;
     }
 
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* stage, uint32_t wave_off, uint32_t off,
@@ -140,51 +170,120 @@ struct Frag {
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)); }
 
-__device__ __forceinline__ float act_value(float x, int act)
+// Phi(x), the normal distribution function, and phi'(x) sqrt(2 pi) = exp(-x^2 / 2), which it takes: erfc by
+// Abramowitz & Stegun 7.1.26, off by at most 1.5e-7, as near as 0.5 (1 + erf) gets in fp32.
+__device__ __forceinline__ float normal_cdf(float x, float* e)
+{
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+    *e = fast_exp(-0.5f * x * x);
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    const float q = 0.5f * t * p * *e;                 // Phi(-|x|)
+    return x >= 0.0f ? 1.0f - q : q;
+}
+
+constexpr float kTanh0 = 1.5957691216057308f;          // 2 sqrt(2 / pi): 0.5 (1 + tanh u) = sigmoid(2u)
+
+// The activation is chosen once for eight values, not for each.
+__device__ __forceinline__ void act_value8(float* x, int act)
 {
     switch (act) {
-    case kActRelu: return x > 0.0f ? x : (x != x ? x : 0.0f);
-    case kActSilu: return x * fast_sigmoid(x);
-    case kActGelu: return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-    // 0.5 (1 + tanh u) = sigmoid(2u)
-    case kActGeluTanh: return x * fast_sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x));
-    default: return x;
+    case kActRelu:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = x[e] > 0.0f || x[e] != x[e] ? x[e] : 0.0f;
+        break;
+    case kActSilu:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] *= fast_sigmoid(x[e]);
+        break;
+    case kActGelu:
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float ignored;
+            x[e] *= normal_cdf(x[e], &ignored);
+        }
+        break;
+    case kActGeluTanh:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] *= fast_sigmoid(kTanh0 * (x[e] + 0.044715f * x[e] * x[e] * x[e]));
+        break;
+    default: break;
     }
 }
 
-__device__ __forceinline__ float act_slope(float x, int act)
+__device__ __forceinline__ float silu_slope(float x)
+{
+    const float s = fast_sigmoid(x);
+    return s * (1.0f + x * (1.0f - s));
+}
+
+__device__ __forceinline__ float gelu_slope(float x)
+{
+    float e;
+    const float c = normal_cdf(x, &e);
+    return fmaf(0.3989422804014327f * x, e, c);
+}
+
+__device__ __forceinline__ float gelu_tanh_slope(float x)
+{
+    if (fabsf(x) > 30.0f)              // s is 0 or 1 there; x^2 could overflow and meet its zero
+        return x > 0.0f ? 1.0f : 0.0f;
+    const float s = fast_sigmoid(kTanh0 * (x + 0.044715f * x * x * x));
+    return s + x * s * (1.0f - s) * kTanh0 * (1.0f + 0.134145f * x * x);
+}
+
+// x[e] *= act'(z[e])
+__device__ __forceinline__ void act_slope8(float* x, const float* z, int act)
 {
     switch (act) {
-    case kActRelu: return x > 0.0f ? 1.0f : 0.0f;
-    case kActSilu: {
-        const float s = fast_sigmoid(x);
-        return s * (1.0f + x * (1.0f - s));
-    }
+    case kActRelu:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = z[e] > 0.0f ? x[e] : 0.0f;
+        break;
+    case kActSilu:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] *= silu_slope(z[e]);
+        break;
     case kActGelu:
-        return 0.5f * (1.0f + erff(x * 0.70710678118654752f)) + x * 0.3989422804014327f * fast_exp(-0.5f * x * x);
-    case kActGeluTanh: {
-        if (fabsf(x) > 30.0f)              // s is 0 or 1 there; x^2 could overflow and meet its zero
-            return x > 0.0f ? 1.0f : 0.0f;
-        const float s = fast_sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x));
-        return s + x * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * x * x);
-    }
-    default: return 1.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] *= gelu_slope(z[e]);
+        break;
+    case kActGeluTanh:
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] *= gelu_tanh_slope(z[e]);
+        break;
+    default: break;
     }
 }
 
 // Eight consecutive bf16 of row `row`, columns [col, col + 8) with `n` of them valid.
+__device__ __forceinline__ bf16x8 load8_raw(const __bf16* p, int n, bool vec)
+{
+    bf16x8 v = {};
+    if (vec && n >= 8)
+        return *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            v[e] = p[e];
+    return v;
+}
+
 __device__ __forceinline__ void load8(const __bf16* p, int n, bool vec, float* x)
 {
-    if (vec && n >= 8) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
+    const bf16x8 v = load8_raw(p, n, vec);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = (float)v[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = e < n ? (float)p[e] : 0.0f;
-    }
+    for (int e = 0; e < 8; ++e)
+        x[e] = (float)v[e];
 }
 
 __device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float* x)
@@ -203,12 +302,12 @@ __device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float* 
     }
 }
 
-// act(x + bias) + residual of eight columns, stored; `pre` gets x + bias.
-__device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t col, int n, bool vec, float* x)
+// act(x + bias) + residual of eight columns, stored; `pre` gets x + bias.  b and r: the eight columns of
+// bias and residual, loaded before.
+__device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t col, int n, bool vec, float* x,
+                                        const float* b, const float* r)
 {
     if (o.bias) {
-        float b[8];
-        load8(o.bias + col, n, vec, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             x[e] += b[e];
@@ -216,14 +315,8 @@ __device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t
     const int64_t at = row * o.ldc + col;
     if (o.pre)
         store8(o.pre + at, n, vec, x);
-    if (o.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = act_value(x[e], o.act);
-    }
+    act_value8(x, o.act);
     if (o.residual) {
-        float r[8];
-        load8(o.residual + at, n, vec, r);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             x[e] += r[e];
@@ -281,6 +374,74 @@ __device__ void group_scan(const int32_t* ends, int E, int64_t limit, int bm, in
     barrier_after_lds_write();
 }
 
+// ------------------------------------------------------------------------------ cross entropy
+// Softmax statistics of the columns [col, col + 8) of a row, n of them valid: LPR neighbouring lanes hold
+// the row's part that pair `slot` covers, so the steps below stay inside the row.
+template <int LPR>
+__device__ __forceinline__ void stat8(const TileArgs& a, int64_t mrow, int64_t M, int64_t col, int n, int64_t slot,
+                                      int lane, const float* x)
+{
+    float mx = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n) {
+            mx = fmaxf(mx, x[e]);
+            nan |= x[e] != x[e];
+        }
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1)
+        mx = fmaxf(mx, __shfl_xor(mx, s));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            sum += fast_exp(x[e] - base);
+    if (nan)
+        sum = NAN;
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1)
+        sum += __shfl_xor(sum, s);
+    if (mrow < M) {
+        if ((lane % LPR) == 0) {
+            float* p = a.stat + (mrow * a.stat_n + slot) * 2;
+            p[0] = mx;
+            p[1] = sum;
+        }
+        const int64_t y = a.targets[mrow] - col;
+        if (y >= 0 && y < n) {
+            float hit = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                hit = e == (int)y ? x[e] : hit;
+            a.hit[mrow] = hit;
+        }
+    }
+}
+
+// d logits = dloss (softmax - one at the target), rounded to bf16 for the products that follow (each is a
+// sum of many such terms, and 2^-9 of a term is what the products' other operand is rounded to);
+// padding columns of the buffer are zero.
+__device__ __forceinline__ void grad8(const TileArgs& a, int64_t mrow, int64_t M, int64_t col, int n, const float* x)
+{
+    if (mrow >= M || col >= a.out.ldc)
+        return;
+    const int64_t y = a.targets[mrow];
+    const bool has = y >= 0 && y < a.vocab;
+    const float lse = a.lse[mrow], w = has ? a.dloss[mrow] : 0.0f;
+    const int64_t hit = y - a.col0 - col;
+    bf16x8 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float p = fast_exp(x[e] - lse);
+        if (hit == e)
+            p -= 1.0f;
+        o[e] = (__bf16)(e < n && has ? p * w : 0.0f);
+    }
+    *reinterpret_cast<bf16x8*>(a.out.C + mrow * a.out.ldc + col) = o;
+}
+
 // ---------------------------------------------------------------------------------- the kernel
 // EPI: kEpiLinear, kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
@@ -328,6 +489,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     Frag<BN, TB, FN> fb;
     fa.init(lane, wm);
     fb.init(lane, wn);
+    sa.init(tid, a.lda);
+    sb.init(tid, a.ldb);
     const uint32_t wave_off = wave * 1024;
 
     for (int64_t t = vid; t < num_tiles; t += G) {
@@ -381,11 +544,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             Bb = a.B + (a.group == kGroupK ? k_first * a.ldb : (zero ? 0 : g) * a.strideB) + n0;
         else
             Bb = a.B + (zero ? 0 : g) * a.strideB + n0 * a.ldb;
-        sa.init(tid, a.lda, K);
-        sb.init(tid, a.ldb, K);
         const int64_t nk_all = (K + BK - 1) / BK;
         const int64_t kb0 = min(split * a.split_steps, nk_all);
         const int64_t kb1 = a.splits > 1 ? min(kb0 + a.split_steps, nk_all) : nk_all;
+        const int64_t k_end = min(K, kb1 * BK);
+        sa.start(Ab, a_rows, K, m0, kb0, k_end);
+        sb.start(Bb, b_rows, K, n0, kb0, !TA && TB ? min(k_end, a.k_valid) : k_end);
 
         f32x16 acc[FM][FN];
 #pragma unroll
@@ -401,20 +565,21 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             uint32_t va, vb, lw, sa_, sb_;
             char *la, *lb;
         };
-        // loads of step kb into a stage; past the last step they read nothing but still count
-        auto dma_setup = [&](int64_t kb, char* la, char* lb) {
+        // the next step's loads, into a stage; past the last step they read nothing but still count
+        auto dma_setup = [&](char* la, char* lb) {
             Dma d;
             d.lw = wave_off;
             d.sa_ = sa.op_stride;
             d.sb_ = sb.op_stride;
             asm volatile("" : "+s"(d.lw), "+s"(d.sa_), "+s"(d.sb_));
-            const int64_t Kd = kb < kb1 ? K : 0;
-            d.ra = SA::rsrc(Ab, a.lda, a_rows, Kd, m0, kb);
-            d.rb = SB::rsrc(Bb, a.ldb, b_rows, !TA && TB ? min(Kd, a.k_valid) : Kd, n0, kb);
-            d.va = sa.offset(kb);
-            d.vb = sb.offset(kb);
+            d.ra = sa.rsrc();
+            d.rb = sb.rsrc();
+            d.va = sa.offset();
+            d.vb = sb.offset();
             d.la = la;
             d.lb = lb;
+            sa.advance();
+            sb.advance();
             return d;
         };
         auto dma_op = [&](const Dma& d, int q) {
@@ -423,8 +588,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             else
                 sb.load(d.rb, d.lb, d.lw, d.vb, d.sb_, q - SA::OPS);
         };
-        auto issue_all = [&](int64_t kb, char* la, char* lb) {
-            const Dma d = dma_setup(kb, la, lb);
+        auto issue_all = [&](char* la, char* lb) {
+            const Dma d = dma_setup(la, lb);
 #pragma unroll
             for (int q = 0; q < ND; ++q)
                 dma_op(d, q);
@@ -476,45 +641,45 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             // pair loop always computes twice per iteration
             int64_t kb = kb0;
             if ((kb1 - kb0) & 1) {
-                issue_all(kb, sA1, sB1);
+                issue_all(sA1, sB1);
                 wait_vmcnt0();
-                __syncthreads();
-                compute(sA1, sB1, dma_setup(kb + 1, sA0, sB0));
+                stage_barrier();
+                compute(sA1, sB1, dma_setup(sA0, sB0));
                 ++kb;
             } else if (kb1 > kb0) {
-                issue_all(kb, sA0, sB0);
+                issue_all(sA0, sB0);
             }
             for (; kb < kb1; kb += 2) {
                 wait_vmcnt0();
-                __syncthreads();
-                compute(sA0, sB0, dma_setup(kb + 1, sA1, sB1));
+                stage_barrier();
+                compute(sA0, sB0, dma_setup(sA1, sB1));
                 wait_vmcnt0();
-                __syncthreads();
-                compute(sA1, sB1, dma_setup(kb + 2, sA0, sB0));
+                stage_barrier();
+                compute(sA1, sB1, dma_setup(sA0, sB0));
             }
         } else {
             // four stages: the loads of three steps are in flight while one is computed
-            issue_all(kb0, sA0, sB0);
-            issue_all(kb0 + 1, sA1, sB1);
-            issue_all(kb0 + 2, sA2, sB2);
+            issue_all(sA0, sB0);
+            issue_all(sA1, sB1);
+            issue_all(sA2, sB2);
             for (int64_t kb = kb0; kb < kb1; kb += 4) {
                 wait_vmcnt<2 * ND>();
-                __syncthreads();
-                compute(sA0, sB0, dma_setup(kb + 3, sA3, sB3));
+                stage_barrier();
+                compute(sA0, sB0, dma_setup(sA3, sB3));
                 if (kb + 1 < kb1) {
                     wait_vmcnt<2 * ND>();
-                    __syncthreads();
-                    compute(sA1, sB1, dma_setup(kb + 4, sA0, sB0));
+                    stage_barrier();
+                    compute(sA1, sB1, dma_setup(sA0, sB0));
                 }
                 if (kb + 2 < kb1) {
                     wait_vmcnt<2 * ND>();
-                    __syncthreads();
-                    compute(sA2, sB2, dma_setup(kb + 5, sA1, sB1));
+                    stage_barrier();
+                    compute(sA2, sB2, dma_setup(sA1, sB1));
                 }
                 if (kb + 3 < kb1) {
                     wait_vmcnt<2 * ND>();
-                    __syncthreads();
-                    compute(sA3, sB3, dma_setup(kb + 6, sA2, sB2));
+                    stage_barrier();
+                    compute(sA3, sB3, dma_setup(sA2, sB2));
                 }
             }
         }
@@ -528,9 +693,31 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         char* slab = 4 * SLAB <= SB::BYTES ? sB0 + wave * SLAB : (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
         constexpr uint32_t SW = WNC / 4 - 1;           // 16-byte units of a slab row, minus one
         constexpr int LPR = WNC / 8;                   // lanes per slab row on the way back
+        constexpr int ITS = WNC / 16;                  // read-backs of a slab
         const uint32_t fr = lane & 31, fh = lane >> 5;
+        // a lane's eight columns are the same in every row it reads back
+        const uint32_t c8 = (lane % LPR) * 8, r_lane = lane / LPR;
+        const int64_t col = n0 + wn * WNC + c8;
+        const int n = (int)max((int64_t)0, min((int64_t)8, a.N - col));
+        __bf16* const C = a.out.C + (EPI == kEpiLinear && a.group == kGroupK ? g * a.M * a.out.ldc : 0);
+        const bool residual = a.out.residual && !a.part;
+        const bool between = !a.part && (a.out.bias || a.out.pre || a.out.act != kActNone);
+        float bias[8] = {};
+        if (EPI == kEpiLinear && between && a.out.bias)
+            load8(a.out.bias + col, n, a.vec, bias);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
+            const int64_t mrow0 = m0 + (wm * FM + i) * 32 + r_lane;       // this lane's first row of the slab
+            const int64_t at0 = (grow0 + mrow0) * a.out.ldc + col;
+            constexpr int RSTEP = 64 / LPR;                                // rows between its read-backs
+            // the slab's residual is on its way while the slab is written
+            bf16x8 res[ITS] = {};
+            if (EPI == kEpiLinear && residual && a.vec) {
+#pragma unroll
+                for (int it = 0; it < ITS; ++it)
+                    if (mrow0 + it * RSTEP < M && n >= 8)
+                        res[it] = *reinterpret_cast<const bf16x8*>(a.out.residual + at0 + it * RSTEP * a.out.ldc);
+            }
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -542,101 +729,77 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
                 }
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
             __builtin_amdgcn_wave_barrier();
+            auto unit = [&](int it, int half) {   // four of this lane's eight columns in its row it
+                const uint32_t r = it * RSTEP + r_lane;
+                return reinterpret_cast<f32x4*>(slab + r * (WNC * 4) + (((c8 + 4 * half) * 4) ^ ((r & SW) << 4)));
+            };
+            if constexpr (EPI == kEpiLinear) {
+                if (between) {
+                    // bias, pre and the activation in a loop of their own, through the slab: unrolled into
+                    // the stores below, the activations would be there once for each row of the block
+#pragma unroll 2
+                    for (int it = 0; it < ITS; ++it) {
+                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                        float x[8] = {x0[0] + bias[0], x0[1] + bias[1], x0[2] + bias[2], x0[3] + bias[3],
+                                      x1[0] + bias[4], x1[1] + bias[5], x1[2] + bias[6], x1[3] + bias[7]};
+                        if (a.out.pre && mrow0 + it * RSTEP < M && n > 0)
+                            store8(a.out.pre + at0 + it * RSTEP * a.out.ldc, n, a.vec, x);
+                        act_value8(x, a.out.act);
+                        *unit(it, 0) = f32x4{x[0], x[1], x[2], x[3]};
+                        *unit(it, 1) = f32x4{x[4], x[5], x[6], x[7]};
+                    }
+                }
+                if (a.part) {
 #pragma unroll
-            for (int it = 0; it < WNC / 16; ++it) {
-                const uint32_t pidx = it * 64 + lane;
-                const uint32_t r = pidx / LPR, c8 = (pidx % LPR) * 8;
-                const f32x4 x0 = *reinterpret_cast<const f32x4*>(slab + r * (WNC * 4) + ((c8 * 4) ^ ((r & SW) << 4)));
-                const f32x4 x1 =
-                    *reinterpret_cast<const f32x4*>(slab + r * (WNC * 4) + (((c8 + 4) * 4) ^ ((r & SW) << 4)));
-                float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-                const int64_t mrow = m0 + (wm * FM + i) * 32 + r, col = n0 + wn * WNC + c8;
-                const int n = (int)max((int64_t)0, min((int64_t)8, a.N - col));
-                const bool in = mrow < M && n > 0;
-                if constexpr (EPI == kEpiLinear) {
-                    if (in) {
-                        const int64_t row = grow0 + mrow;
-                        if (a.part) {
-                            float* p = a.part + (split * a.M + row) * a.ldp + col;   // ldp % 8 == 0: whole vectors
-                            f32x4* pv = reinterpret_cast<f32x4*>(p);
+                    for (int it = 0; it < ITS; ++it) {
+                        const int64_t mrow = mrow0 + it * RSTEP;
+                        f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                        if (mrow < M && n > 0) {       // ldp % 8 == 0: whole vectors
+                            f32x4* pv = reinterpret_cast<f32x4*>(a.part + (split * a.M + mrow) * a.ldp + col);
                             if (a.accumulate) {
-                                const f32x4 o0 = pv[0], o1 = pv[1];
-                                pv[0] = f32x4{x[0], x[1], x[2], x[3]} + o0;
-                                pv[1] = f32x4{x[4], x[5], x[6], x[7]} + o1;
-                            } else {
-                                pv[0] = f32x4{x[0], x[1], x[2], x[3]};
-                                pv[1] = f32x4{x[4], x[5], x[6], x[7]};
+                                x0 += pv[0];
+                                x1 += pv[1];
                             }
-                        } else {
-                            LinearOut o = a.out;
-                            if (a.group == kGroupK)
-                                o.C += g * a.M * a.out.ldc;
-                            linear8(o, row, col, n, a.vec, x);
+                            pv[0] = x0;
+                            pv[1] = x1;
                         }
                     }
-                } else if constexpr (EPI == kEpiStat) {
-                    // maximum and sum of exponentials of this row's WNC columns: LPR neighbouring lanes
-                    // hold them, so the steps below stay inside the row
-                    float mx = -INFINITY;
+                } else if (a.vec) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < n)
-                            mx = fmaxf(mx, x[e]);
-                    bool nan = false;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        nan |= e < n && x[e] != x[e];
-#pragma unroll
-                    for (int s = 1; s < LPR; s <<= 1)
-                        mx = fmaxf(mx, __shfl_xor(mx, s));
-                    const float base = mx == -INFINITY ? 0.0f : mx;
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < n)
-                            sum += fast_exp(x[e] - base);
-                    if (nan)
-                        sum = NAN;
-#pragma unroll
-                    for (int s = 1; s < LPR; s <<= 1)
-                        sum += __shfl_xor(sum, s);
-                    if (mrow < M) {
-                        if ((lane % LPR) == 0) {
-                            float* p = a.stat + (mrow * a.stat_n + tn * WN + wn) * 2;
-                            p[0] = mx;
-                            p[1] = sum;
-                        }
-                        const int64_t y = a.targets[mrow] - col;
-                        if (y >= 0 && y < n) {
-                            float hit = 0.0f;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                hit = e == (int)y ? x[e] : hit;
-                            a.hit[mrow] = hit;
-                        }
-                    }
-                } else {
-                    // d logits = dloss (softmax - one at the target), rounded to bf16 for the products that
-                    // follow (each is a sum of many such terms; 2^-9 of each term is their input's own
-                    // precision); padding columns of the buffer are zero
-                    if (mrow < M && col < a.out.ldc) {
-                        const int64_t y = a.targets[mrow];
-                        const bool has = y >= 0 && y < a.vocab;
-                        const float lse = a.lse[mrow], w = has ? a.dloss[mrow] : 0.0f;
-                        const int64_t hit = y - a.col0 - col;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float p = fast_exp(x[e] - lse);
-                            if (hit == e)
-                                p -= 1.0f;
-                            x[e] = (e < n && has) ? p * w : 0.0f;
-                        }
+                    for (int it = 0; it < ITS; ++it) {
+                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
                         bf16x8 o;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            o[e] = (__bf16)x[e];
-                        *reinterpret_cast<bf16x8*>(a.out.C + mrow * a.out.ldc + col) = o;
+                            o[e] = (__bf16)((e < 4 ? x0[e & 3] : x1[e & 3]) + (residual ? (float)res[it][e] : 0.0f));
+                        // C is not read here again: its stores pass the tiles' lines in L2 by
+                        if (mrow0 + it * RSTEP < M && n >= 8)
+                            __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(C + at0 + it * RSTEP * a.out.ldc));
                     }
+                } else {
+#pragma unroll 1
+                    for (int it = 0; it < ITS; ++it) {
+                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                        if (mrow0 + it * RSTEP < M)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (e < n) {
+                                    const int64_t at = at0 + it * RSTEP * a.out.ldc + e;
+                                    const float x = e < 4 ? x0[e & 3] : x1[e & 3];
+                                    C[at] = (__bf16)(residual ? x + (float)a.out.residual[at] : x);
+                                }
+                    }
+                }
+            } else {
+#pragma unroll 2
+                for (int it = 0; it < ITS; ++it) {
+                    const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                    float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+                    const int64_t mrow = mrow0 + it * RSTEP;
+                    if constexpr (EPI == kEpiStat)
+                        stat8<LPR>(a, mrow, M, col, n, tn * WN + wn, lane, x);
+                    else
+                        grad8(a, mrow, M, col, n, x);
                 }
             }
             __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
