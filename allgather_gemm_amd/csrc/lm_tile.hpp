@@ -594,11 +594,35 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             for (int q = 0; q < ND; ++q)
                 dma_op(d, q);
         };
-        // One K step: four substeps of NM MFMAs.  The next stage's loads go out spread over the first
-        // two substeps, the next substep's fragments are read in between, so neither queue backs up
-        // into the matrix instructions.
-        auto compute = [&](const char* la, const char* lb, const Dma& d) {
-            bf16x8 af[2][FM], bf[2][FN];
+        // MFMAs of one substep out of (bf, af), with what is to be issued between them: the next
+        // substep's fragment reads into (nbf, naf), one after each of the first MFMAs, and loads
+        // [q0, q1) spread over all of them, so neither queue backs up into the matrix instructions.
+        bf16x8 af[2][FM], bf[2][FN];
+        auto block = [&](int set, const char* la, const char* lb, int next, const Dma& d, int q0, int q1) {
+            const int other = set ^ 1;
+#pragma unroll
+            for (int gi = 0; gi < NM; ++gi) {
+                const int i = gi / FN, j = gi % FN;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[set][j], af[set][i], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                constexpr int NR = FM + FN;
+                constexpr int RS = NM >= NR ? NR : NM;            // MFMAs that a read follows
+                if (next >= 0 && gi < RS) {
+#pragma unroll
+                    for (int r = gi * NR / RS; r < (gi + 1) * NR / RS; ++r) {
+                        if (r < FN)
+                            bf[other][r] = fb.read(lb, next, r);
+                        else
+                            af[other][r - FN] = fa.read(la, next, r - FN);
+                    }
+                }
+#pragma unroll
+                for (int q = q0 + (q1 - q0) * gi / NM; q < q0 + (q1 - q0) * (gi + 1) / NM; ++q)
+                    dma_op(d, q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto first_frags = [&](const char* la, const char* lb) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 bf[0][j] = fb.read(lb, 0, j);
@@ -606,59 +630,57 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             for (int i = 0; i < FM; ++i)
                 af[0][i] = fa.read(la, 0, i);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int cur = kk & 1, nxt = cur ^ 1;
-#pragma unroll
-                for (int gidx = 0; gidx < NM; ++gidx) {
-                    const int i = gidx / FN, j = gidx % FN;
-                    acc[i][j] =
-                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[cur][j], af[cur][i], acc[i][j], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (kk < 2) {
-                        const int s0 = kk * NM + gidx;
-#pragma unroll
-                        for (int q = s0 * ND / (2 * NM); q < (s0 + 1) * ND / (2 * NM); ++q)
-                            dma_op(d, q);
-                    }
-                    if (kk < 3) {
-                        constexpr int NR = FM + FN;
-#pragma unroll
-                        for (int r = (gidx * NR + NM - 1) / NM; r < ((gidx + 1) * NR + NM - 1) / NM; ++r) {
-                            if (r < FN)
-                                bf[nxt][r] = fb.read(lb, kk + 1, r);
-                            else
-                                af[nxt][r - FN] = fa.read(la, kk + 1, r - FN);
-                        }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
         };
 
         if constexpr (S == 2) {
-            // double buffer; with an odd number of steps the first runs alone out of stage 1, so the
-            // pair loop always computes twice per iteration
+            // Double buffer.  A step out of stage c is four substeps; its barrier stands before the last
+            // one: there every wave has read all of stage c's fragments, and the other stage's loads,
+            // issued around the step's start, have landed.  The last substep's MFMAs then cover the
+            // first fragment reads of the next step and the first half of the loads that refill stage c.
+            Dma d;
+            auto step = [&](char* ca, char* cb, char* na, char* nb) {
+                block(0, ca, cb, 1, d, ND / 2, ND);
+                block(1, ca, cb, 2, d, 0, 0);
+                block(0, ca, cb, 3, d, 0, 0);
+                wait_vmcnt0();
+                stage_barrier();
+                d = dma_setup(ca, cb);
+                block(1, na, nb, 0, d, 0, ND / 2);
+            };
+            // the start of a tile: its first step into one stage, half of its second into the other
+            auto start = [&](char* ca, char* cb, char* na, char* nb) {
+                issue_all(ca, cb);
+                wait_vmcnt0();
+                stage_barrier();
+                d = dma_setup(na, nb);
+#pragma unroll
+                for (int q = 0; q < ND / 2; ++q)
+                    dma_op(d, q);
+                first_frags(ca, cb);
+            };
+            // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
+            // computes twice per iteration
             int64_t kb = kb0;
             if ((kb1 - kb0) & 1) {
-                issue_all(sA1, sB1);
-                wait_vmcnt0();
-                stage_barrier();
-                compute(sA1, sB1, dma_setup(sA0, sB0));
+                start(sA1, sB1, sA0, sB0);
+                step(sA1, sB1, sA0, sB0);
                 ++kb;
             } else if (kb1 > kb0) {
-                issue_all(sA0, sB0);
+                start(sA0, sB0, sA1, sB1);
             }
             for (; kb < kb1; kb += 2) {
-                wait_vmcnt0();
-                stage_barrier();
-                compute(sA0, sB0, dma_setup(sA1, sB1));
-                wait_vmcnt0();
-                stage_barrier();
-                compute(sA1, sB1, dma_setup(sA0, sB0));
+                step(sA0, sB0, sA1, sB1);
+                step(sA1, sB1, sA0, sB0);
             }
         } else {
             // four stages: the loads of three steps are in flight while one is computed
+            auto compute = [&](const char* la, const char* lb, const Dma& d) {
+                first_frags(la, lb);
+                block(0, la, lb, 1, d, 0, ND / 2);
+                block(1, la, lb, 2, d, ND / 2, ND);
+                block(0, la, lb, 3, d, 0, 0);
+                block(1, la, lb, -1, d, 0, 0);
+            };
             issue_all(sA0, sB0);
             issue_all(sA1, sB1);
             issue_all(sA2, sB2);
