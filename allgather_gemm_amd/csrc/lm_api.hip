@@ -120,9 +120,20 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     return w;
 }
 
-Tile xent_tile(int64_t T) { return T <= 32 ? kTile32 : T <= 128 ? kTile128 : kTile256; }
+Tile xent_tile(int64_t T) { return T <= 128 ? kTile128 : kTile256; }
 
-int64_t stat_pairs(Tile t, int64_t V) { return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t)); }
+int64_t stat_pairs(int64_t T, int64_t V)
+{
+    if (T <= kRowsMost)
+        return (V + rows_cols(V, T) - 1) / rows_cols(V, T);
+    const Tile t = xent_tile(T);
+    return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
+}
+
+hipError_t launch_logits(Epi epi, const TileArgs& a, hipStream_t s)
+{
+    return a.M <= kRowsMost ? launch_rows(epi, a.M, a, s) : launch_nt(xent_tile(a.M), epi, a, s);
+}
 
 struct XentBwd {
     int64_t piece;           // columns of the vocabulary at a time, a multiple of 256
@@ -175,7 +186,7 @@ extern "C" int64_t gemm_bias_act_workspace(int64_t M, int64_t Nc, int64_t K)
 {
     if (!shapes_ok(M, Nc, K) || too_large(M, Nc, K))
         return 0;
-    return plan_product(M, Nc, K, true).part_bytes(M, Nc);
+    return M <= kRowsMost ? 0 : plan_product(M, Nc, K, false).part_bytes(M, Nc);
 }
 
 extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, int64_t M, int64_t Nc,
@@ -189,15 +200,18 @@ extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, con
         return AG_EINVAL;
     if (too_large(M, Nc, K))
         return AG_EUNSUPPORTED;
-    const Plan p = plan_product(M, Nc, K, true);
-    if (work_bytes < p.part_bytes(M, Nc) || bad(work, p.part_bytes(M, Nc)))
+    const int64_t need = gemm_bias_act_workspace(M, Nc, K);
+    if (work_bytes < need || bad(work, need))
         return AG_EINVAL;
     TileArgs a = product(A, K, B, K, M, Nc, K, C, Nc);
     a.out.bias = static_cast<const __bf16*>(bias);
     a.out.residual = static_cast<const __bf16*>(residual);
     a.out.pre = static_cast<__bf16*>(pre);
     a.out.act = act;
-    LM_HIP(run_product(nt_linear, p, a, work, static_cast<hipStream_t>(stream)), "launch gemm_bias_act");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    LM_HIP(M <= kRowsMost ? launch_rows(kEpiLinear, M, a, s)
+                          : run_product(nt_linear, plan_product(M, Nc, K, false), a, work, s),
+           "launch gemm_bias_act");
     return AG_OK;
 }
 
@@ -274,7 +288,9 @@ extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, i
     a.E = E;
     a.group = kGroupRows;
     a.strideB = Nc * K;
-    LM_HIP(launch_nt(group_tile(M, E), kEpiLinear, a, static_cast<hipStream_t>(stream)), "launch gemm_grouped");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, E), kEpiLinear, a, s),
+           "launch gemm_grouped");
     return AG_OK;
 }
 
@@ -312,7 +328,7 @@ extern "C" int64_t gemm_xent_workspace(int64_t T, int64_t V, int64_t K)
 {
     if (!xent_shapes_ok(T, V, K) || too_large(T, V, K))
         return 0;
-    return region(T * stat_pairs(xent_tile(T), V) * 8) + region(T * 4);
+    return region(T * stat_pairs(T, V) * 8) + region(T * 4);
 }
 
 extern "C" int gemm_xent(const void* A, const void* B, const int64_t* targets, int64_t T, int64_t V, int64_t K, float* loss,
@@ -329,13 +345,12 @@ extern "C" int gemm_xent(const void* A, const void* B, const int64_t* targets, i
     if (work_bytes < gemm_xent_workspace(T, V, K))
         return AG_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Tile t = xent_tile(T);
     TileArgs a = product(A, K, B, K, T, V, K, nullptr, 0);
-    a.stat_n = stat_pairs(t, V);
+    a.stat_n = stat_pairs(T, V);
     a.stat = static_cast<float*>(work);
     a.hit = reinterpret_cast<float*>(static_cast<char*>(work) + region(T * a.stat_n * 8));
     a.targets = targets;
-    LM_HIP(launch_nt(t, kEpiStat, a, s), "launch gemm_xent");
+    LM_HIP(launch_logits(kEpiStat, a, s), "launch gemm_xent");
     LM_HIP(launch_xent_join(a.stat, a.stat_n, a.hit, targets, T, V, loss, lse, s), "launch xent_join");
     return AG_OK;
 }
@@ -376,7 +391,7 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         a.dloss = dloss;
         a.vocab = V;
         a.col0 = v0;
-        LM_HIP(launch_nt(xent_tile(T), kEpiGrad, a, s), "launch d logits");
+        LM_HIP(launch_logits(kEpiGrad, a, s), "launch d logits");
         if (dA) {
             a = product(ws, ldd, Bp, K, T, K, up(n, 8), dA, K);
             a.k_valid = n;

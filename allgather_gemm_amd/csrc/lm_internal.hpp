@@ -10,6 +10,7 @@ namespace ag {
 namespace lm {
 
 constexpr int kMaxGroups = 1024;
+constexpr int kRowsMost = 64;        // rows of X that the few-rows kernel takes at a time
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Group { kGroupNone = 0, kGroupRows = 1, kGroupK = 2 };
@@ -63,6 +64,9 @@ int stat_cols(Tile t);       // columns that one statistics pair covers
 
 // X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_m and tiles_n are filled in here.
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream);
+// X (M, K) Y (N, K) for few rows (a.M, or a group's, about `rows`); out.part is not used.
+int rows_cols(int64_t N, int64_t rows);     // columns that one of its statistics pairs covers
+hipError_t launch_rows(Epi epi, int64_t rows, TileArgs a, hipStream_t stream);
 hipError_t launch_nn(Tile t, TileArgs a, hipStream_t stream);
 hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream);
 

@@ -18,26 +18,18 @@ __global__ __launch_bounds__(NT, 2) void nt128_kernel(TileArgs a)
 }
 
 template <int EPI>
-__global__ __launch_bounds__(NT, 1) void nt32_kernel(TileArgs a)
-{
-    tile_body<32, 128, 1, 4, 4, false, false, EPI>(a);
-}
-
-template <int EPI>
 hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 {
-    switch (t) {
-    case kTile256: return launch_tiles(nt256_kernel<EPI>, 256, 256, 1, a, stream);
-    case kTile128: return launch_tiles(nt128_kernel<EPI>, 128, 128, 2, a, stream);
-    default: return launch_tiles(nt32_kernel<EPI>, 32, 128, 1, a, stream);
-    }
+    if (t == kTile256)
+        return launch_tiles(nt256_kernel<EPI>, 256, 256, 1, a, stream);
+    return launch_tiles(nt128_kernel<EPI>, 128, 128, 2, a, stream);
 }
 
 }  // namespace
 
 int tile_m(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 32; }
 int tile_n(Tile t) { return t == kTile256 ? 256 : 128; }
-int stat_cols(Tile t) { return t == kTile256 ? 128 : t == kTile128 ? 64 : 32; }
+int stat_cols(Tile t) { return t == kTile256 ? 128 : 64; }
 
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream)
 {

@@ -10,25 +10,47 @@ namespace ag {
 namespace lm {
 namespace {
 
-// Eight columns of one row per thread: the fp32 sums of the splits, added in the order of the splits.
+// Eight columns of one row per unit: the fp32 sums of the splits.  L threads share a unit where there are
+// few units and many splits (thread l adds splits l, l + L, ... in that order, then the L sums are added in
+// theirs), so that enough loads are in flight: 64 splits of 33 x 1024 took 20 us with L = 1.
+template <int L>
 __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits, int64_t M, int64_t N, int64_t ldp,
                                                   LinearOut out, bool vec)
 {
+    constexpr int U = NT / L;                      // units of a workgroup
+    __shared__ f32x4 s_sum[L > 1 ? L - 1 : 1][U][2];
     const int64_t units = ldp / 8;
-    const int64_t u = blockIdx.x * (int64_t)NT + threadIdx.x;
-    if (u >= M * units)
-        return;
-    const int64_t row = u / units, col = (u - row * units) * 8;
-    const float* p = part + row * ldp + col;
-    f32x4 s0 = reinterpret_cast<const f32x4*>(p)[0], s1 = reinterpret_cast<const f32x4*>(p)[1];
-    for (int s = 1; s < splits; ++s) {
-        const f32x4* q = reinterpret_cast<const f32x4*>(p + s * M * ldp);
-        s0 += q[0];
-        s1 += q[1];
+    const int ul = threadIdx.x % U, sl = threadIdx.x / U;
+    const int64_t u = blockIdx.x * (int64_t)U + ul;
+    const bool there = u < M * units;
+    const int64_t row = there ? u / units : 0, col = there ? (u - row * units) * 8 : 0;
+    f32x4 s0 = {}, s1 = {};
+    if (there) {
+        const float* p = part + row * ldp + col;
+#pragma unroll 4
+        for (int s = sl; s < splits; s += L) {
+            const f32x4* q = reinterpret_cast<const f32x4*>(p + s * M * ldp);
+            s0 += q[0];
+            s1 += q[1];
+        }
+    }
+    if (L > 1) {
+        if (sl > 0) {
+            s_sum[sl - 1][ul][0] = s0;
+            s_sum[sl - 1][ul][1] = s1;
+        }
+        __syncthreads();
+        if (sl > 0)
+            return;
+#pragma unroll
+        for (int l = 0; l < L - 1; ++l) {
+            s0 += s_sum[l][ul][0];
+            s1 += s_sum[l][ul][1];
+        }
     }
     float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
     const int n = (int)min((int64_t)8, N - col);
-    if (n <= 0)
+    if (!there || n <= 0)
         return;
     float b[8] = {}, r[8] = {};
     if (out.bias)
@@ -85,43 +107,68 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
     }
 }
 
+// 64 columns of a workgroup, each summed by four threads (rows r, r + 4, ... of the partial sums).
 __global__ __launch_bounds__(NT) void colsum_join_kernel(const float* colsum, int64_t rows, int64_t N, __bf16* out)
 {
-    const int64_t c = blockIdx.x * (int64_t)NT + threadIdx.x;
-    if (c >= N)
-        return;
+    __shared__ float s_sum[4][64];
+    const int cl = threadIdx.x & 63, rl = threadIdx.x >> 6;
+    const int64_t c = blockIdx.x * (int64_t)64 + cl;
     float s = 0.0f;
-    for (int64_t r = 0; r < rows; ++r)
-        s += colsum[r * N + c];
-    out[c] = (__bf16)s;
+    if (c < N) {
+#pragma unroll 8
+        for (int64_t r = rl; r < rows; r += 4)
+            s += colsum[r * N + c];
+    }
+    s_sum[rl][cl] = s;
+    __syncthreads();
+    if (rl == 0 && c < N)
+        out[c] = (__bf16)((s_sum[0][cl] + s_sum[1][cl]) + (s_sum[2][cl] + s_sum[3][cl]));
 }
 
-// One wave per row: the pieces' (maximum, sum) pairs under one maximum.
+// The pieces' (maximum, sum) pairs of a row under one maximum.  W waves share a row: one, or four where a
+// row has so many pairs that one wave would read them in more than eight rounds.
+template <int W>
 __global__ __launch_bounds__(NT) void xent_join_kernel(const float* stat, int64_t stat_n, const float* hit,
                                                        const int64_t* targets, int64_t T, int64_t vocab, float* loss,
                                                        float* lse)
 {
-    const int64_t row = blockIdx.x * (int64_t)(NT / 64) + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
+    __shared__ float s_red[2][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = W == 1 ? blockIdx.x * (int64_t)(NT / 64) + wave : blockIdx.x;
     if (row >= T)
         return;
     const float2* p = reinterpret_cast<const float2*>(stat) + row * stat_n;
+    const int64_t i0 = W == 1 ? lane : threadIdx.x;
     float mx = -INFINITY;
-    for (int64_t i = lane; i < stat_n; i += 64)
+#pragma unroll 4
+    for (int64_t i = i0; i < stat_n; i += W * 64)
         mx = fmaxf(mx, p[i].x);
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1)
         mx = fmaxf(mx, __shfl_xor(mx, s));
+    if (W > 1) {
+        if (lane == 0)
+            s_red[0][wave] = mx;
+        __syncthreads();
+        mx = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+    }
     const float base = mx == -INFINITY ? 0.0f : mx;
     float sum = 0.0f;
-    for (int64_t i = lane; i < stat_n; i += 64) {
+#pragma unroll 4
+    for (int64_t i = i0; i < stat_n; i += W * 64) {
         const float2 v = p[i];
         sum += v.y * (v.x == -INFINITY ? (v.y != v.y ? v.y : 0.0f) : fast_exp(v.x - base));
     }
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1)
         sum += __shfl_xor(sum, s);
-    if (lane == 0) {
+    if (W > 1) {
+        if (lane == 0)
+            s_red[1][wave] = sum;
+        __syncthreads();
+        sum = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+    }
+    if (i0 == 0) {
         const float l = base + logf(sum);
         const int64_t y = targets[row];
         lse[row] = l;
@@ -137,7 +184,15 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
     const int64_t units = M * (ldp / 8);
     if (units <= 0)
         return hipSuccess;
-    join_kernel<<<dim3((unsigned)((units + NT - 1) / NT)), dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+    // four threads a unit once that leaves the chip's CUs with less than four workgroups each, sixteen likewise
+    const int L = splits >= 32 && units < 16384 ? 16 : splits >= 8 && units < 65536 ? 4 : 1;
+    const dim3 grid((unsigned)((units * L + NT - 1) / NT));
+    if (L == 16)
+        join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+    else if (L == 4)
+        join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+    else
+        join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
     return hipGetLastError();
 }
 
@@ -160,7 +215,7 @@ hipError_t launch_colsum_join(const float* colsum, int64_t rows, int64_t N, __bf
 {
     if (N <= 0)
         return hipSuccess;
-    colsum_join_kernel<<<dim3((unsigned)((N + NT - 1) / NT)), dim3(NT), 0, stream>>>(colsum, rows, N, out);
+    colsum_join_kernel<<<dim3((unsigned)((N + 63) / 64)), dim3(NT), 0, stream>>>(colsum, rows, N, out);
     return hipGetLastError();
 }
 
@@ -169,9 +224,11 @@ hipError_t launch_xent_join(const float* stat, int64_t stat_n, const float* hit,
 {
     if (T <= 0)
         return hipSuccess;
-    const int per = NT / 64;
-    xent_join_kernel<<<dim3((unsigned)((T + per - 1) / per)), dim3(NT), 0, stream>>>(stat, stat_n, hit, targets, T,
-                                                                                     vocab, loss, lse);
+    if (stat_n > 512)
+        xent_join_kernel<4><<<dim3((unsigned)T), dim3(NT), 0, stream>>>(stat, stat_n, hit, targets, T, vocab, loss, lse);
+    else
+        xent_join_kernel<1><<<dim3((unsigned)((T + NT / 64 - 1) / (NT / 64))), dim3(NT), 0, stream>>>(
+            stat, stat_n, hit, targets, T, vocab, loss, lse);
     return hipGetLastError();
 }
 
