@@ -442,6 +442,238 @@ __device__ __forceinline__ void grad8(const TileArgs& a, int64_t mrow, int64_t M
     *reinterpret_cast<bf16x8*>(a.out.C + mrow * a.out.ldc + col) = o;
 }
 
+// A tile's 32 rows x 32 FN columns in the accumulators of a wave, transposed: lane l has row l % 32 and, of each
+// 8 columns, the four from 4 (l / 32); acc[j][4 q + e] is column 32 j + 8 q + 4 (l / 32) + e.  Two lanes have a
+// row, so a row's maximum and sum need one step between lanes and no LDS.  `n`: valid columns of the block, yo:
+// the target's column in it, or -1.
+template <int FN>
+__device__ __forceinline__ void stat_block(const TileArgs& a, const f32x16* acc, int64_t row0, int64_t rows, int n, int yo,
+                                           int64_t slot, int lane)
+{
+    const uint32_t fh = lane >> 5;
+    const int64_t mrow = row0 + (lane & 31);
+    const bool valid = mrow < rows;
+    const int nr = n - (int)fh * 4;            // valid columns counted from the lane's first
+    constexpr float kLog2e = 1.4426950408889634f;
+    float v[FN * 16];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[j * 16 + e] = acc[j][e];
+    if (n < FN * 32) {                         // the vocabulary's last columns
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (j * 32 + (e >> 2) * 8 + (e & 3) >= nr)
+                    v[j * 16 + e] = -INFINITY;
+    }
+    float mx = v[0];                           // fmaxf passes over NaN: it comes back in the sum
+#pragma unroll
+    for (int e = 1; e < FN * 16; ++e)
+        mx = fmaxf(mx, v[e]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float base = mx == -INFINITY || mx != mx ? 0.0f : mx * kLog2e;
+    float sum[4] = {};
+#pragma unroll
+    for (int e = 0; e < FN * 16; ++e)
+        sum[e & 3] += __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -base));
+    float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    all += __shfl_xor(all, 32);
+    if (valid && fh == 0) {
+        float2* p = reinterpret_cast<float2*>(a.stat) + mrow * a.stat_n + slot;
+        *p = make_float2(mx, all);
+    }
+    const bool here = valid && yo >= 0 && yo < n && ((uint32_t)yo >> 2 & 1) == fh;
+    if (__ballot(here)) {
+        const int at = (yo >> 5) * 16 + (yo >> 3 & 3) * 4 + (yo & 3);
+        float hit = 0.0f;
+#pragma unroll
+        for (int e = 0; e < FN * 16; ++e)
+            hit = e == at ? v[e] : hit;
+        if (here)
+            a.hit[mrow] = hit;
+    }
+}
+
+// A wave's block in bf16 through its LDS slab: 32 rows of 64 FN bytes, 16-byte units swizzled by the row, the
+// units' halves by the row's bit 4, so that 32 rows of one column fall into distinct banks.
+template <int FN>
+__device__ __forceinline__ bf16x4* half_slab_at(char* slab, int j, int q, uint32_t fr, uint32_t fh)
+{
+    constexpr uint32_t RB = FN * 64, UN = RB / 16;
+    return reinterpret_cast<bf16x4*>(slab + fr * RB + (fh ^ (fr >> 4)) * 8 + (((uint32_t)(j * 4 + q) ^ (fr & (UN - 1))) * 16));
+}
+
+// The slab to memory in 16-byte pieces; p: the block's first element, rows, cols: what is valid of it (cols a
+// multiple of 8, rows start at 16-byte boundaries).  PAST: the stores pass the tiles' lines in L2 by.
+template <int FN, bool PAST>
+__device__ __forceinline__ void half_slab_out(const char* slab, __bf16* p, int64_t ld, int64_t rows, int64_t cols, int lane)
+{
+    constexpr uint32_t RB = FN * 64, UN = RB / 16;         // bytes and 16-byte units of a slab row
+    constexpr int RPI = 64 / UN;                           // rows of one read-back
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t u = lane % UN, r0 = lane / UN;
+    p += r0 * ld + u * 8;
+#pragma unroll
+    for (int it = 0; it < 32 / RPI; ++it) {
+        const uint32_t r = it * RPI + r0;
+        const i32x4 x = *reinterpret_cast<const i32x4*>(slab + r * RB + ((u ^ (r & (UN - 1))) * 16));
+        const i32x4 y = it * RPI >= 16 ? i32x4{x[2], x[3], x[0], x[1]} : x;   // RPI divides 16
+        if (r < rows && u * 8 < cols) {
+            i32x4* const out = reinterpret_cast<i32x4*>(p + it * RPI * ld);
+            if (PAST)
+                __builtin_nontemporal_store(y, out);
+            else
+                *out = y;
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
+    __builtin_amdgcn_wave_barrier();
+}
+
+// d logits of the same block, w (softmax - one at the target), rounded to bf16 for the products that follow;
+// zero in rows without a target.  neg_lse2: -lse log2(e).
+template <int FN>
+__device__ __forceinline__ void grad_block(const TileArgs& a, const f32x16* acc, char* slab, int64_t ldc, int64_t row0, int64_t rows,
+                                           int64_t col0, int n, int yo, bool has, float neg_lse2, float w, int lane)
+{
+    constexpr float kLog2e = 1.4426950408889634f;
+    const uint32_t fr = lane & 31, fh = lane >> 5;
+    const int nr = has ? n - (int)fh * 4 : 0;  // valid columns counted from the lane's first
+    float p[FN * 16];
+#pragma unroll
+    for (int e = 0; e < FN * 16; ++e)
+        p[e] = __builtin_amdgcn_exp2f(fmaf(acc[e >> 4][e & 15], kLog2e, neg_lse2));
+    if (__ballot(yo >= 0)) {
+        const int at = ((uint32_t)yo >> 2 & 1) == fh ? (yo >> 5) * 16 + (yo >> 3 & 3) * 4 + (yo & 3) : -1;
+#pragma unroll
+        for (int e = 0; e < FN * 16; ++e)
+            p[e] -= yo >= 0 && e == at ? 1.0f : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            bf16x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[e] = (__bf16)(j * 32 + q * 8 + e < nr ? p[j * 16 + q * 4 + e] * w : 0.0f);
+            }
+            *half_slab_at<FN>(slab, j, q, fr, fh) = o;
+        }
+    half_slab_out<FN, false>(slab, a.out.C + row0 * ldc + col0, ldc, rows - row0, ldc - col0, lane);
+}
+
+// act(x + bias) + residual of the same block, x in the accumulators, through the wave's LDS slab (32 rows of
+// 128 FN bytes of fp32, 16-byte units swizzled by the row); or x itself into `part` where the reduction is
+// split.  A row's eight columns come back to one lane.  part and C: the block's first row and column; at: the
+// same place in residual and pre; rows, cols: what is valid of the block.
+template <int FN>
+__device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* acc, char* slab, __bf16* C, float* part,
+                                             int64_t at, int64_t ldc, int64_t ldp, int rows, int cols, const float* bias,
+                                             bool between, int lane)
+{
+    constexpr int WNC = FN * 32;
+    constexpr uint32_t SW = WNC / 4 - 1;           // 16-byte units of a slab row, minus one
+    constexpr int LPR = WNC / 8;                   // lanes per slab row on the way back
+    constexpr int ITS = WNC / 16, RSTEP = 64 / LPR;  // read-backs of a slab, rows of one
+    const uint32_t fr = lane & 31, fh = lane >> 5;
+    const uint32_t c8 = (lane % LPR) * 8;
+    const int r0 = lane / LPR, n = min(8, cols - (int)c8);
+    const bool residual = a.out.residual && !part;
+    at += r0 * ldc + c8;
+    C += r0 * ldc + c8;
+    // the slab's residual is on its way while the slab is written
+    bf16x8 res[ITS] = {};
+    if (residual && a.vec) {
+#pragma unroll
+        for (int it = 0; it < ITS; ++it)
+            if (r0 + it * RSTEP < rows && n >= 8)
+                res[it] = *reinterpret_cast<const bf16x8*>(a.out.residual + at + it * RSTEP * ldc);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t colb = (j * 32 + q * 8 + fh * 4) * 4;
+            const f32x4 v4 = {acc[j][q * 4 + 0], acc[j][q * 4 + 1], acc[j][q * 4 + 2], acc[j][q * 4 + 3]};
+            *reinterpret_cast<f32x4*>(slab + fr * (WNC * 4) + (colb ^ ((fr & SW) << 4))) = v4;
+        }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
+    __builtin_amdgcn_wave_barrier();
+    auto unit = [&](int it, int half) {   // four of this lane's eight columns in its row it
+        const uint32_t r = it * RSTEP + r0;
+        return reinterpret_cast<f32x4*>(slab + r * (WNC * 4) + (((c8 + 4 * half) * 4) ^ ((r & SW) << 4)));
+    };
+    if (part) {
+        part += r0 * ldp + c8;
+#pragma unroll
+        for (int it = 0; it < ITS; ++it) {
+            f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+            if (r0 + it * RSTEP < rows && n > 0) {       // ldp % 8 == 0: whole vectors
+                f32x4* pv = reinterpret_cast<f32x4*>(part + it * RSTEP * ldp);
+                if (a.accumulate) {
+                    x0 += pv[0];
+                    x1 += pv[1];
+                }
+                pv[0] = x0;
+                pv[1] = x1;
+            }
+        }
+    } else {
+        if (between) {
+            // bias, pre and the activation in a loop of their own: unrolled into the stores below, the
+            // activations would be there once for each row of the block
+#pragma unroll 2
+            for (int it = 0; it < ITS; ++it) {
+                const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                float x[8] = {x0[0] + bias[0], x0[1] + bias[1], x0[2] + bias[2], x0[3] + bias[3],
+                              x1[0] + bias[4], x1[1] + bias[5], x1[2] + bias[6], x1[3] + bias[7]};
+                const bool in = r0 + it * RSTEP < rows && n > 0;
+                if (a.out.pre && in)
+                    store8(a.out.pre + at + it * RSTEP * ldc, n, a.vec, x);
+                act_value8(x, a.out.act);
+                if (residual) {
+                    *unit(it, 0) = f32x4{x[0], x[1], x[2], x[3]};
+                    *unit(it, 1) = f32x4{x[4], x[5], x[6], x[7]};
+                } else if (in) {
+                    store8(C + it * RSTEP * ldc, n, a.vec, x);
+                }
+            }
+        }
+        if (a.vec && (residual || !between)) {
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) {
+                const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                bf16x8 o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = (__bf16)((e < 4 ? x0[e & 3] : x1[e & 3]) + (residual ? (float)res[it][e] : 0.0f));
+                if (r0 + it * RSTEP < rows && n >= 8)
+                    __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(C + it * RSTEP * ldc));
+            }
+        } else if (residual || !between) {
+#pragma unroll 1
+            for (int it = 0; it < ITS; ++it) {
+                const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                if (r0 + it * RSTEP < rows)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < n) {
+                            const float x = e < 4 ? x0[e & 3] : x1[e & 3];
+                            C[it * RSTEP * ldc + e] =
+                                (__bf16)(residual ? x + (float)a.out.residual[at + it * RSTEP * ldc + e] : x);
+                        }
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------------------------- the kernel
 // EPI: kEpiLinear, kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
@@ -559,6 +791,22 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     acc[i][j][v] = 0.0f;
+
+        // cross entropy: what a lane's rows need in the epilogue is on its way during the K loop
+        const uint32_t fr = lane & 31;
+        int64_t target[FM];
+        float row_lse[FM], row_w[FM];
+        if constexpr (EPI != kEpiLinear) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int64_t mrow = min(m0 + (wm * FM + i) * 32 + fr, M - 1);
+                target[i] = a.targets[mrow];
+                if (EPI == kEpiGrad) {
+                    row_lse[i] = a.lse[mrow];
+                    row_w[i] = a.dloss[mrow];
+                }
+            }
+        }
 
         struct Dma {
             __amdgpu_buffer_rsrc_t ra, rb;
@@ -708,124 +956,73 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         wait_vmcnt0();     // loads past the last step have landed too
         __syncthreads();   // all waves are done with the stages
 
-        // ---- epilogue, one 32-row slab of the wave's block at a time through LDS: the read-back gives
-        // each lane eight consecutive columns of a row
+        // ---- epilogue, 32 rows of the wave's block at a time
         constexpr int SLAB = 32 * WNC * 4;
         static_assert(4 * SLAB <= SB::BYTES || (2 * SLAB <= SA::BYTES && 2 * SLAB <= SB::BYTES), "slabs fit a stage");
-        char* slab = 4 * SLAB <= SB::BYTES ? sB0 + wave * SLAB : (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
-        constexpr uint32_t SW = WNC / 4 - 1;           // 16-byte units of a slab row, minus one
-        constexpr int LPR = WNC / 8;                   // lanes per slab row on the way back
-        constexpr int ITS = WNC / 16;                  // read-backs of a slab
-        const uint32_t fr = lane & 31, fh = lane >> 5;
-        // a lane's eight columns are the same in every row it reads back
-        const uint32_t c8 = (lane % LPR) * 8, r_lane = lane / LPR;
-        const int64_t col = n0 + wn * WNC + c8;
-        const int n = (int)max((int64_t)0, min((int64_t)8, a.N - col));
-        __bf16* const C = a.out.C + (EPI == kEpiLinear && a.group == kGroupK ? g * a.M * a.out.ldc : 0);
-        const bool residual = a.out.residual && !a.part;
-        const bool between = !a.part && (a.out.bias || a.out.pre || a.out.act != kActNone);
-        float bias[8] = {};
-        if (EPI == kEpiLinear && between && a.out.bias)
-            load8(a.out.bias + col, n, a.vec, bias);
+        char* const slab = 4 * SLAB <= SB::BYTES ? sB0 + wave * SLAB : (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
+        // one block at a time in registers: its accumulators leave the matrix unit's registers here and not
+        // before, and nothing it computes is shared with the next block's or moved across
+        auto one_block = [&](f32x16* blk, int& lane_, int& flag) {
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (NM >= 16) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int64_t mrow0 = m0 + (wm * FM + i) * 32 + r_lane;       // this lane's first row of the slab
-            const int64_t at0 = (grow0 + mrow0) * a.out.ldc + col;
-            constexpr int RSTEP = 64 / LPR;                                // rows between its read-backs
-            // the slab's residual is on its way while the slab is written
-            bf16x8 res[ITS] = {};
-            if (EPI == kEpiLinear && residual && a.vec) {
-#pragma unroll
-                for (int it = 0; it < ITS; ++it)
-                    if (mrow0 + it * RSTEP < M && n >= 8)
-                        res[it] = *reinterpret_cast<const bf16x8*>(a.out.residual + at0 + it * RSTEP * a.out.ldc);
+                for (int j = 0; j < FN; ++j)
+                    asm volatile("" : "+a"(blk[j]));
             }
+            asm volatile("" : "+v"(lane_), "+s"(flag));
+        };
+        // what only the epilogue uses is computed here, not ahead of the tile loop where it would hold registers
+        // through the K loop
+        int el = lane;
+        int64_t ldc = a.out.ldc, ldp = a.ldp;
+        asm volatile("" : "+v"(el), "+s"(ldc), "+s"(ldp));
+        const int64_t wcol = n0 + wn * WNC;                            // the wave's first column
+        const int wcols = (int)max((int64_t)0, min((int64_t)WNC, a.N - wcol));
+        if constexpr (EPI == kEpiLinear) {
+            const int64_t mrow0 = m0 + wm * FM * 32;
+            const int64_t at = (grow0 + mrow0) * ldc + wcol;
+            __bf16* const C = a.out.C + (a.group == kGroupK ? g * a.M * ldc : 0) + at;
+            float* const part = a.part ? a.part + (split * a.M + mrow0) * ldp + wcol : nullptr;
+            const bool between = a.out.bias || a.out.pre || a.out.act != kActNone;
+            int plain = !(a.part || between || a.out.residual || !a.vec);
+            float bias[8] = {};
+            const int c8 = (el % (WNC / 8)) * 8, n = min(8, wcols - c8);
+            if (a.out.bias && n > 0)
+                load8(a.out.bias + wcol + c8, n, a.vec, bias);
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int i = 0; i < FM; ++i) {
+                one_block(acc[i], el, plain);
+                if (plain) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t colb = (j * 32 + q * 8 + fh * 4) * 4;
-                    const f32x4 v4 = {acc[i][j][q * 4 + 0], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2],
-                                      acc[i][j][q * 4 + 3]};
-                    *reinterpret_cast<f32x4*>(slab + fr * (WNC * 4) + (colb ^ ((fr & SW) << 4))) = v4;
-                }
-            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
-            __builtin_amdgcn_wave_barrier();
-            auto unit = [&](int it, int half) {   // four of this lane's eight columns in its row it
-                const uint32_t r = it * RSTEP + r_lane;
-                return reinterpret_cast<f32x4*>(slab + r * (WNC * 4) + (((c8 + 4 * half) * 4) ^ ((r & SW) << 4)));
-            };
-            if constexpr (EPI == kEpiLinear) {
-                if (between) {
-                    // bias, pre and the activation in a loop of their own, through the slab: unrolled into
-                    // the stores below, the activations would be there once for each row of the block
-#pragma unroll 2
-                    for (int it = 0; it < ITS; ++it) {
-                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                        float x[8] = {x0[0] + bias[0], x0[1] + bias[1], x0[2] + bias[2], x0[3] + bias[3],
-                                      x1[0] + bias[4], x1[1] + bias[5], x1[2] + bias[6], x1[3] + bias[7]};
-                        if (a.out.pre && mrow0 + it * RSTEP < M && n > 0)
-                            store8(a.out.pre + at0 + it * RSTEP * a.out.ldc, n, a.vec, x);
-                        act_value8(x, a.out.act);
-                        *unit(it, 0) = f32x4{x[0], x[1], x[2], x[3]};
-                        *unit(it, 1) = f32x4{x[4], x[5], x[6], x[7]};
-                    }
-                }
-                if (a.part) {
+                    for (int j = 0; j < FN; ++j)
 #pragma unroll
-                    for (int it = 0; it < ITS; ++it) {
-                        const int64_t mrow = mrow0 + it * RSTEP;
-                        f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                        if (mrow < M && n > 0) {       // ldp % 8 == 0: whole vectors
-                            f32x4* pv = reinterpret_cast<f32x4*>(a.part + (split * a.M + mrow) * a.ldp + col);
-                            if (a.accumulate) {
-                                x0 += pv[0];
-                                x1 += pv[1];
-                            }
-                            pv[0] = x0;
-                            pv[1] = x1;
-                        }
-                    }
-                } else if (a.vec) {
-#pragma unroll
-                    for (int it = 0; it < ITS; ++it) {
-                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                        bf16x8 o;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o[e] = (__bf16)((e < 4 ? x0[e & 3] : x1[e & 3]) + (residual ? (float)res[it][e] : 0.0f));
-                        // C is not read here again: its stores pass the tiles' lines in L2 by
-                        if (mrow0 + it * RSTEP < M && n >= 8)
-                            __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(C + at0 + it * RSTEP * a.out.ldc));
-                    }
+                        for (int q = 0; q < 4; ++q)
+                            *half_slab_at<FN>(slab, j, q, el & 31, (uint32_t)el >> 5) =
+                                bf16x4{(__bf16)acc[i][j][q * 4 + 0], (__bf16)acc[i][j][q * 4 + 1],
+                                       (__bf16)acc[i][j][q * 4 + 2], (__bf16)acc[i][j][q * 4 + 3]};
+                    half_slab_out<FN, true>(slab, C + i * 32 * ldc, ldc, M - mrow0 - i * 32, wcols, el);
                 } else {
-#pragma unroll 1
-                    for (int it = 0; it < ITS; ++it) {
-                        const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                        if (mrow0 + it * RSTEP < M)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (e < n) {
-                                    const int64_t at = at0 + it * RSTEP * a.out.ldc + e;
-                                    const float x = e < 4 ? x0[e & 3] : x1[e & 3];
-                                    C[at] = (__bf16)(residual ? x + (float)a.out.residual[at] : x);
-                                }
-                    }
-                }
-            } else {
-#pragma unroll 2
-                for (int it = 0; it < ITS; ++it) {
-                    const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                    float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-                    const int64_t mrow = mrow0 + it * RSTEP;
-                    if constexpr (EPI == kEpiStat)
-                        stat8<LPR>(a, mrow, M, col, n, tn * WN + wn, lane, x);
-                    else
-                        grad8(a, mrow, M, col, n, x);
+                    linear_block<FN>(a, acc[i], slab, C + i * 32 * ldc, part ? part + i * 32 * ldp : nullptr,
+                                     at + i * 32 * ldc, ldc, ldp, (int)max((int64_t)0, min((int64_t)32, M - mrow0 - i * 32)),
+                                     wcols, bias, between, el);
                 }
             }
-            __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
-            __builtin_amdgcn_wave_barrier();
+        } else {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                int cols = wcols;
+                one_block(acc[i], el, cols);
+                const int64_t brow = m0 + (wm * FM + i) * 32;
+                const int64_t y = target[i] - a.col0 - wcol;
+                const int yo = y >= 0 && y < WNC ? (int)y : -1;
+                if constexpr (EPI == kEpiStat) {
+                    stat_block<FN>(a, acc[i], brow, M, cols, yo, tn * WN + wn, el);
+                } else {
+                    const bool has = target[i] >= 0 && target[i] < a.vocab;
+                    grad_block<FN>(a, acc[i], slab, ldc, brow, M, wcol, cols, yo, has, -row_lse[i] * 1.4426950408889634f,
+                                   row_w[i], el);
+                }
+            }
         }
         __syncthreads();   // LDS is free for the next tile's loads
     }
