@@ -173,7 +173,11 @@ bool shapes_ok(int64_t M, int64_t Nc, int64_t K)
     return M >= 0 && Nc >= 0 && K >= 0 && K % 8 == 0;
 }
 
-bool too_large(int64_t M, int64_t Nc, int64_t K) { return K > kMaxDim || Nc > kMaxDim || M > kMaxRows; }
+bool too_large(int64_t M, int64_t Nc, int64_t K)
+{
+    // tiles are counted in 32 bits
+    return K > kMaxDim || Nc > kMaxDim || M > kMaxRows || (M / 128 + 1) * (std::max(Nc, K) / 128 + 1) > (1 << 28);
+}
 
 }  // namespace
 }  // namespace lm

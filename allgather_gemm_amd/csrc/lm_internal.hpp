@@ -32,7 +32,7 @@ struct TileArgs {
     int64_t lda, ldb;        // row strides in elements, multiples of 8
     int64_t M, N, K;
     int64_t k_valid;         // rows that a (K, N) B has where X's rows are zero-padded to K (launch_nn)
-    int64_t tiles_m, tiles_n;
+    int64_t tiles_n;
     // groups: rows [ends[e-1], ends[e]) of A (kGroupRows), or of the reduction (kGroupK; out.C of
     // group e starts at e * M * ldc)
     const int32_t* ends;
@@ -62,7 +62,7 @@ int tile_m(Tile t);
 int tile_n(Tile t);
 int stat_cols(Tile t);       // columns that one statistics pair covers
 
-// X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_m and tiles_n are filled in here.
+// X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_n is filled in here.
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream);
 // X (M, K) Y (N, K) for few rows (a.M, or a group's, about `rows`); out.part is not used.
 int rows_cols(int64_t N, int64_t rows);     // columns that one of its statistics pairs covers

@@ -9,22 +9,20 @@
 namespace ag {
 namespace lm {
 
-// Workgroups of a launch: one per tile, but with groups of rows, whose tile count only the device
-// knows, no more than stay resident (each walks the tiles in steps of the grid).
+// Workgroups of a launch: no more than stay resident, each walks the tiles in steps of the grid.  How many
+// tiles groups of rows make only the device knows.
 template <typename Kernel>
 hipError_t launch_tiles(Kernel kernel, int bm, int bn, int per_cu, TileArgs& a, hipStream_t stream)
 {
-    a.tiles_m = (a.M + bm - 1) / bm;
     a.tiles_n = (a.N + bn - 1) / bn;
     int cus = 0;
     hipError_t e = device_cus(&cus);
     if (e != hipSuccess)
         return e;
-    int64_t tiles = a.tiles_m * a.tiles_n * a.splits;
+    int64_t rows = (a.M + bm - 1) / bm;        // bm: of the lowest tile
     if (a.group == kGroupRows)
-        tiles = (a.tiles_m + a.E + 1) * a.tiles_n;
-    else if (a.group == kGroupK)
-        tiles *= a.E;
+        rows += a.E + 1;
+    const int64_t tiles = rows * a.tiles_n * (a.group == kGroupK ? a.E : a.splits);
     if (tiles <= 0)
         return hipSuccess;
     const int64_t grid = std::min<int64_t>(tiles, (int64_t)cus * per_cu);

@@ -8,20 +8,20 @@ namespace {
 template <int EPI>
 __global__ __launch_bounds__(NT, 1) void nt256_kernel(TileArgs a)
 {
-    tile_body<256, 256, 2, 2, 2, false, false, EPI>(a);
+    tile_body<256, 256, 2, 2, 2, false, false, EPI, true>(a);
 }
 
 template <int EPI>
 __global__ __launch_bounds__(NT, 2) void nt128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 2, false, false, EPI>(a);
+    tile_body<128, 128, 2, 2, 2, false, false, EPI, false>(a);
 }
 
 template <int EPI>
 hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 {
     if (t == kTile256)
-        return launch_tiles(nt256_kernel<EPI>, 256, 256, 1, a, stream);
+        return launch_tiles(nt256_kernel<EPI>, 128, 256, 1, a, stream);
     return launch_tiles(nt128_kernel<EPI>, 128, 128, 2, a, stream);
 }
 

@@ -17,8 +17,9 @@
 #pragma once
 
 #include "ag_device.hpp"
-#include "ag_protocol.hpp"
 #include "lm_internal.hpp"
+
+#include <type_traits>
 
 namespace ag {
 namespace lm {
@@ -40,6 +41,12 @@ __device__ __forceinline__ void stage_barrier()
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
+
+// One operand's stage in LDS.  One of 32 KiB is two arrays of 16 KiB, or one array and its middle; a smaller one
+// is `lo`.
+struct Part {
+    char *lo, *hi;
+};
 
 // One operand's side of the tile: R rows of the output's extent, T: column operand.
 template <int R, bool T>
@@ -119,16 +126,21 @@ struct Side {
             bytes -= BK * 2;
     }
 
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* stage, uint32_t wave_off, uint32_t off,
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, const Part& s, uint32_t wave_off, uint32_t off,
                                          uint32_t stride, int q) const
     {
-        dma16(r, stage + q * 4096 + wave_off, off + q * stride);
+        dma16(r, (OPS == 8 && q >= 4 ? s.hi + (q - 4) * 4096 : s.lo + q * 4096) + wave_off, off + q * stride);
     }
 };
 
-// Fragment addressing of one wave: F fragments of 32 rows, the wave's first row w * F * 32.
-template <int R, bool T, int F>
+// Fragment addressing of one wave: F fragments of 32 rows, those of the waves in turn (INTER: fragment i of wave w
+// is the tile's i * R / 32 / F + w, so which half of a 32 KiB stage it is in does not depend on the wave) or
+// one wave's next to each other (w * F + i; a row operand's 32 KiB are then one array).
+template <int R, bool T, int F, bool INTER>
 struct Frag {
+    static constexpr int WAVES = R / 32 / F;
+    static constexpr bool TWO = R == 256;
+    static_assert(!TWO || F == 4, "a stage's half has two of a wave's fragments, or all");
     uint32_t off[4 > F ? 4 : F];
 
     __device__ __forceinline__ void init(int lane, int w)
@@ -139,20 +151,21 @@ struct Frag {
             const uint32_t within = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
             for (int i = 0; i < F; ++i)
-                off[i] = k * Side<R, T>::RB + (((uint32_t)(w * F + i)) ^ Side<R, T>::ksw(k)) * 64 + within;
+                off[i] = k * Side<R, T>::RB +
+                         (((uint32_t)(INTER ? i * WAVES + w : w * F + i)) ^ Side<R, T>::ksw(k)) * 64 + within;
         } else {
             const uint32_t fsw = swz(fr & 15);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                off[kk] = (uint32_t)(w * F * 32 + fr) * 128 + (((uint32_t)(2 * kk) + fh) ^ fsw) * 16;
+                off[kk] = (uint32_t)((INTER ? w : w * F) * 32 + fr) * 128 + (((uint32_t)(2 * kk) + fh) ^ fsw) * 16;
         }
     }
 
     // Fragment i of substep kk: lane l holds row l % 32, k = 16 kk + 8 (l / 32) .. + 7.
-    __device__ __forceinline__ bf16x8 read(const char* stage, int kk, int i) const
+    __device__ __forceinline__ bf16x8 read(const Part& s, int kk, int i) const
     {
         if (T) {
-            const char* p = stage + off[i] + kk * 16 * Side<R, T>::RB;
+            const char* p = (TWO && kk >= 2 ? s.hi : s.lo) + off[i] + (TWO ? kk & 1 : kk) * 16 * Side<R, T>::RB;
             const bf16x4 lo = __builtin_bit_cast(
                 bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)const_cast<char*>(p)));
             const bf16x4 hi = __builtin_bit_cast(
@@ -160,7 +173,10 @@ struct Frag {
                 __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)const_cast<char*>(p + 4 * Side<R, T>::RB)));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-        return *reinterpret_cast<const bf16x8*>(stage + off[kk] + i * 4096);
+        if (INTER)
+            return *reinterpret_cast<const bf16x8*>((TWO && i >= 2 ? s.hi : s.lo) + off[kk] +
+                                                    (TWO ? i & 1 : i) * WAVES * 4096);
+        return *reinterpret_cast<const bf16x8*>(s.lo + off[kk] + i * 4096);      // one array
     }
 };
 
@@ -325,11 +341,33 @@ __device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t
 }
 
 // ------------------------------------------------------------------------------------- groups
-// Ends of the groups as the kernel uses them: s_end[e] is the running maximum of ends[0..e] within
-// [0, limit], so groups from any table stay inside the tensors, and s_end[E] = limit closes a last
-// group of rows that belong to none.  s_tile[e] is the first of group e's tile rows of bm rows,
-// s_tile[E + 1] their number.  Wave 0 scans, 64 lanes over E + 1 entries; ends with a barrier.
-__device__ void group_scan(const int32_t* ends, int E, int64_t limit, int bm, int32_t* s_end, int32_t* s_tile)
+// The groups as the kernel uses them.  end[e] is the running maximum of ends[0..e] within [0, limit], so
+// groups from any table stay inside the tensors, and end[E] = limit closes a last group of rows that belong to
+// none.  Rows of group e are cut into tile rows of BM and, where at most BM / 2 remain, one of BM / 2: big[e]
+// and half[e] are the first of each kind, big[E + 1] and half[E + 1] their numbers.
+struct Groups {
+    int32_t end[kMaxGroups + 1], big[kMaxGroups + 2], half[kMaxGroups + 2];
+};
+// Groups of the reduction have no tile rows of their own, but an order: by their size, largest first.
+struct KGroups {
+    int32_t end[kMaxGroups + 1], order[kMaxGroups];
+};
+
+// Tile rows of n rows: of BM rows, and (HALF) of BM / 2.
+template <int BM, bool HALF>
+__device__ __forceinline__ int big_rows(int n)
+{
+    return HALF ? n / BM + (n % BM > BM / 2) : (n + BM - 1) / BM;
+}
+template <int BM, bool HALF>
+__device__ __forceinline__ int half_rows(int n)
+{
+    return HALF && n % BM > 0 && n % BM <= BM / 2;
+}
+
+// Wave 0 scans, 64 lanes over E + 1 entries; ends with a barrier.
+template <int BM, bool HALF, typename G>
+__device__ void group_scan(const int32_t* ends, int E, int64_t limit, G& s)
 {
     if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) == 0) {
         const int lane = threadIdx.x & 63;
@@ -347,31 +385,98 @@ __device__ void group_scan(const int32_t* ends, int E, int64_t limit, int bm, in
         before = __shfl_up(before, 1);
         if (lane == 0)
             before = 0;
-        int prev = before, tiles = 0;
+        int prev = before, big = 0, half = 0;
         for (int e = e0; e < e1; ++e) {
             const int end = max(prev, e < E ? min(ends[e], lim) : lim);
-            s_end[e] = end;
-            tiles += (end - prev + bm - 1) / bm;
+            s.end[e] = end;
+            big += big_rows<BM, HALF>(end - prev);
+            half += half_rows<BM, HALF>(end - prev);
             prev = end;
         }
-        int first = tiles;
-        for (int s = 1; s < 64; s <<= 1) {
-            const int o = __shfl_up(first, s);
-            if (lane >= s)
-                first += o;
+        if constexpr (std::is_same<G, Groups>::value) {
+            int big0 = big, half0 = half;
+            for (int s = 1; s < 64; s <<= 1) {
+                const int o = __shfl_up(big0, s), q = __shfl_up(half0, s);
+                if (lane >= s) {
+                    big0 += o;
+                    half0 += q;
+                }
+            }
+            big0 -= big;
+            half0 -= half;
+            prev = before;
+            for (int e = e0; e < e1; ++e) {
+                s.big[e] = big0;
+                s.half[e] = half0;
+                const int n = s.end[e] - prev;
+                big0 += big_rows<BM, HALF>(n);
+                half0 += half_rows<BM, HALF>(n);
+                prev = s.end[e];
+            }
+            if (e1 == E + 1 && e0 < e1) {
+                s.big[E + 1] = big0;
+                s.half[E + 1] = half0;
+            }
         }
-        first -= tiles;
-        prev = before;
-        for (int e = e0; e < e1; ++e) {
-            s_tile[e] = first;
-            const int end = s_end[e];
-            first += (end - prev + bm - 1) / bm;
-            prev = end;
-        }
-        if (e1 == E + 1 && e0 < e1)
-            s_tile[E + 1] = first;
     }
     barrier_after_lds_write();
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The last group whose first, as first(group) says, is <= x.
+template <typename First>
+__device__ __forceinline__ int group_of(int E, int x, First first)
+{
+    int lo = 0, hi = E + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uniform(first(mid)) <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Ends with a barrier.
+__device__ __forceinline__ void order_groups(KGroups& s, int E)
+{
+    for (int e = threadIdx.x; e < E; e += NT) {
+        const int n = s.end[e] - (e ? s.end[e - 1] : 0);
+        int rank = 0, prev = 0;
+        for (int f = 0; f < E; ++f) {
+            const int end = s.end[f], m = end - prev;
+            rank += m > n || (m == n && f < e);
+            prev = end;
+        }
+        s.order[rank] = e;
+    }
+    barrier_after_lds_write();
+}
+
+// Tile t of a rows x cols grid, GROUP_M tile rows at a time column by column, so that the tiles in flight
+// share rows of A and of B in the caches.
+__device__ __forceinline__ void tile_of(int t, int rows, int cols, int& m, int& n)
+{
+    const int per = GROUP_M * cols, group = t / per, first = group * GROUP_M;
+    const int here = min(rows - first, GROUP_M), in = t - group * per;
+    n = in / here;
+    m = first + in - n * here;
+}
+
+// Units (tile rows, or two halves) to be taken apart into halves so that a last round of tiles that fills few of G
+// workgroups becomes a shorter one: n units and `lone` halves of c tiles each.  A half tile takes about 12/20 of a
+// tile's time.
+__device__ __forceinline__ int units_to_halve(int n, int lone, int c, int G)
+{
+    const int last = (int)((int64_t)n * c % G);
+    if (last == 0)
+        return 0;
+    const int64_t keep = max((int64_t)0, (int64_t)lone * c - 2 * (G - last));        // halves left past the last round
+    const int d = (last + c - 1) / c;
+    const int64_t cut = max((int64_t)0, (int64_t)(lone + 2 * d) * c - 2 * (d * c - last));
+    return 20 + 12 * ((keep + G - 1) / G) > 12 * ((cut + G - 1) / G) ? d : 0;
 }
 
 // ------------------------------------------------------------------------------ cross entropy
@@ -675,107 +780,53 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
 }
 
 // ---------------------------------------------------------------------------------- the kernel
-// EPI: kEpiLinear, kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
+// The stages, in arrays of their own: the compiler then sees that the loads in flight fill another stage than the
+// one being read, and does not wait for them.  slab: this wave's part of them in the epilogue.
+template <int S>
+struct Stages {
+    Part a[S], b[S];
+    char* slab;
+};
+
+// Where a tile lies: its first row within its group (or among all rows) and first column.
+struct Where {
+    int64_t m0, n0, M, K, k_first, grow0;
+    int tn, g, split;
+    bool zero;                                         // rows past the last group
+};
+
+// One tile.  EPI: kEpiLinear, kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
-__device__ __forceinline__ void tile_body(const TileArgs& a)
+__device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>& l, const Where& w)
 {
-    static_assert(WM * WN == 4 && (S == 2 || S == 4), "four waves; two or four stages");
+    static_assert(WM * WN == 4, "four waves");
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32, NM = FM * FN;
     typedef Side<BM, TA> SA;
     typedef Side<BN, TB> SB;
     constexpr int ND = SA::OPS + SB::OPS;
     constexpr int WNC = FN * 32;                       // columns of a wave's block
 
-    // one array per stage and operand: the compiler then sees that the loads in flight fill another
-    // stage than the one being read, and does not wait for them
-    __shared__ __attribute__((aligned(1024))) char sA0[SA::BYTES];
-    __shared__ __attribute__((aligned(1024))) char sB0[SB::BYTES];
-    __shared__ __attribute__((aligned(1024))) char sA1[SA::BYTES];
-    __shared__ __attribute__((aligned(1024))) char sB1[SB::BYTES];
-    __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? SA::BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? SB::BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sA3[S > 2 ? SA::BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sB3[S > 2 ? SB::BYTES : 16];
-    __shared__ int32_t s_end[EPI == kEpiLinear ? kMaxGroups + 2 : 1];    // clamped ends of the groups, and M
-    __shared__ int32_t s_tile[EPI == kEpiLinear ? kMaxGroups + 2 : 1];   // first tile row of each group
-
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int G = gridDim.x;
-    // workgroups are dispatched round-robin over the 8 XCDs: each XCD takes a contiguous run of tiles
-    const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
-
-    int64_t tile_rows = a.tiles_m;
-    if (EPI == kEpiLinear && a.group != kGroupNone) {
-        group_scan(a.ends, a.E, a.group == kGroupRows ? a.M : a.K, BM, s_end, s_tile);
-        if (a.group == kGroupRows)
-            tile_rows = __builtin_amdgcn_readfirstlane(s_tile[a.E + 1]);
-    }
-    const int64_t num_tiles = tile_rows * a.tiles_n * (a.group == kGroupK ? a.E : 1) * a.splits;
+    const int64_t m0 = w.m0, n0 = w.n0, M = w.M, K = w.K, grow0 = w.grow0, tn = w.tn, g = w.g, split = w.split;
 
     SA sa;
     SB sb;
-    Frag<BM, TA, FM> fa;
-    Frag<BN, TB, FN> fb;
+    Frag<BM, TA, FM, true> fa;
+    Frag<BN, TB, FN, false> fb;
     fa.init(lane, wm);
     fb.init(lane, wn);
     sa.init(tid, a.lda);
     sb.init(tid, a.ldb);
     const uint32_t wave_off = wave * 1024;
-
-    for (int64_t t = vid; t < num_tiles; t += G) {
-        // ---- which tile
-        int64_t tm, tn, split = 0, g = 0, grow0 = 0, M = a.M, K = a.K, k_first = 0;
-        bool zero = false;
-        if (EPI == kEpiLinear && a.group == kGroupRows) {
-            const int64_t tr = t / a.tiles_n;            // tile rows of one group lie together
-            int lo = 0, hi = a.E + 1;
-            while (hi - lo > 1) {                        // last group whose first tile row is <= tr
-                const int mid = (lo + hi) >> 1;
-                if (__builtin_amdgcn_readfirstlane(s_tile[mid]) <= tr)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            g = lo;
-            const int64_t first = __builtin_amdgcn_readfirstlane(s_tile[lo]);
-            const int64_t rows_here = __builtin_amdgcn_readfirstlane(s_tile[lo + 1]) - first;
-            pm_tile_of(t - first * a.tiles_n, rows_here, a.tiles_n, 0, GROUP_M, tm, tn);
-            grow0 = lo == 0 ? 0 : __builtin_amdgcn_readfirstlane(s_end[lo - 1]);
-            M = __builtin_amdgcn_readfirstlane(s_end[lo]) - grow0;
-            zero = lo == a.E;                            // rows past the last group
-            if (zero)
-                K = 0;
-        } else {
-            int64_t u = t;
-            if (EPI == kEpiLinear) {
-                const int64_t per = a.tiles_m * a.tiles_n;
-                if (a.group == kGroupK) {
-                    g = u / per;
-                    u -= g * per;
-                    k_first = g == 0 ? 0 : __builtin_amdgcn_readfirstlane(s_end[g - 1]);
-                    K = __builtin_amdgcn_readfirstlane(s_end[g]) - k_first;
-                } else {
-                    split = u / per;
-                    u -= split * per;
-                }
-            }
-            pm_tile_of(u, a.tiles_m, a.tiles_n, 0, GROUP_M, tm, tn);
-        }
-        const int64_t m0 = tm * BM, n0 = tn * BN;
+    {
         const int64_t a_rows = min((int64_t)BM, M - m0), b_rows = min((int64_t)BN, a.N - n0);
-        const __bf16* Ab;
-        const __bf16* Bb;
-        if (TA)
-            Ab = a.A + k_first * a.lda + m0;
-        else
-            Ab = a.A + (grow0 + m0) * a.lda;
-        if (TB)
-            Bb = a.B + (a.group == kGroupK ? k_first * a.ldb : (zero ? 0 : g) * a.strideB) + n0;
-        else
-            Bb = a.B + (zero ? 0 : g) * a.strideB + n0 * a.ldb;
+        const int64_t gb = w.zero ? 0 : g;
+        const __bf16* const Ab = TA ? a.A + w.k_first * a.lda + m0 : a.A + (grow0 + m0) * a.lda;
+        const __bf16* const Bb = TB ? a.B + (a.group == kGroupK ? w.k_first * a.ldb : gb * a.strideB) + n0
+                                    : a.B + gb * a.strideB + n0 * a.ldb;
         const int64_t nk_all = (K + BK - 1) / BK;
         const int64_t kb0 = min(split * a.split_steps, nk_all);
         const int64_t kb1 = a.splits > 1 ? min(kb0 + a.split_steps, nk_all) : nk_all;
@@ -799,7 +850,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         if constexpr (EPI != kEpiLinear) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                const int64_t mrow = min(m0 + (wm * FM + i) * 32 + fr, M - 1);
+                const int64_t mrow = min(m0 + (i * WM + wm) * 32 + fr, M - 1);
                 target[i] = a.targets[mrow];
                 if (EPI == kEpiGrad) {
                     row_lse[i] = a.lse[mrow];
@@ -811,10 +862,10 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         struct Dma {
             __amdgpu_buffer_rsrc_t ra, rb;
             uint32_t va, vb, lw, sa_, sb_;
-            char *la, *lb;
+            Part la, lb;
         };
         // the next step's loads, into a stage; past the last step they read nothing but still count
-        auto dma_setup = [&](char* la, char* lb) {
+        auto dma_setup = [&](int c) {
             Dma d;
             d.lw = wave_off;
             d.sa_ = sa.op_stride;
@@ -824,8 +875,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             d.rb = sb.rsrc();
             d.va = sa.offset();
             d.vb = sb.offset();
-            d.la = la;
-            d.lb = lb;
+            d.la = l.a[c];
+            d.lb = l.b[c];
             sa.advance();
             sb.advance();
             return d;
@@ -836,17 +887,17 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             else
                 sb.load(d.rb, d.lb, d.lw, d.vb, d.sb_, q - SA::OPS);
         };
-        auto issue_all = [&](char* la, char* lb) {
-            const Dma d = dma_setup(la, lb);
+        auto issue_all = [&](int c) {
+            const Dma d = dma_setup(c);
 #pragma unroll
             for (int q = 0; q < ND; ++q)
                 dma_op(d, q);
         };
         // MFMAs of one substep out of (bf, af), with what is to be issued between them: the next
-        // substep's fragment reads into (nbf, naf), one after each of the first MFMAs, and loads
+        // substep's fragment reads (out of stage c), one after each of the first MFMAs, and loads
         // [q0, q1) spread over all of them, so neither queue backs up into the matrix instructions.
         bf16x8 af[2][FM], bf[2][FN];
-        auto block = [&](int set, const char* la, const char* lb, int next, const Dma& d, int q0, int q1) {
+        auto block = [&](int set, int c, int next, const Dma& d, int q0, int q1) {
             const int other = set ^ 1;
 #pragma unroll
             for (int gi = 0; gi < NM; ++gi) {
@@ -859,9 +910,9 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
 #pragma unroll
                     for (int r = gi * NR / RS; r < (gi + 1) * NR / RS; ++r) {
                         if (r < FN)
-                            bf[other][r] = fb.read(lb, next, r);
+                            bf[other][r] = fb.read(l.b[c], next, r);
                         else
-                            af[other][r - FN] = fa.read(la, next, r - FN);
+                            af[other][r - FN] = fa.read(l.a[c], next, r - FN);
                     }
                 }
 #pragma unroll
@@ -870,86 +921,84 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        auto first_frags = [&](const char* la, const char* lb) {
+        auto first_frags = [&](int c) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                bf[0][j] = fb.read(lb, 0, j);
+                bf[0][j] = fb.read(l.b[c], 0, j);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                af[0][i] = fa.read(la, 0, i);
+                af[0][i] = fa.read(l.a[c], 0, i);
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        if constexpr (S == 2) {
-            // Double buffer.  A step out of stage c is four substeps; its barrier stands before the last
-            // one: there every wave has read all of stage c's fragments, and the other stage's loads,
-            // issued around the step's start, have landed.  The last substep's MFMAs then cover the
-            // first fragment reads of the next step and the first half of the loads that refill stage c.
+        if constexpr (S == 2 || S == 3) {
+            // A step out of stage c is four substeps; its barrier stands before the last one: there every wave
+            // has read all of stage c's fragments, and the next stage's loads have landed.  The last substep's
+            // MFMAs then cover the first fragment reads of the next step and the first half of the loads that
+            // refill stage c; the other half follows in the next step's first substep.
             Dma d;
-            auto step = [&](char* ca, char* cb, char* na, char* nb) {
-                block(0, ca, cb, 1, d, ND / 2, ND);
-                block(1, ca, cb, 2, d, 0, 0);
-                block(0, ca, cb, 3, d, 0, 0);
-                wait_vmcnt0();
+            auto step = [&](int c) {
+                const int n = (c + 1) % S;
+                block(0, c, 1, d, ND / 2, ND);
+                block(1, c, 2, d, 0, 0);
+                block(0, c, 3, d, 0, 0);
+                wait_vmcnt<(S - 2) * ND>();
                 stage_barrier();
-                d = dma_setup(ca, cb);
-                block(1, na, nb, 0, d, 0, ND / 2);
+                d = dma_setup(c);
+                block(1, n, 0, d, 0, ND / 2);
             };
-            // the start of a tile: its first step into one stage, half of its second into the other
-            auto start = [&](char* ca, char* cb, char* na, char* nb) {
-                issue_all(ca, cb);
-                wait_vmcnt0();
+            // the start of a tile: its first S - 1 steps into the stages from c on, half of the next one
+            auto start = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < S - 1; ++i)
+                    issue_all((c + i) % S);
+                wait_vmcnt<(S - 2) * ND>();
                 stage_barrier();
-                d = dma_setup(na, nb);
+                d = dma_setup((c + S - 1) % S);
 #pragma unroll
                 for (int q = 0; q < ND / 2; ++q)
                     dma_op(d, q);
-                first_frags(ca, cb);
+                first_frags(c);
             };
-            // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
-            // computes twice per iteration
             int64_t kb = kb0;
-            if ((kb1 - kb0) & 1) {
-                start(sA1, sB1, sA0, sB0);
-                step(sA1, sB1, sA0, sB0);
-                ++kb;
+            if constexpr (S == 2) {
+                // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
+                // computes twice per iteration
+                if ((kb1 - kb0) & 1) {
+                    start(1);
+                    step(1);
+                    ++kb;
+                } else if (kb1 > kb0) {
+                    start(0);
+                }
             } else if (kb1 > kb0) {
-                start(sA0, sB0, sA1, sB1);
+                start(0);                // steps past the last, up to a multiple of three, multiply zeros
             }
-            for (; kb < kb1; kb += 2) {
-                step(sA0, sB0, sA1, sB1);
-                step(sA1, sB1, sA0, sB0);
+            for (; kb < kb1; kb += S) {
+#pragma unroll
+                for (int c = 0; c < S; ++c)
+                    step(c);
             }
         } else {
             // four stages: the loads of three steps are in flight while one is computed
-            auto compute = [&](const char* la, const char* lb, const Dma& d) {
-                first_frags(la, lb);
-                block(0, la, lb, 1, d, 0, ND / 2);
-                block(1, la, lb, 2, d, ND / 2, ND);
-                block(0, la, lb, 3, d, 0, 0);
-                block(1, la, lb, -1, d, 0, 0);
+            auto compute = [&](int c, const Dma& d) {
+                first_frags(c);
+                block(0, c, 1, d, 0, ND / 2);
+                block(1, c, 2, d, ND / 2, ND);
+                block(0, c, 3, d, 0, 0);
+                block(1, c, -1, d, 0, 0);
             };
-            issue_all(sA0, sB0);
-            issue_all(sA1, sB1);
-            issue_all(sA2, sB2);
+            issue_all(0);
+            issue_all(1);
+            issue_all(2);
             for (int64_t kb = kb0; kb < kb1; kb += 4) {
-                wait_vmcnt<2 * ND>();
-                stage_barrier();
-                compute(sA0, sB0, dma_setup(sA3, sB3));
-                if (kb + 1 < kb1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (kb + c >= kb1)
+                        break;
                     wait_vmcnt<2 * ND>();
                     stage_barrier();
-                    compute(sA1, sB1, dma_setup(sA0, sB0));
-                }
-                if (kb + 2 < kb1) {
-                    wait_vmcnt<2 * ND>();
-                    stage_barrier();
-                    compute(sA2, sB2, dma_setup(sA1, sB1));
-                }
-                if (kb + 3 < kb1) {
-                    wait_vmcnt<2 * ND>();
-                    stage_barrier();
-                    compute(sA3, sB3, dma_setup(sA2, sB2));
+                    compute(c, dma_setup((c + 3) % 4));
                 }
             }
         }
@@ -957,9 +1006,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         __syncthreads();   // all waves are done with the stages
 
         // ---- epilogue, 32 rows of the wave's block at a time
-        constexpr int SLAB = 32 * WNC * 4;
-        static_assert(4 * SLAB <= SB::BYTES || (2 * SLAB <= SA::BYTES && 2 * SLAB <= SB::BYTES), "slabs fit a stage");
-        char* const slab = 4 * SLAB <= SB::BYTES ? sB0 + wave * SLAB : (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
+        char* const slab = l.slab;
         // one block at a time in registers: its accumulators leave the matrix unit's registers here and not
         // before, and nothing it computes is shared with the next block's or moved across
         auto one_block = [&](f32x16* blk, int& lane_, int& flag) {
@@ -979,7 +1026,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         const int64_t wcol = n0 + wn * WNC;                            // the wave's first column
         const int wcols = (int)max((int64_t)0, min((int64_t)WNC, a.N - wcol));
         if constexpr (EPI == kEpiLinear) {
-            const int64_t mrow0 = m0 + wm * FM * 32;
+            const int64_t mrow0 = m0 + wm * 32;                        // blocks WM x 32 rows apart
             const int64_t at = (grow0 + mrow0) * ldc + wcol;
             __bf16* const C = a.out.C + (a.group == kGroupK ? g * a.M * ldc : 0) + at;
             float* const part = a.part ? a.part + (split * a.M + mrow0) * ldp + wcol : nullptr;
@@ -1000,10 +1047,10 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
                             *half_slab_at<FN>(slab, j, q, el & 31, (uint32_t)el >> 5) =
                                 bf16x4{(__bf16)acc[i][j][q * 4 + 0], (__bf16)acc[i][j][q * 4 + 1],
                                        (__bf16)acc[i][j][q * 4 + 2], (__bf16)acc[i][j][q * 4 + 3]};
-                    half_slab_out<FN, true>(slab, C + i * 32 * ldc, ldc, M - mrow0 - i * 32, wcols, el);
+                    half_slab_out<FN, true>(slab, C + i * WM * 32 * ldc, ldc, M - mrow0 - i * WM * 32, wcols, el);
                 } else {
-                    linear_block<FN>(a, acc[i], slab, C + i * 32 * ldc, part ? part + i * 32 * ldp : nullptr,
-                                     at + i * 32 * ldc, ldc, ldp, (int)max((int64_t)0, min((int64_t)32, M - mrow0 - i * 32)),
+                    linear_block<FN>(a, acc[i], slab, C + i * WM * 32 * ldc, part ? part + i * WM * 32 * ldp : nullptr,
+                                     at + i * WM * 32 * ldc, ldc, ldp, (int)max((int64_t)0, min((int64_t)32, M - mrow0 - i * WM * 32)),
                                      wcols, bias, between, el);
                 }
             }
@@ -1012,7 +1059,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             for (int i = 0; i < FM; ++i) {
                 int cols = wcols;
                 one_block(acc[i], el, cols);
-                const int64_t brow = m0 + (wm * FM + i) * 32;
+                const int64_t brow = m0 + (i * WM + wm) * 32;
                 const int64_t y = target[i] - a.col0 - wcol;
                 const int yo = y >= 0 && y < WNC ? (int)y : -1;
                 if constexpr (EPI == kEpiStat) {
@@ -1025,6 +1072,199 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
             }
         }
         __syncthreads();   // LDS is free for the next tile's loads
+    }
+}
+
+// The tiles of one workgroup.  HALF: tiles of half the height exist too, for what is left of a group's rows and
+// for the last round of tiles.
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI, bool HALF>
+__device__ __forceinline__ void tile_body(const TileArgs& a)
+{
+    // The half tile has three stages, for it computes on one for half as long: A of two in the halves of A's first
+    // stage, in arrays of their own, B of the third where A's second is.
+    constexpr int AB = Side<BM, TA>::BYTES, BB = Side<BN, TB>::BYTES, HALF_A = 16384;
+    static_assert(!HALF || (AB == 32768 && BB == 32768), "256 x 256");
+    __shared__ __attribute__((aligned(1024))) char sA0[HALF ? HALF_A : AB], sU0[HALF ? HALF_A : 16];
+    __shared__ __attribute__((aligned(1024))) char sB0[BB];
+    __shared__ __attribute__((aligned(1024))) char sA1[AB];
+    __shared__ __attribute__((aligned(1024))) char sB1[BB];
+    __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? AB : HALF ? HALF_A : 16];
+    __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? BB : 16];
+    __shared__ __attribute__((aligned(1024))) char sA3[S > 2 ? AB : 16];
+    __shared__ __attribute__((aligned(1024))) char sB3[S > 2 ? BB : 16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int SLAB = 32 * (BN / WN) * 4;           // 32 rows of a wave's block in fp32
+    Stages<S> l;
+    l.a[0] = {sA0, sU0};
+    l.b[0] = {sB0, sB0 + 16384};
+    l.a[1] = {sA1, sA1 + AB / 2};
+    l.b[1] = {sB1, sB1 + 16384};
+    if constexpr (S == 4) {
+        static_assert(4 * SLAB <= BB, "slabs fit a stage of B");
+        l.a[2].lo = sA2;
+        l.b[2] = {sB2, sB2 + 16384};
+        l.a[3].lo = sA3;
+        l.b[3] = {sB3, sB3 + 16384};
+        l.slab = sB0 + wave * SLAB;
+    } else {
+        static_assert(HALF ? SLAB == HALF_A : 2 * SLAB <= AB && 2 * SLAB <= BB, "slabs fit a stage");
+        l.slab = wave >= 2 ? sB0 + (wave - 2) * SLAB : !HALF ? sA0 + wave * SLAB : wave ? sU0 : sA0;
+    }
+    Stages<3> lh;
+    lh.a[0].lo = sA0;
+    lh.a[1].lo = sU0;
+    lh.a[2].lo = sA2;
+    lh.b[0] = l.b[0];
+    lh.b[1] = l.b[1];
+    lh.b[2] = l.a[1];
+    lh.slab = l.slab;
+    constexpr bool ROWS = EPI == kEpiLinear && !TA, KS = EPI == kEpiLinear && TA;   // groups there can be
+    __shared__ typename std::conditional<ROWS, Groups, typename std::conditional<KS, KGroups, int>::type>::type s_groups;
+
+    const int G = gridDim.x;
+    // workgroups are dispatched round-robin over the 8 XCDs: each XCD takes a contiguous run of tiles
+    const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+    const int cols = (int)a.tiles_n;
+    const bool by_rows = ROWS && a.group == kGroupRows, by_k = KS && a.group == kGroupK;
+
+    // Units of one tile's time: a tile row, or two groups' halves, which stand where the second group's rows end,
+    // so that a group's weights are read for its tiles and its half at about the same time.  `lone`: a half left
+    // over.  (Of groups that split the reduction each has all the rows.)
+    int nb = big_rows<BM, HALF>((int)a.M), nh = half_rows<BM, HALF>((int)a.M);
+    if constexpr (ROWS) {
+        if (by_rows) {
+            group_scan<BM, HALF>(a.ends, a.E, a.M, s_groups);
+            nb = uniform(s_groups.big[a.E + 1]);
+            nh = uniform(s_groups.half[a.E + 1]);
+        }
+    }
+    if constexpr (KS) {
+        if (by_k) {
+            group_scan<BM, HALF>(a.ends, a.E, a.K, s_groups);
+            order_groups(s_groups, a.E);
+        }
+    }
+    const int parts = by_k ? a.E : a.splits, lone = nh & 1;
+    const int all_units = nb + nh / 2, cut = HALF && !by_k ? units_to_halve(all_units, lone, cols * parts, G) : 0;
+    const int units = all_units - cut, halves = 2 * cut + lone;        // rows of tiles
+
+    auto in_part = [&](int t, int rows, int& tm, Where& w) {           // tile t of `rows` rows for each part
+        const int per = rows * cols, part = t / per;
+        tile_of(t - part * per, rows, cols, tm, w.tn);
+        if constexpr (KS) {
+            if (by_k) {
+                const int g = uniform(s_groups.order[part]);
+                w.g = g;
+                w.k_first = g ? uniform(s_groups.end[g - 1]) : 0;
+                w.K = uniform(s_groups.end[g]) - w.k_first;
+                return;
+            }
+        }
+        w.split = part;
+    };
+    auto in_group = [&](int g, Where& w) {
+        if constexpr (ROWS) {
+            w.g = g;
+            w.grow0 = g ? uniform(s_groups.end[g - 1]) : 0;
+            w.M = uniform(s_groups.end[g]) - w.grow0;
+            w.zero = g == a.E;
+            if (w.zero)
+                w.K = 0;
+        }
+    };
+    auto unit_of = [&](int g) { return ROWS ? ((const Groups&)s_groups).big[g] + ((const Groups&)s_groups).half[g] / 2 : 0; };
+    auto group_half = [&](int q, Where& w) {                           // the groups' half number q
+        if constexpr (ROWS) {
+            const int g = group_of(a.E, q, [&](int e) { return s_groups.half[e]; });
+            in_group(g, w);
+            w.m0 = (int64_t)(uniform(s_groups.big[g + 1]) - uniform(s_groups.big[g])) * BM;
+        }
+    };
+
+    const int tiles = units * cols * parts, last = tiles % G, idle = last ? G - last : 0;
+    const int p = vid >= last ? vid - last : vid - last + G;
+    bool whole = true;                                                 // units, then halves
+    for (int i = 0;; ++i) {
+        Where w = {0, 0, a.M, a.K, 0, 0, 0, 0, 0, false};
+        int two = -1;                                                  // first of a unit's two halves
+        bool full = false;
+        if (whole) {
+            // groups that split the reduction come by size: a workgroup that had the first of a round has the
+            // last of the next
+            const int t = i * G + (by_k && (i & 1) ? G - 1 - vid : vid);
+            if (i * G >= tiles) {
+                if (!HALF)
+                    break;
+                whole = false;
+                i = -1;
+                continue;
+            }
+            if (t >= tiles)
+                continue;
+            int tm = 0;
+            full = true;
+            if (by_rows) {
+                if constexpr (ROWS) {
+                    const int g = group_of(a.E, t / cols, unit_of), u0 = uniform(unit_of(g));
+                    const int big = min(uniform(s_groups.big[g + 1]) - uniform(s_groups.big[g]), units - u0);
+                    const int in = t - u0 * cols;
+                    full = !HALF || in < big * cols;
+                    if (full) {
+                        tile_of(in, big, cols, tm, w.tn);
+                        in_group(g, w);
+                    } else {
+                        w.tn = in - big * cols;
+                        two = uniform(s_groups.half[g]) - 1;
+                    }
+                }
+            } else {
+                in_part(t, units, tm, w);
+            }
+            w.m0 = (int64_t)tm * BM;
+        } else {
+            // the workgroups that the last round left without a unit take two of the halves first
+            int h = 2 * idle + p + (i - 2) * G;
+            if (i < 2) {
+                if (p >= idle)
+                    continue;
+                h = p + i * idle;
+            }
+            if (h >= halves * cols * parts)
+                break;
+            int hr = 0;
+            if (by_rows) {
+                if constexpr (ROWS) {
+                    hr = h / cols;
+                    w.tn = h - hr * cols;
+                    if (hr == 2 * cut) {
+                        group_half(nh - 1, w);
+                    } else {
+                        const int u = units + hr / 2, g = group_of(a.E, u, unit_of), in = u - uniform(unit_of(g));
+                        if (in < uniform(s_groups.big[g + 1]) - uniform(s_groups.big[g])) {
+                            in_group(g, w);
+                            w.m0 = (int64_t)in * BM + (hr & 1) * (BM / 2);
+                        } else {
+                            group_half(uniform(s_groups.half[g]) - 1 + (hr & 1), w);
+                        }
+                    }
+                }
+            } else {
+                in_part(h, halves, hr, w);
+                w.m0 = (int64_t)units * BM + (int64_t)hr * (BM / 2);
+            }
+        }
+        w.n0 = (int64_t)w.tn * BN;
+        if (full) {
+            product_tile<BM, BN, WM, WN, S, TA, TB, EPI>(a, l, w);
+        } else if constexpr (HALF) {
+            for (int q = 0; q < 2; ++q) {
+                if (two >= 0)
+                    group_half(two + q, w);
+                product_tile<BM / 2, BN, WM, WN, 3, TA, TB, EPI>(a, lh, w);
+                if (two < 0)
+                    break;
+            }
+        }
     }
 }
 

@@ -57,6 +57,36 @@ def test_linear_forward(i, shape):
         assert ok_c() and ok_p()
 
 
+# enough output for the tallest tiles, in whole, cut and partial rounds over the CUs
+LARGE = [(4100, 72, 4360), (2200, 136, 8200), (5000, 64, 6001), (4353, 200, 4090), (300, 64, 33000)]
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(LARGE)))
+def test_linear_forward_and_backward_large(i, shape):
+    M, K, Nc = shape
+    g = gen(150 + i)
+    A, B = normal(g, M, K), normal(g, Nc, K, std=max(K, 1) ** -0.5)
+    for act, with_bias, with_res in (("none", False, False), (ACTS[1 + i % 4], True, i % 2 == 0)):
+        print("linear large", shape, act, flush=True)
+        bias = normal(g, Nc) if with_bias else None
+        res = normal(g, M, Nc) if with_res else None
+        C, ok_c = guarded(M, Nc)
+        pre, ok_p = guarded(M, Nc)
+        ag.gemm_bias_act(A, B, bias=bias, act=act, residual=res, C=C, pre=pre if with_bias else None)
+        y, y_off, p, p_off = ref.linear(A, B, bias, act, res)
+        ref.near(C, y, y_off, "C")
+        if with_bias:
+            ref.near(pre, p, p_off, "pre")
+        assert ok_c() and ok_p()
+    # the products of the backward pass with M, K and Nc in turn as their large output
+    for m, k, n in ((M, Nc // 8 * 8, K), (K, Nc // 8 * 8, M)):
+        print("linear bwd large", m, k, n, flush=True)
+        A, B, dC = normal(g, m, k), normal(g, n, k, std=0.1), normal(g, m, n)
+        got = ag.gemm_bias_act_bwd(dC, A, B)
+        for name, t, (want, off) in zip(("dA", "dB", "dbias"), got, ref.linear_bwd(dC, A, B, "none", None)):
+            ref.near(t, want, off, name)
+
+
 def test_linear_residual_in_place():
     g = gen(3)
     A, B, C = normal(g, 70, 256), normal(g, 200, 256, std=0.06), normal(g, 70, 200)
@@ -104,6 +134,9 @@ GROUPED = [([1], 0, 8, 8), ([0, 0, 3], 2, 64, 40), ([5, 0, 1, 0, 0, 9, 2], 0, 72
            ([2] * 16, 0, 2048, 512), ([33, 1, 0, 200, 31], 7, 136, 264), ([130, 127, 128, 129], 1, 520, 384),
            ([700, 0, 5, 300, 256], 90, 264, 520), ([64, 0, 3, 100] * 80, 11, 64, 72), ([1] * 1024, 3, 64, 16),
            ([900, 257, 256, 255], 0, 0, 48)]
+# enough rows for the tallest tiles, groups that end inside one; weights large enough for the tallest tiles of dB
+GROUPED += [([700, 513, 0, 1200, 130, 2, 128, 384, 640, 1], 33, 136, 2056), ([257] * 12, 0, 72, 1544),
+            ([300, 0, 1, 511, 64, 900, 256], 5, 2056, 1288)]
 
 
 @pytest.mark.parametrize("i,case", list(enumerate(GROUPED)))
