@@ -45,19 +45,49 @@ struct Plan {
     int64_t part_bytes(int64_t M, int64_t N) const { return splits > 1 ? region(splits * M * up(N, 8) * 4) : 0; }
 };
 
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32)
+// Time of one product's tiles, us, by rates measured on this card: a 256 x 256 tile takes 1.6 us for a step of 64
+// and 5 us besides, its half 0.86 and 3.5, a 128 x 128 tile 0.44 and 2.
+double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts)
+{
+    const int64_t n = cus();
+    if (t == kTile128)
+        return (double)((((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n) * (0.44 * steps + 2);
+    const int64_t c = (N + 255) / 256 * parts, units = M / 256 + (M % 256 > 128), lone = M % 256 > 0 && M % 256 <= 128;
+    const double full = 1.6 * steps + 5, half = 0.86 * steps + 3.5;
+    const int64_t rounds = units * c / n, last = units * c % n;
+    const auto halves = [&](int64_t tiles) { return (double)((tiles + n - 1) / n) * half; };
+    double tail = halves(lone * c);
+    if (last > 0)
+        tail = std::min(full + halves(std::max<int64_t>(0, lone * c - 2 * (n - last))), halves(lone * c + 2 * last));
+    return rounds * full + tail;
+}
+
+// The tile and the split that take the least time.  A split product writes and reads its fp32 sums, and joining
+// them is a launch.  (us, 128 x 128 against 256 x 256: 2048 x 2048 x 2048 23 | 31, 1024 x 4096 x 4096 37 | 52,
+// 3000 x 3000 x 3000 100 | 90; 128 x 4096 x 4096 33 in one part, 18.5 in four.)
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32, bool split = true)
 {
     Plan p;
-    const int64_t n = cus();
-    auto tiles = [&](Tile t) { return ((M + tile_m(t) - 1) / tile_m(t)) * ((N + tile_n(t) - 1) / tile_n(t)); };
-    if (rows32 && M <= 32)
+    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64);
+    int64_t parts = 1;
+    if (rows32 && M <= 32) {
         p.tile = kTile32;
-    else
-        p.tile = tiles(kTile256) * 2 >= n ? kTile256 : kTile128;
-    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64), t = std::max<int64_t>(1, tiles(p.tile));
-    const int64_t room = p.tile == kTile128 ? 2 * n : n;
-    int64_t s = std::max<int64_t>(1, std::min(room / t, steps / 4));
-    p.split_steps = (steps + s - 1) / s;
+        if (split)
+            parts = std::max<int64_t>(1, std::min(cus() / std::max<int64_t>(1, (N + 127) / 128), steps / 4));
+    } else {
+        p.tile = kTile128;
+        double best = 1e30;
+        for (const Tile t : {kTile128, kTile256})
+            for (int64_t s = 1; s == 1 || (split && s <= 32 && s * 2 <= steps); ++s) {
+                const double us = tile_time(t, M, N, (steps + s - 1) / s, s) + (s > 1 ? 4 + 8e-6 / 5 * s * M * N : 0);
+                if (us < best) {
+                    best = us;
+                    p.tile = t;
+                    parts = s;
+                }
+            }
+    }
+    p.split_steps = (steps + parts - 1) / parts;
     p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
     return p;
 }
@@ -120,19 +150,19 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     return w;
 }
 
-Tile xent_tile(int64_t T) { return T <= 128 ? kTile128 : kTile256; }
+Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, false, false).tile; }
 
-int64_t stat_pairs(int64_t T, int64_t V)
+int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
 {
     if (T <= kRowsMost)
         return (V + rows_cols(V, T) - 1) / rows_cols(V, T);
-    const Tile t = xent_tile(T);
+    const Tile t = xent_tile(T, V, K);
     return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
 }
 
 hipError_t launch_logits(Epi epi, const TileArgs& a, hipStream_t s)
 {
-    return a.M <= kRowsMost ? launch_rows(epi, a.M, a, s) : launch_nt(xent_tile(a.M), epi, a, s);
+    return a.M <= kRowsMost ? launch_rows(epi, a.M, a, s) : launch_nt(xent_tile(a.M, a.N, a.K), epi, a, s);
 }
 
 struct XentBwd {
@@ -269,11 +299,11 @@ static bool groups_ok(const void* ends, int32_t E, int64_t M, int64_t Nc, int64_
     return shapes_ok(M, Nc, K) && Nc % 8 == 0 && E >= 1 && !bad(ends, 1, 4);
 }
 
-// Tile of the products whose rows are grouped, by the mean rows of a group.
-static Tile group_tile(int64_t M, int32_t E)
+// Tile of the products whose rows are grouped: the large one, whose weights are read half as often, once there
+// are two rounds of it, half of each group's last tile taken as empty.
+static Tile group_tile(int64_t M, int64_t N, int32_t E)
 {
-    const int64_t mean = M / E;
-    return mean <= 32 ? kTile32 : mean < 192 ? kTile128 : kTile256;
+    return (M / 256 + E / 2) * ((N + 255) / 256) >= 2 * cus() ? kTile256 : kTile128;
 }
 
 extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M, int64_t Nc, int64_t K,
@@ -293,7 +323,7 @@ extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, i
     a.group = kGroupRows;
     a.strideB = Nc * K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, E), kEpiLinear, a, s),
+    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, Nc, E), kEpiLinear, a, s),
            "launch gemm_grouped");
     return AG_OK;
 }
@@ -314,7 +344,7 @@ extern "C" int gemm_grouped_bwd(const void* dC, const void* A, const void* B, co
         a.E = E;
         a.group = kGroupRows;
         a.strideB = Nc * K;
-        LM_HIP(launch_nn(group_tile(M, E), a, s), "launch dA");
+        LM_HIP(launch_nn(M / E <= 32 ? kTile32 : group_tile(M, K, E), a, s), "launch dA");
     }
     if (dB && Nc > 0 && K > 0) {
         TileArgs a = product(dC, Nc, A, K, Nc, K, M, dB, K);
@@ -332,7 +362,7 @@ extern "C" int64_t gemm_xent_workspace(int64_t T, int64_t V, int64_t K)
 {
     if (!xent_shapes_ok(T, V, K) || too_large(T, V, K))
         return 0;
-    return region(T * stat_pairs(T, V) * 8) + region(T * 4);
+    return region(T * stat_pairs(T, V, K) * 8) + region(T * 4);
 }
 
 extern "C" int gemm_xent(const void* A, const void* B, const int64_t* targets, int64_t T, int64_t V, int64_t K, float* loss,
@@ -350,7 +380,7 @@ extern "C" int gemm_xent(const void* A, const void* B, const int64_t* targets, i
         return AG_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
     TileArgs a = product(A, K, B, K, T, V, K, nullptr, 0);
-    a.stat_n = stat_pairs(T, V);
+    a.stat_n = stat_pairs(T, V, K);
     a.stat = static_cast<float*>(work);
     a.hit = reinterpret_cast<float*>(static_cast<char*>(work) + region(T * a.stat_n * 8));
     a.targets = targets;
@@ -410,7 +440,7 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         }
         if (dB) {
             a = product(ws, ldd, A, K, n, K, T, static_cast<char*>(dB) + v0 * K * 2, K);
-            const Plan p = plan_product(n, K, T, false);
+            const Plan p = plan_product(n, K, T, false, false);
             LM_HIP(launch_tn(p.tile, a, s), "launch dB");
         }
     }

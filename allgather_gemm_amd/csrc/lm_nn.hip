@@ -10,9 +10,9 @@ __global__ __launch_bounds__(NT, 1) void nn256_kernel(TileArgs a)
     tile_body<256, 256, 2, 2, 2, false, true, kEpiLinear, true>(a);
 }
 
-__global__ __launch_bounds__(NT, 2) void nn128_kernel(TileArgs a)
+__global__ __launch_bounds__(NT, 1) void nn128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 2, false, true, kEpiLinear, false>(a);
+    tile_body<128, 128, 2, 2, 4, false, true, kEpiLinear, false>(a);
 }
 
 __global__ __launch_bounds__(NT, 1) void nn32_kernel(TileArgs a)
@@ -27,7 +27,7 @@ hipError_t launch_nn(Tile t, TileArgs a, hipStream_t stream)
     switch (t) {
     case kTile256: return launch_tiles(nn256_kernel, 128, 256, 1, a, stream);
     case kTile32: return launch_tiles(nn32_kernel, 32, 128, 1, a, stream);
-    default: return launch_tiles(nn128_kernel, 128, 128, 2, a, stream);
+    default: return launch_tiles(nn128_kernel, 128, 128, 1, a, stream);
     }
 }
 

@@ -12,9 +12,9 @@ __global__ __launch_bounds__(NT, 1) void nt256_kernel(TileArgs a)
 }
 
 template <int EPI>
-__global__ __launch_bounds__(NT, 2) void nt128_kernel(TileArgs a)
+__global__ __launch_bounds__(NT, 1) void nt128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 2, false, false, EPI, false>(a);
+    tile_body<128, 128, 2, 2, 4, false, false, EPI, false>(a);
 }
 
 template <int EPI>
@@ -22,7 +22,7 @@ hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 {
     if (t == kTile256)
         return launch_tiles(nt256_kernel<EPI>, 128, 256, 1, a, stream);
-    return launch_tiles(nt128_kernel<EPI>, 128, 128, 2, a, stream);
+    return launch_tiles(nt128_kernel<EPI>, 128, 128, 1, a, stream);
 }
 
 }  // namespace

@@ -931,74 +931,60 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        if constexpr (S == 2 || S == 3) {
-            // A step out of stage c is four substeps; its barrier stands before the last one: there every wave
-            // has read all of stage c's fragments, and the next stage's loads have landed.  The last substep's
-            // MFMAs then cover the first fragment reads of the next step and the first half of the loads that
-            // refill stage c; the other half follows in the next step's first substep.
-            Dma d;
-            auto step = [&](int c) {
-                const int n = (c + 1) % S;
-                block(0, c, 1, d, ND / 2, ND);
-                block(1, c, 2, d, 0, 0);
-                block(0, c, 3, d, 0, 0);
-                wait_vmcnt<(S - 2) * ND>();
-                stage_barrier();
-                d = dma_setup(c);
-                block(1, n, 0, d, 0, ND / 2);
-            };
-            // the start of a tile: its first S - 1 steps into the stages from c on, half of the next one
-            auto start = [&](int c) {
+        // A step out of stage c is four substeps; its barrier stands before the last one: there every wave
+        // has read all of stage c's fragments, and the next stage's loads have landed.  The last substep's
+        // MFMAs then cover the first fragment reads of the next step and the first half of the loads that
+        // refill stage c; the other half follows in the next step's first substep.
+        Dma d;
+        auto step = [&](int c) {
+            const int n = (c + 1) % S;
+            block(0, c, 1, d, ND / 2, ND);
+            block(1, c, 2, d, 0, 0);
+            block(0, c, 3, d, 0, 0);
+            wait_vmcnt<(S - 2) * ND>();
+            stage_barrier();
+            d = dma_setup(c);
+            block(1, n, 0, d, 0, ND / 2);
+        };
+        // the start of a tile: its first S - 1 steps into the stages from c on, half of the next one
+        auto start = [&](int c) {
 #pragma unroll
-                for (int i = 0; i < S - 1; ++i)
-                    issue_all((c + i) % S);
-                wait_vmcnt<(S - 2) * ND>();
-                stage_barrier();
-                d = dma_setup((c + S - 1) % S);
+            for (int i = 0; i < S - 1; ++i)
+                issue_all((c + i) % S);
+            wait_vmcnt<(S - 2) * ND>();
+            stage_barrier();
+            d = dma_setup((c + S - 1) % S);
 #pragma unroll
-                for (int q = 0; q < ND / 2; ++q)
-                    dma_op(d, q);
-                first_frags(c);
-            };
-            int64_t kb = kb0;
-            if constexpr (S == 2) {
-                // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
-                // computes twice per iteration
-                if ((kb1 - kb0) & 1) {
-                    start(1);
-                    step(1);
-                    ++kb;
-                } else if (kb1 > kb0) {
-                    start(0);
-                }
+            for (int q = 0; q < ND / 2; ++q)
+                dma_op(d, q);
+            first_frags(c);
+        };
+        int64_t kb = kb0;
+        if constexpr (S == 2) {
+            // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
+            // computes twice per iteration
+            if ((kb1 - kb0) & 1) {
+                start(1);
+                step(1);
+                ++kb;
             } else if (kb1 > kb0) {
-                start(0);                // steps past the last, up to a multiple of three, multiply zeros
+                start(0);
             }
-            for (; kb < kb1; kb += S) {
+        } else if (kb1 > kb0) {
+            start(0);
+        }
+        for (; kb + S <= kb1; kb += S) {
 #pragma unroll
-                for (int c = 0; c < S; ++c)
-                    step(c);
-            }
-        } else {
-            // four stages: the loads of three steps are in flight while one is computed
-            auto compute = [&](int c, const Dma& d) {
-                first_frags(c);
-                block(0, c, 1, d, 0, ND / 2);
-                block(1, c, 2, d, ND / 2, ND);
-                block(0, c, 3, d, 0, 0);
-                block(1, c, -1, d, 0, 0);
-            };
-            issue_all(0);
-            issue_all(1);
-            issue_all(2);
-            for (int64_t kb = kb0; kb < kb1; kb += 4) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (kb + c >= kb1)
-                        break;
-                    wait_vmcnt<2 * ND>();
-                    stage_barrier();
-                    compute(c, dma_setup((c + 3) % 4));
+            for (int c = 0; c < S; ++c)
+                step(c);
+        }
+        if constexpr (S > 2) {               // what is left, out of the first stages
+            if (kb < kb1) {
+                step(0);
+                if (kb + 1 < kb1) {
+                    step(1);
+                    if (S > 3 && kb + 2 < kb1)
+                        step(2);
                 }
             }
         }
@@ -1100,12 +1086,13 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     l.a[1] = {sA1, sA1 + AB / 2};
     l.b[1] = {sB1, sB1 + 16384};
     if constexpr (S == 4) {
-        static_assert(4 * SLAB <= BB, "slabs fit a stage of B");
+
         l.a[2].lo = sA2;
         l.b[2] = {sB2, sB2 + 16384};
         l.a[3].lo = sA3;
         l.b[3] = {sB3, sB3 + 16384};
-        l.slab = sB0 + wave * SLAB;
+        static_assert(2 * SLAB <= BB, "slabs fit two stages of B");
+        l.slab = (wave < 2 ? sB0 : sB1) + (wave & 1) * SLAB;
     } else {
         static_assert(HALF ? SLAB == HALF_A : 2 * SLAB <= AB && 2 * SLAB <= BB, "slabs fit a stage");
         l.slab = wave >= 2 ? sB0 + (wave - 2) * SLAB : !HALF ? sA0 + wave * SLAB : wave ? sU0 : sA0;

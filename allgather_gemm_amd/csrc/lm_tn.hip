@@ -10,9 +10,9 @@ __global__ __launch_bounds__(NT, 1) void tn256_kernel(TileArgs a)
     tile_body<256, 256, 2, 2, 2, true, true, kEpiLinear, true>(a);
 }
 
-__global__ __launch_bounds__(NT, 2) void tn128_kernel(TileArgs a)
+__global__ __launch_bounds__(NT, 1) void tn128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 2, true, true, kEpiLinear, false>(a);
+    tile_body<128, 128, 2, 2, 4, true, true, kEpiLinear, false>(a);
 }
 
 }  // namespace
@@ -21,7 +21,7 @@ hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream)
 {
     switch (t) {
     case kTile256: return launch_tiles(tn256_kernel, 128, 256, 1, a, stream);
-    default: return launch_tiles(tn128_kernel, 128, 128, 2, a, stream);
+    default: return launch_tiles(tn128_kernel, 128, 128, 1, a, stream);
     }
 }
 
