@@ -46,12 +46,15 @@ struct Plan {
 };
 
 // Time of one product's tiles, us, by rates measured on this card: a 256 x 256 tile takes 1.6 us for a step of 64
-// and 5 us besides, its half 0.86 and 3.5, a 128 x 128 tile 0.44 and 2.
+// and 5 us besides, its half 0.86 and 3.5, a 128 x 128 tile 0.44 and 2 (a fifth more once there is more than
+// a round of them, for it reads twice as much per product out of the caches).
 double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts)
 {
     const int64_t n = cus();
-    if (t == kTile128)
-        return (double)((((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n) * (0.44 * steps + 2);
+    if (t == kTile128) {
+        const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n;
+        return (double)rounds * (0.44 * steps + 2) * (rounds > 1 ? 1.2 : 1.0);
+    }
     const int64_t c = (N + 255) / 256 * parts, units = M / 256 + (M % 256 > 128), lone = M % 256 > 0 && M % 256 <= 128;
     const double full = 1.6 * steps + 5, half = 0.86 * steps + 3.5;
     const int64_t rounds = units * c / n, last = units * c % n;
