@@ -308,12 +308,12 @@ def _need(t, name: str, shape: tuple, dtype=torch.bfloat16, device=None):
     """Checks a tensor argument; returns its device pointer (None for an absent one)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and (device is None or t.device == device):
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s %s, not %s %s" % (name, shape, dtype, tuple(t.shape), t.dtype))
     _check_dev(t, name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, device))
-    return t.data_ptr()
+    raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, device))
 
 
 def _dims(t, name: str, n: int):
@@ -327,23 +327,27 @@ class _on:
     handed to other work before the call's kernels are done with them."""
 
     def __init__(self, stream, device):
-        self.device = device
+        self.guard = torch.cuda.device(device)
         self.ctx = None if stream is None else torch.cuda.stream(stream)
-        self.guard = None
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
+        self.guard.__enter__()
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+def _elsewhere(stream, device) -> bool:
+    """Whether a call needs another stream or device than the current one (it then enters _on and starts over)."""
+    return stream is not None or (device.type == "cuda" and device.index != torch._C._cuda_getDevice())
+
+
+def _stream_of(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -375,15 +379,17 @@ def gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = 
     M, K = _dims(A, "A", 2)
     Nc = _dims(B, "B", 2)[0]
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_bias_act(A, B, bias, act, residual, C, pre)
     a, b = _need(A, "A", (M, K)), _need(B, "B", (Nc, K), device=dev)
     bi, r = _need(bias, "bias", (Nc,), device=dev), _need(residual, "residual", (M, Nc), device=dev)
     pr = _need(pre, "pre", (M, Nc), device=dev)
-    with _on(stream, dev) as s:
-        if C is None:
-            C = torch.empty((M, Nc), dtype=torch.bfloat16, device=dev)
-        c = _need(C, "C", (M, Nc), device=dev)
-        w, n = _work("gemm_bias_act", dev, M, Nc, K)
-        _done(lib().gemm_bias_act(a, b, bi, r, M, Nc, K, _ACTS[act], c, pr, _p(w), n, s), "gemm_bias_act")
+    if C is None:
+        C = A.new_empty((M, Nc))
+    c = _need(C, "C", (M, Nc), device=dev)
+    w, n = _work("gemm_bias_act", dev, M, Nc, K)
+    _done(lib().gemm_bias_act(a, b, bi, r, M, Nc, K, _ACTS[act], c, pr, _p(w), n, _stream_of(dev)), "gemm_bias_act")
     return C
 
 
@@ -395,18 +401,20 @@ def gemm_bias_act_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, act: s
     M, K = _dims(A, "A", 2)
     Nc = _dims(B, "B", 2)[0]
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_bias_act_bwd(dC, A, B, act, pre, need_dA, need_dB, need_dbias)
     d, a = _need(dC, "dC", (M, Nc), device=dev), _need(A, "A", (M, K))
     b, pr = _need(B, "B", (Nc, K), device=dev), _need(pre, "pre", (M, Nc), device=dev)
     code = _ACTS[act]
     if code != ACT_NONE and pre is None:
         raise ValueError("act %r needs pre" % act)
-    with _on(stream, dev) as s:
-        dA = torch.empty_like(A) if need_dA else None
-        dB = torch.empty_like(B) if need_dB else None
-        dbias = torch.empty((Nc,), dtype=torch.bfloat16, device=dev) if need_dbias else None
-        w, n = _work("gemm_bias_act_bwd", dev, M, Nc, K, code)
-        _done(lib().gemm_bias_act_bwd(d, a, b, pr, M, Nc, K, code, _p(dA), _p(dB), _p(dbias), _p(w), n, s),
-              "gemm_bias_act_bwd")
+    dA = torch.empty_like(A) if need_dA else None
+    dB = torch.empty_like(B) if need_dB else None
+    dbias = A.new_empty((Nc,)) if need_dbias else None
+    w, n = _work("gemm_bias_act_bwd", dev, M, Nc, K, code)
+    _done(lib().gemm_bias_act_bwd(d, a, b, pr, M, Nc, K, code, _p(dA), _p(dB), _p(dbias), _p(w), n, _stream_of(dev)),
+          "gemm_bias_act_bwd")
     return dA, dB, dbias
 
 
@@ -418,13 +426,15 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, C: torch.
     M, K = _dims(A, "A", 2)
     E, Nc, _ = _dims(B, "B", 3)
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_grouped(A, B, ends, C)
     a, b = _need(A, "A", (M, K)), _need(B, "B", (E, Nc, K), device=dev)
     en = _need(ends, "ends", (E,), torch.int32, dev)
-    with _on(stream, dev) as s:
-        if C is None:
-            C = torch.empty((M, Nc), dtype=torch.bfloat16, device=dev)
-        c = _need(C, "C", (M, Nc), device=dev)
-        _done(lib().gemm_grouped(a, b, en, E, M, Nc, K, c, s), "gemm_grouped")
+    if C is None:
+        C = A.new_empty((M, Nc))
+    c = _need(C, "C", (M, Nc), device=dev)
+    _done(lib().gemm_grouped(a, b, en, E, M, Nc, K, c, _stream_of(dev)), "gemm_grouped")
     return C
 
 
@@ -434,12 +444,14 @@ def gemm_grouped_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ends: t
     M, K = _dims(A, "A", 2)
     E, Nc, _ = _dims(B, "B", 3)
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_grouped_bwd(dC, A, B, ends, need_dA, need_dB)
     d, a = _need(dC, "dC", (M, Nc), device=dev), _need(A, "A", (M, K))
     b, en = _need(B, "B", (E, Nc, K), device=dev), _need(ends, "ends", (E,), torch.int32, dev)
-    with _on(stream, dev) as s:
-        dA = torch.empty_like(A) if need_dA else None
-        dB = torch.empty_like(B) if need_dB else None
-        _done(lib().gemm_grouped_bwd(d, a, b, en, E, M, Nc, K, _p(dA), _p(dB), s), "gemm_grouped_bwd")
+    dA = torch.empty_like(A) if need_dA else None
+    dB = torch.empty_like(B) if need_dB else None
+    _done(lib().gemm_grouped_bwd(d, a, b, en, E, M, Nc, K, _p(dA), _p(dB), _stream_of(dev)), "gemm_grouped_bwd")
     return dA, dB
 
 
@@ -450,13 +462,15 @@ def gemm_xent(A: torch.Tensor, B: torch.Tensor, targets: torch.Tensor, stream=No
     T, K = _dims(A, "A", 2)
     V = _dims(B, "B", 2)[0]
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_xent(A, B, targets)
     a, b = _need(A, "A", (T, K)), _need(B, "B", (V, K), device=dev)
     y = _need(targets, "targets", (T,), torch.int64, dev)
-    with _on(stream, dev) as s:
-        loss = torch.empty((T,), dtype=torch.float32, device=dev)
-        lse = torch.empty((T,), dtype=torch.float32, device=dev)
-        w, n = _work("gemm_xent", dev, T, V, K)
-        _done(lib().gemm_xent(a, b, y, T, V, K, loss.data_ptr(), lse.data_ptr(), _p(w), n, s), "gemm_xent")
+    loss = torch.empty((T,), dtype=torch.float32, device=dev)
+    lse = torch.empty((T,), dtype=torch.float32, device=dev)
+    w, n = _work("gemm_xent", dev, T, V, K)
+    _done(lib().gemm_xent(a, b, y, T, V, K, loss.data_ptr(), lse.data_ptr(), _p(w), n, _stream_of(dev)), "gemm_xent")
     return loss, lse
 
 
@@ -468,18 +482,20 @@ def gemm_xent_bwd(dloss: torch.Tensor, A: torch.Tensor, B: torch.Tensor, targets
     T, K = _dims(A, "A", 2)
     V = _dims(B, "B", 2)[0]
     dev = A.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return gemm_xent_bwd(dloss, A, B, targets, lse, need_dA, need_dB, work_bytes)
     a, b = _need(A, "A", (T, K)), _need(B, "B", (V, K), device=dev)
     y, g = _need(targets, "targets", (T,), torch.int64, dev), _need(dloss, "dloss", (T,), torch.float32, dev)
     ls = _need(lse, "lse", (T,), torch.float32, dev)
-    with _on(stream, dev) as s:
-        dA = torch.empty_like(A) if need_dA else None
-        dB = torch.empty_like(B) if need_dB else None
-        if work_bytes is None:
-            w, n = _work("gemm_xent_bwd", dev, T, V, K)
-        else:
-            n = work_bytes
-            w = torch.empty(n, dtype=torch.uint8, device=dev)
-        _done(lib().gemm_xent_bwd(g, a, b, y, ls, T, V, K, _p(dA), _p(dB), _p(w), n, s), "gemm_xent_bwd")
+    dA = torch.empty_like(A) if need_dA else None
+    dB = torch.empty_like(B) if need_dB else None
+    if work_bytes is None:
+        w, n = _work("gemm_xent_bwd", dev, T, V, K)
+    else:
+        n = work_bytes
+        w = torch.empty(n, dtype=torch.uint8, device=dev)
+    _done(lib().gemm_xent_bwd(g, a, b, y, ls, T, V, K, _p(dA), _p(dB), _p(w), n, _stream_of(dev)), "gemm_xent_bwd")
     return dA, dB
 
 

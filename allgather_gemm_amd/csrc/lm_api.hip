@@ -29,7 +29,7 @@ bool bad(const void* p, int64_t elements, uintptr_t n = 16) { return (elements >
 int64_t up(int64_t x, int64_t n) { return (x + n - 1) / n * n; }
 int64_t region(int64_t bytes) { return up(bytes, 256); }
 
-int cus()
+int64_t cus()
 {
     int n = 0;
     if (device_cus(&n) != hipSuccess || n <= 0)
@@ -48,9 +48,8 @@ struct Plan {
 // Time of one product's tiles, us, by rates measured on this card: a 256 x 256 tile takes 1.6 us for a step of 64
 // and 5 us besides, its half 0.86 and 3.5, a 128 x 128 tile 0.44 and 2 (a fifth more once there is more than
 // a round of them, for it reads twice as much per product out of the caches).
-double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts)
+double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int64_t n)
 {
-    const int64_t n = cus();
     if (t == kTile128) {
         const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n;
         return (double)rounds * (0.44 * steps + 2) * (rounds > 1 ? 1.2 : 1.0);
@@ -71,18 +70,20 @@ double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts)
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32, bool split = true)
 {
     Plan p;
-    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64);
+    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64), n = cus();
     int64_t parts = 1;
     if (rows32 && M <= 32) {
         p.tile = kTile32;
         if (split)
-            parts = std::max<int64_t>(1, std::min(cus() / std::max<int64_t>(1, (N + 127) / 128), steps / 4));
+            parts = std::max<int64_t>(1, std::min(n / std::max<int64_t>(1, (N + 127) / 128), steps / 4));
     } else {
         p.tile = kTile128;
         double best = 1e30;
         for (const Tile t : {kTile128, kTile256})
-            for (int64_t s = 1; s == 1 || (split && s <= 32 && s * 2 <= steps); ++s) {
-                const double us = tile_time(t, M, N, (steps + s - 1) / s, s) + (s > 1 ? 4 + 8e-6 / 5 * s * M * N : 0);
+            for (const int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+                if (s > 1 && (!split || s * 2 > steps))
+                    break;
+                const double us = tile_time(t, M, N, (steps + s - 1) / s, s, n) + (s > 1 ? 4 + 8e-6 / 5 * s * M * N : 0);
                 if (us < best) {
                     best = us;
                     p.tile = t;
@@ -237,7 +238,9 @@ extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, con
         return AG_EINVAL;
     if (too_large(M, Nc, K))
         return AG_EUNSUPPORTED;
-    const int64_t need = gemm_bias_act_workspace(M, Nc, K);
+    const bool few = M <= kRowsMost;
+    const Plan p = few ? Plan() : plan_product(M, Nc, K, false);
+    const int64_t need = few ? 0 : p.part_bytes(M, Nc);
     if (work_bytes < need || bad(work, need))
         return AG_EINVAL;
     TileArgs a = product(A, K, B, K, M, Nc, K, C, Nc);
@@ -246,9 +249,7 @@ extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, con
     a.out.pre = static_cast<__bf16*>(pre);
     a.out.act = act;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    LM_HIP(M <= kRowsMost ? launch_rows(kEpiLinear, M, a, s)
-                          : run_product(nt_linear, plan_product(M, Nc, K, false), a, work, s),
-           "launch gemm_bias_act");
+    LM_HIP(few ? launch_rows(kEpiLinear, M, a, s) : run_product(nt_linear, p, a, work, s), "launch gemm_bias_act");
     return AG_OK;
 }
 
