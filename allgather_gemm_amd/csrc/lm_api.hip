@@ -109,7 +109,6 @@ TileArgs product(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t
     a.K = K;
     a.k_valid = K;
     a.splits = 1;
-    a.vec = ldc % 8 == 0;
     a.out.C = static_cast<__bf16*>(C);
     a.out.ldc = ldc;
     return a;
@@ -127,7 +126,7 @@ hipError_t run_product(Launch launch, const Plan& p, TileArgs a, void* part, hip
     }
     hipError_t e = launch(p.tile, a, s);
     if (e == hipSuccess && p.splits > 1)
-        e = launch_join(a.part, p.splits, a.M, a.N, a.ldp, a.out, a.vec, s);
+        e = launch_join(a.part, p.splits, a.M, a.N, a.ldp, a.out, s);
     return e;
 }
 
@@ -452,7 +451,7 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         LinearOut out = {};
         out.C = static_cast<__bf16*>(dA);
         out.ldc = K;
-        LM_HIP(launch_join(part, w.da.splits, T, K, K, out, true, s), "launch dA join");
+        LM_HIP(launch_join(part, w.da.splits, T, K, K, out, s), "launch dA join");
     }
     return AG_OK;
 }

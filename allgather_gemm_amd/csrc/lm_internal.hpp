@@ -45,8 +45,8 @@ struct TileArgs {
     float* part;
     int64_t ldp;             // multiple of 8
     int accumulate;          // add to part instead of writing it
-    bool vec;                // rows of C, pre and residual start at 16-byte boundaries
     LinearOut out;
+    int plain;               // nothing follows the sums but their rounding into out.C (filled in at the launch)
     // softmax statistics of each row's columns: stat[row][stat_n][2] = (maximum, sum of exponentials)
     float* stat;
     int64_t stat_n;
@@ -72,7 +72,7 @@ hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream);
 
 // out = epilogue of the sum over splits of part[s][row][col]
 hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
-                       bool vec, hipStream_t stream);
+                       hipStream_t stream);
 
 // d (M, ldd) = dC act'(pre), columns [N, ldd) zero (d may be null); colsum: null or fp32
 // [colsum_rows(M)][N] partial column sums of the unrounded products

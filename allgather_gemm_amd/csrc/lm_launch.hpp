@@ -15,6 +15,7 @@ template <typename Kernel>
 hipError_t launch_tiles(Kernel kernel, int bm, int bn, int per_cu, TileArgs& a, hipStream_t stream)
 {
     a.tiles_n = (a.N + bn - 1) / bn;
+    a.plain = !(a.part || a.out.bias || a.out.pre || a.out.residual || a.out.act != kActNone);
     int cus = 0;
     hipError_t e = device_cus(&cus);
     if (e != hipSuccess)

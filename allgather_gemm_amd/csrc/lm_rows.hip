@@ -73,12 +73,7 @@ __device__ __forceinline__ void finish8(const TileArgs& a, int64_t mrow, bool va
     } else if constexpr (EPI == kEpiGrad) {
         grad8(a, mrow, a.M, col, n, x);
     } else if (valid && n > 0) {
-        float b[8] = {}, res[8] = {};
-        if (a.out.bias)
-            load8(a.out.bias + col, n, a.vec, b);
-        if (a.out.residual)
-            load8(a.out.residual + mrow * a.out.ldc + col, n, a.vec, res);
-        linear8(a.out, mrow, col, n, a.vec, x, b, res);
+        linear8(a.out, mrow, col, n, x);
     }
 }
 

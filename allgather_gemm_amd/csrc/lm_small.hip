@@ -15,7 +15,7 @@ namespace {
 // theirs), so that enough loads are in flight: 64 splits of 33 x 1024 took 20 us with L = 1.
 template <int L>
 __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits, int64_t M, int64_t N, int64_t ldp,
-                                                  LinearOut out, bool vec)
+                                                  LinearOut out)
 {
     constexpr int U = NT / L;                      // units of a workgroup
     __shared__ f32x4 s_sum[L > 1 ? L - 1 : 1][U][2];
@@ -52,19 +52,14 @@ __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits,
     const int n = (int)min((int64_t)8, N - col);
     if (!there || n <= 0)
         return;
-    float b[8] = {}, r[8] = {};
-    if (out.bias)
-        load8(out.bias + col, n, vec, b);
-    if (out.residual)
-        load8(out.residual + row * out.ldc + col, n, vec, r);
-    linear8(out, row, col, n, vec, x, b, r);
+    linear8(out, row, col, n, x);
 }
 
 constexpr int COLS = 256;      // columns of a workgroup of act_bwd_kernel: 32 lanes of 8
 
 // d = dC act'(pre), rounded to bf16 for the two products; its column sums from the unrounded values.
 __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N,
-                                                     int64_t chunk, __bf16* d, int64_t ldd, float* colsum, bool vec)
+                                                     int64_t chunk, __bf16* d, int64_t ldd, float* colsum)
 {
     __shared__ float s_sum[8][COLS + 8];
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -72,25 +67,30 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
     const int64_t r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
     const int n = (int)max((int64_t)0, min((int64_t)8, N - col));
     float sum[8] = {};
-    for (int64_t row = r0 + rl; row < r1; row += 8) {
-        float x[8];
-        load8(dC + row * N + col, n, vec, x);
-        if (act != kActNone) {
-            float z[8];
-            load8(pre + row * N + col, n, vec, z);
-            act_slope8(x, z, act);
-        }
-        if (d && col < ldd) {
-            bf16x8 o;
+    auto rows = [&](auto load) {
+        for (int64_t row = r0 + rl; row < r1; row += 8) {
+            float x[8], z[8];
+            load(dC + row * N + col, x);
+            if (act != kActNone) {
+                load(pre + row * N + col, z);
+                act_slope8(x, z, act);
+            }
+            if (d && col < ldd) {
+                bf16x8 o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = (__bf16)x[e];
+                *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = (__bf16)x[e];
-            *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+                sum[e] += x[e];
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum[e] += x[e];
-    }
+    };
+    if (n < 8)
+        rows([&](const __bf16* p, float* x) { load8(p, n, x); });
+    else
+        rows([](const __bf16* p, float* x) { load8(p, 8, x); });
     if (!colsum)
         return;
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(NT) void xent_join_kernel(const float* stat, int64_
 
 }  // namespace
 
-hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out, bool vec,
+hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
                        hipStream_t stream)
 {
     const int64_t units = M * (ldp / 8);
@@ -188,11 +188,11 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
     const int L = splits >= 32 && units < 16384 ? 16 : splits >= 8 && units < 65536 ? 4 : 1;
     const dim3 grid((unsigned)((units * L + NT - 1) / NT));
     if (L == 16)
-        join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+        join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
     else if (L == 4)
-        join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+        join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
     else
-        join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, vec);
+        join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
     return hipGetLastError();
 }
 
@@ -207,7 +207,7 @@ hipError_t launch_act_bwd(const __bf16* dC, const __bf16* pre, int act, int64_t 
     if (M <= 0 || N <= 0)
         return hipSuccess;
     const dim3 grid((unsigned)((N + COLS - 1) / COLS), (unsigned)colsum_rows(M));
-    act_bwd_kernel<<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum, N % 8 == 0);
+    act_bwd_kernel<<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum);
     return hipGetLastError();
 }
 

@@ -281,63 +281,76 @@ __device__ __forceinline__ void act_slope8(float* x, const float* z, int act)
     }
 }
 
-// Eight consecutive bf16 of row `row`, columns [col, col + 8) with `n` of them valid.
-__device__ __forceinline__ bf16x8 load8_raw(const __bf16* p, int n, bool vec)
+// Sixteen bytes at any element: rows of an odd length start anywhere, and the memory takes them so.
+typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+
+// Eight consecutive bf16, `n` of them valid.  Less than eight come one by one, all at a time: the loads are not
+// left out past the last but repeat it.
+__device__ __forceinline__ bf16x8 load8_few(const __bf16* p, int n)
 {
     bf16x8 v = {};
-    if (vec && n >= 8)
-        return *reinterpret_cast<const bf16x8*>(p);
+    if (n > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n)
-            v[e] = p[e];
+        for (int e = 0; e < 8; ++e)
+            v[e] = p[min(e, n - 1)];
+    }
     return v;
 }
 
-__device__ __forceinline__ void load8(const __bf16* p, int n, bool vec, float* x)
+__device__ __forceinline__ void load8(const __bf16* p, int n, float* x)
 {
-    const bf16x8 v = load8_raw(p, n, vec);
+    const bf16x8 v = n >= 8 ? *reinterpret_cast<const bf16x8_any*>(p) : load8_few(p, n);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        x[e] = (float)v[e];
+        x[e] = e < n ? (float)v[e] : 0.0f;
 }
 
-__device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float* x)
+__device__ __forceinline__ void store8(__bf16* p, const float* x)
 {
     bf16x8 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         o[e] = (__bf16)x[e];
-    if (vec && n >= 8) {
-        __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(p));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n)
-                p[e] = o[e];
-    }
+    __builtin_nontemporal_store(o, reinterpret_cast<bf16x8_any*>(p));
 }
 
-// act(x + bias) + residual of eight columns, stored; `pre` gets x + bias.  b and r: the eight columns of
-// bias and residual, loaded before.
-__device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t col, int n, bool vec, float* x,
-                                        const float* b, const float* r)
+__device__ __forceinline__ void store8(__bf16* p, int n, const float* x)
 {
-    if (o.bias) {
+    if (n >= 8)
+        return store8(p, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] += b[e];
-    }
-    const int64_t at = row * o.ldc + col;
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            p[e] = (__bf16)x[e];
+}
+
+// act(x + bias) + residual of eight columns into C; `pre` gets x + bias.  b and r: the eight columns of bias and
+// residual (zeros without), at: the place of the first in pre.
+__device__ __forceinline__ void finish_linear8(const LinearOut& o, __bf16* C, int64_t at, int n, float* x, const float* b,
+                                               const float* r)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] += b[e];
     if (o.pre)
-        store8(o.pre + at, n, vec, x);
+        store8(o.pre + at, n, x);
     act_value8(x, o.act);
-    if (o.residual) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] += r[e];
-    }
-    store8(o.C + at, n, vec, x);
+    for (int e = 0; e < 8; ++e)
+        x[e] += r[e];
+    store8(C, n, x);
+}
+
+__device__ __forceinline__ void linear8(const LinearOut& o, int64_t row, int64_t col, int n, float* x)
+{
+    const int64_t at = row * o.ldc + col;
+    float b[8] = {}, r[8] = {};
+    if (o.bias)
+        load8(o.bias + col, n, b);
+    if (o.residual)
+        load8(o.residual + at, n, r);
+    finish_linear8(o, o.C + at, at, n, x, b, r);
 }
 
 // ------------------------------------------------------------------------------------- groups
@@ -611,8 +624,8 @@ __device__ __forceinline__ bf16x4* half_slab_at(char* slab, int j, int q, uint32
     return reinterpret_cast<bf16x4*>(slab + fr * RB + (fh ^ (fr >> 4)) * 8 + (((uint32_t)(j * 4 + q) ^ (fr & (UN - 1))) * 16));
 }
 
-// The slab to memory in 16-byte pieces; p: the block's first element, rows, cols: what is valid of it (cols a
-// multiple of 8, rows start at 16-byte boundaries).  PAST: the stores pass the tiles' lines in L2 by.
+// The slab to memory in 16-byte pieces; p: the block's first element, rows, cols: what is valid of it.  PAST: the
+// stores pass the tiles' lines in L2 by (16384 x 14336 x 4096 takes 5 % more without).
 template <int FN, bool PAST>
 __device__ __forceinline__ void half_slab_out(const char* slab, __bf16* p, int64_t ld, int64_t rows, int64_t cols, int lane)
 {
@@ -622,17 +635,37 @@ __device__ __forceinline__ void half_slab_out(const char* slab, __bf16* p, int64
     __builtin_amdgcn_wave_barrier();
     const uint32_t u = lane % UN, r0 = lane / UN;
     p += r0 * ld + u * 8;
-#pragma unroll
-    for (int it = 0; it < 32 / RPI; ++it) {
+    auto row_of = [&](int it) {
         const uint32_t r = it * RPI + r0;
         const i32x4 x = *reinterpret_cast<const i32x4*>(slab + r * RB + ((u ^ (r & (UN - 1))) * 16));
-        const i32x4 y = it * RPI >= 16 ? i32x4{x[2], x[3], x[0], x[1]} : x;   // RPI divides 16
-        if (r < rows && u * 8 < cols) {
-            i32x4* const out = reinterpret_cast<i32x4*>(p + it * RPI * ld);
-            if (PAST)
-                __builtin_nontemporal_store(y, out);
-            else
-                *out = y;
+        return it * RPI >= 16 ? i32x4{x[2], x[3], x[0], x[1]} : x;   // RPI divides 16
+    };
+    if (cols >= FN * 32) {
+#pragma unroll
+        for (int it = 0; it < 32 / RPI; ++it) {
+            const i32x4 y = row_of(it);
+            i32x4_any* const out = reinterpret_cast<i32x4_any*>(p + it * RPI * ld);
+            if (it * RPI + r0 < rows) {
+                if (PAST)
+                    __builtin_nontemporal_store(y, out);
+                else
+                    *out = y;
+            }
+        }
+    } else {                                               // the last columns
+#pragma unroll 2
+        for (int it = 0; it < 32 / RPI; ++it) {
+            const bf16x8 y = __builtin_bit_cast(bf16x8, row_of(it));
+            const int n = (int)cols - (int)u * 8;
+            if (it * RPI + r0 < rows) {
+                if (n >= 8)
+                    *reinterpret_cast<bf16x8_any*>(p + it * RPI * ld) = y;
+                else
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (e < n)
+                            p[it * RPI * ld + e] = y[e];
+            }
         }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
@@ -688,16 +721,22 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
     const uint32_t fr = lane & 31, fh = lane >> 5;
     const uint32_t c8 = (lane % LPR) * 8;
     const int r0 = lane / LPR, n = min(8, cols - (int)c8);
-    const bool residual = a.out.residual && !part;
+    const bool edge = cols < WNC, residual = a.out.residual && !part;      // edge: some lanes have less than eight
     at += r0 * ldc + c8;
     C += r0 * ldc + c8;
     // the slab's residual is on its way while the slab is written
     bf16x8 res[ITS] = {};
-    if (residual && a.vec) {
+    if (residual && (!edge || n >= 8)) {
 #pragma unroll
         for (int it = 0; it < ITS; ++it)
-            if (r0 + it * RSTEP < rows && n >= 8)
-                res[it] = *reinterpret_cast<const bf16x8*>(a.out.residual + at + it * RSTEP * ldc);
+            if (r0 + it * RSTEP < rows)
+                res[it] = *reinterpret_cast<const bf16x8_any*>(a.out.residual + at + it * RSTEP * ldc);
+    }
+    if (residual && edge && n < 8) {
+#pragma unroll
+        for (int it = 0; it < ITS; ++it)
+            if (r0 + it * RSTEP < rows)
+                res[it] = load8_few(a.out.residual + at + it * RSTEP * ldc, n);
     }
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -729,49 +768,53 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
             }
         }
     } else {
-        if (between) {
-            // bias, pre and the activation in a loop of their own: unrolled into the stores below, the
-            // activations would be there once for each row of the block
+        // bias, pre and the activation in a loop of their own: unrolled into the stores below, the activations
+        // would be there once for each row of the block
+        auto activate = [&](int it, auto store_pre) {
+            const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+            float x[8] = {x0[0] + bias[0], x0[1] + bias[1], x0[2] + bias[2], x0[3] + bias[3],
+                          x1[0] + bias[4], x1[1] + bias[5], x1[2] + bias[6], x1[3] + bias[7]};
+            if (a.out.pre && r0 + it * RSTEP < rows)
+                store_pre(a.out.pre + at + it * RSTEP * ldc, x);
+            act_value8(x, a.out.act);
+            if (residual || edge) {
+                *unit(it, 0) = f32x4{x[0], x[1], x[2], x[3]};
+                *unit(it, 1) = f32x4{x[4], x[5], x[6], x[7]};
+            } else if (r0 + it * RSTEP < rows) {
+                store8(C + it * RSTEP * ldc, x);
+            }
+        };
+        if (between && edge) {
+#pragma unroll 1
+            for (int it = 0; it < ITS; ++it)
+                activate(it, [&](__bf16* p, const float* x) { store8(p, n, x); });
+        } else if (between) {
 #pragma unroll 2
+            for (int it = 0; it < ITS; ++it)
+                activate(it, [&](__bf16* p, const float* x) { store8(p, x); });
+        }
+        if (residual) {
+#pragma unroll
             for (int it = 0; it < ITS; ++it) {
-                const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                float x[8] = {x0[0] + bias[0], x0[1] + bias[1], x0[2] + bias[2], x0[3] + bias[3],
-                              x1[0] + bias[4], x1[1] + bias[5], x1[2] + bias[6], x1[3] + bias[7]};
-                const bool in = r0 + it * RSTEP < rows && n > 0;
-                if (a.out.pre && in)
-                    store8(a.out.pre + at + it * RSTEP * ldc, n, a.vec, x);
-                act_value8(x, a.out.act);
-                if (residual) {
-                    *unit(it, 0) = f32x4{x[0], x[1], x[2], x[3]};
-                    *unit(it, 1) = f32x4{x[4], x[5], x[6], x[7]};
-                } else if (in) {
-                    store8(C + it * RSTEP * ldc, n, a.vec, x);
+                f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                x0 += f32x4{(float)res[it][0], (float)res[it][1], (float)res[it][2], (float)res[it][3]};
+                x1 += f32x4{(float)res[it][4], (float)res[it][5], (float)res[it][6], (float)res[it][7]};
+                if (edge) {
+                    *unit(it, 0) = x0;
+                    *unit(it, 1) = x1;
+                } else if (r0 + it * RSTEP < rows) {
+                    const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+                    store8(C + it * RSTEP * ldc, x);
                 }
             }
         }
-        if (a.vec && (residual || !between)) {
-#pragma unroll
-            for (int it = 0; it < ITS; ++it) {
-                const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
-                bf16x8 o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    o[e] = (__bf16)((e < 4 ? x0[e & 3] : x1[e & 3]) + (residual ? (float)res[it][e] : 0.0f));
-                if (r0 + it * RSTEP < rows && n >= 8)
-                    __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(C + it * RSTEP * ldc));
-            }
-        } else if (residual || !between) {
+        if (edge) {
 #pragma unroll 1
             for (int it = 0; it < ITS; ++it) {
                 const f32x4 x0 = *unit(it, 0), x1 = *unit(it, 1);
+                const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
                 if (r0 + it * RSTEP < rows)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < n) {
-                            const float x = e < 4 ? x0[e & 3] : x1[e & 3];
-                            C[it * RSTEP * ldc + e] =
-                                (__bf16)(residual ? x + (float)a.out.residual[at + it * RSTEP * ldc + e] : x);
-                        }
+                    store8(C + it * RSTEP * ldc, n, x);
             }
         }
     }
@@ -1017,13 +1060,13 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
             __bf16* const C = a.out.C + (a.group == kGroupK ? g * a.M * ldc : 0) + at;
             float* const part = a.part ? a.part + (split * a.M + mrow0) * ldp + wcol : nullptr;
             const bool between = a.out.bias || a.out.pre || a.out.act != kActNone;
-            int plain = !(a.part || between || a.out.residual || !a.vec);
             float bias[8] = {};
             const int c8 = (el % (WNC / 8)) * 8, n = min(8, wcols - c8);
             if (a.out.bias && n > 0)
-                load8(a.out.bias + wcol + c8, n, a.vec, bias);
+                load8(a.out.bias + wcol + c8, n, bias);
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
+                int plain = a.plain;
                 one_block(acc[i], el, plain);
                 if (plain) {
 #pragma unroll
