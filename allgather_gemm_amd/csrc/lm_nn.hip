@@ -7,17 +7,17 @@ namespace {
 
 __global__ __launch_bounds__(NT, 1) void nn256_kernel(TileArgs a)
 {
-    tile_body<256, 256, 2, 2, 2, false, true, kEpiLinear, true>(a);
+    tile_body<256, 256, 2, 2, 2, false, true, kEpiSum, true>(a);
 }
 
 __global__ __launch_bounds__(NT, 1) void nn128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 4, false, true, kEpiLinear, false>(a);
+    tile_body<128, 128, 2, 2, 4, false, true, kEpiSum, false>(a);
 }
 
 __global__ __launch_bounds__(NT, 1) void nn32_kernel(TileArgs a)
 {
-    tile_body<32, 128, 1, 4, 4, false, true, kEpiLinear, false>(a);
+    tile_body<32, 128, 1, 4, 4, false, true, kEpiSum, false>(a);
 }
 
 }  // namespace

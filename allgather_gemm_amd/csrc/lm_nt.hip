@@ -38,8 +38,12 @@ hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream)
         a.stat_n = (a.N + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
         return launch<kEpiStat>(t, a, stream);
     case kEpiGrad: return launch<kEpiGrad>(t, a, stream);
-    default: return launch<kEpiLinear>(t, a, stream);
+    default: break;
     }
+    // a kernel of its own without what may follow the sums
+    const LinearOut& o = a.out;
+    const bool sum = a.splits > 1 || !(o.bias || o.pre || o.residual || o.act != kActNone);
+    return sum ? launch<kEpiSum>(t, a, stream) : launch<kEpiLinear>(t, a, stream);
 }
 
 }  // namespace lm

@@ -180,6 +180,16 @@ struct Frag {
     }
 };
 
+// f(0), ..., f(N - 1) with compile-time arguments
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        each<N, I + 1>(f);
+    }
+}
+
 // ------------------------------------------------------------------------------- activations
 // Values and slopes in fp32.  exp goes through exp2 (one hardware instruction); its relative error,
 // a few 2^-24 times the argument's size, is far below the bf16 rounding of the result.
@@ -707,10 +717,10 @@ __device__ __forceinline__ void grad_block(const TileArgs& a, const f32x16* acc,
 
 // act(x + bias) + residual of the same block, x in the accumulators, through the wave's LDS slab (32 rows of
 // 128 FN bytes of fp32, 16-byte units swizzled by the row); or x itself into `part` where the reduction is
-// split.  A row's eight columns come back to one lane.  part and C: the block's first row and column; at: the
+// split (all that there is without ACT).  A row's eight columns come back to one lane.  part and C: the block's first row and column; at: the
 // same place in residual and pre; rows, cols: what is valid of the block.
-template <int FN>
-__device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* acc, char* slab, __bf16* C, float* part,
+template <int FN, bool ACT, typename Fill>
+__device__ __forceinline__ void linear_block(const TileArgs& a, Fill fill, char* slab, __bf16* C, float* part,
                                              int64_t at, int64_t ldc, int64_t ldp, int rows, int cols, const float* bias,
                                              bool between, int lane)
 {
@@ -721,7 +731,7 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
     const uint32_t fr = lane & 31, fh = lane >> 5;
     const uint32_t c8 = (lane % LPR) * 8;
     const int r0 = lane / LPR, n = min(8, cols - (int)c8);
-    const bool edge = cols < WNC, residual = a.out.residual && !part;      // edge: some lanes have less than eight
+    const bool edge = cols < WNC, residual = ACT && a.out.residual && !part;      // edge: some lanes have less than eight
     at += r0 * ldc + c8;
     C += r0 * ldc + c8;
     // the slab's residual is on its way while the slab is written
@@ -738,14 +748,16 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
             if (r0 + it * RSTEP < rows)
                 res[it] = load8_few(a.out.residual + at + it * RSTEP * ldc, n);
     }
+    fill([&](const f32x16* acc) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t colb = (j * 32 + q * 8 + fh * 4) * 4;
-            const f32x4 v4 = {acc[j][q * 4 + 0], acc[j][q * 4 + 1], acc[j][q * 4 + 2], acc[j][q * 4 + 3]};
-            *reinterpret_cast<f32x4*>(slab + fr * (WNC * 4) + (colb ^ ((fr & SW) << 4))) = v4;
-        }
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t colb = (j * 32 + q * 8 + fh * 4) * 4;
+                const f32x4 v4 = {acc[j][q * 4 + 0], acc[j][q * 4 + 1], acc[j][q * 4 + 2], acc[j][q * 4 + 3]};
+                *reinterpret_cast<f32x4*>(slab + fr * (WNC * 4) + (colb ^ ((fr & SW) << 4))) = v4;
+            }
+    });
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
     __builtin_amdgcn_wave_barrier();
     auto unit = [&](int it, int half) {   // four of this lane's eight columns in its row it
@@ -767,7 +779,7 @@ __device__ __forceinline__ void linear_block(const TileArgs& a, const f32x16* ac
                 pv[1] = x1;
             }
         }
-    } else {
+    } else if constexpr (ACT) {
         // bias, pre and the activation in a loop of their own: unrolled into the stores below, the activations
         // would be there once for each row of the block
         auto activate = [&](int it, auto store_pre) {
@@ -838,7 +850,8 @@ struct Where {
     bool zero;                                         // rows past the last group
 };
 
-// One tile.  EPI: kEpiLinear, kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
+// One tile.  EPI: kEpiLinear, kEpiSum (the sums alone: a kernel without the activations' code
+// takes 37 us instead of 41 for 16384 x 4096 x 8), kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
 __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>& l, const Where& w)
 {
@@ -848,6 +861,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
     typedef Side<BN, TB> SB;
     constexpr int ND = SA::OPS + SB::OPS;
     constexpr int WNC = FN * 32;                       // columns of a wave's block
+    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -890,7 +904,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
         const uint32_t fr = lane & 31;
         int64_t target[FM];
         float row_lse[FM], row_w[FM];
-        if constexpr (EPI != kEpiLinear) {
+        if constexpr (!LIN) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int64_t mrow = min(m0 + (i * WM + wm) * 32 + fr, M - 1);
@@ -1054,7 +1068,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
         asm volatile("" : "+v"(el), "+s"(ldc), "+s"(ldp));
         const int64_t wcol = n0 + wn * WNC;                            // the wave's first column
         const int wcols = (int)max((int64_t)0, min((int64_t)WNC, a.N - wcol));
-        if constexpr (EPI == kEpiLinear) {
+        if constexpr (LIN) {
             const int64_t mrow0 = m0 + wm * 32;                        // blocks WM x 32 rows apart
             const int64_t at = (grow0 + mrow0) * ldc + wcol;
             __bf16* const C = a.out.C + (a.group == kGroupK ? g * a.M * ldc : 0) + at;
@@ -1062,13 +1076,13 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
             const bool between = a.out.bias || a.out.pre || a.out.act != kActNone;
             float bias[8] = {};
             const int c8 = (el % (WNC / 8)) * 8, n = min(8, wcols - c8);
-            if (a.out.bias && n > 0)
+            if (EPI == kEpiLinear && a.out.bias && n > 0)
                 load8(a.out.bias + wcol + c8, n, bias);
+            if (a.plain) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                int plain = a.plain;
-                one_block(acc[i], el, plain);
-                if (plain) {
+                for (int i = 0; i < FM; ++i) {
+                    int cols = wcols;
+                    one_block(acc[i], el, cols);
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -1076,11 +1090,29 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
                             *half_slab_at<FN>(slab, j, q, el & 31, (uint32_t)el >> 5) =
                                 bf16x4{(__bf16)acc[i][j][q * 4 + 0], (__bf16)acc[i][j][q * 4 + 1],
                                        (__bf16)acc[i][j][q * 4 + 2], (__bf16)acc[i][j][q * 4 + 3]};
-                    half_slab_out<FN, true>(slab, C + i * WM * 32 * ldc, ldc, M - mrow0 - i * WM * 32, wcols, el);
-                } else {
-                    linear_block<FN>(a, acc[i], slab, C + i * WM * 32 * ldc, part ? part + i * WM * 32 * ldp : nullptr,
-                                     at + i * WM * 32 * ldc, ldc, ldp, (int)max((int64_t)0, min((int64_t)32, M - mrow0 - i * WM * 32)),
-                                     wcols, bias, between, el);
+                    half_slab_out<FN, true>(slab, C + i * WM * 32 * ldc, ldc, M - mrow0 - i * WM * 32, cols, el);
+                }
+            } else {
+                // a loop at run time, in which only the accumulators' way into the slab is there for each block:
+                // the waves of a CU go through this code one tile at a time, and what the instruction cache does
+                // not hold they wait for (four copies: silu 5 % more time at 8192 x 8192 x 2048)
+#pragma unroll 1
+                for (int i = 0; i < FM; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    auto fill = [&](auto write) {
+                        each<FM>([&](auto index) {
+                            constexpr int I = decltype(index)::value;
+                            if (i == I) {
+                                int flag = 0;
+                                one_block(acc[I], el, flag);
+                                write(acc[I]);
+                            }
+                        });
+                    };
+                    linear_block<FN, EPI == kEpiLinear>(
+                        a, fill, slab, C + i * WM * 32 * ldc, part ? part + i * WM * 32 * ldp : nullptr,
+                        at + i * WM * 32 * ldc, ldc, ldp, (int)max((int64_t)0, min((int64_t)32, M - mrow0 - i * WM * 32)),
+                        wcols, bias, between, el);
                 }
             }
         } else {
@@ -1148,7 +1180,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     lh.b[1] = l.b[1];
     lh.b[2] = l.a[1];
     lh.slab = l.slab;
-    constexpr bool ROWS = EPI == kEpiLinear && !TA, KS = EPI == kEpiLinear && TA;   // groups there can be
+    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum, ROWS = LIN && !TA, KS = LIN && TA;   // groups there can be
     __shared__ typename std::conditional<ROWS, Groups, typename std::conditional<KS, KGroups, int>::type>::type s_groups;
 
     const int G = gridDim.x;

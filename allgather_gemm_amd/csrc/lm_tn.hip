@@ -7,12 +7,12 @@ namespace {
 
 __global__ __launch_bounds__(NT, 1) void tn256_kernel(TileArgs a)
 {
-    tile_body<256, 256, 2, 2, 2, true, true, kEpiLinear, true>(a);
+    tile_body<256, 256, 2, 2, 2, true, true, kEpiSum, true>(a);
 }
 
 __global__ __launch_bounds__(NT, 1) void tn128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 4, true, true, kEpiLinear, false>(a);
+    tile_body<128, 128, 2, 2, 4, true, true, kEpiSum, false>(a);
 }
 
 }  // namespace
