@@ -46,16 +46,16 @@ struct Plan {
 };
 
 // Time of one product's tiles, us, by rates measured on this card: a 256 x 256 tile takes 1.6 us for a step of 64
-// and 5 us besides, its half 0.86 and 3.5, a 128 x 128 tile 0.44 and 2 (a fifth more once there is more than
+// and 6 us besides, its half 0.86 and 4, a 128 x 128 tile 0.44 and 3 (a fifth more once there is more than
 // a round of them, for it reads twice as much per product out of the caches).
 double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int64_t n)
 {
     if (t == kTile128) {
         const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n;
-        return (double)rounds * (0.44 * steps + 2) * (rounds > 1 ? 1.2 : 1.0);
+        return (double)rounds * (0.44 * steps + 3) * (rounds > 1 ? 1.2 : 1.0);
     }
     const int64_t c = (N + 255) / 256 * parts, units = M / 256 + (M % 256 > 128), lone = M % 256 > 0 && M % 256 <= 128;
-    const double full = 1.6 * steps + 5, half = 0.86 * steps + 3.5;
+    const double full = 1.6 * steps + 6, half = 0.86 * steps + 4;
     const int64_t rounds = units * c / n, last = units * c % n;
     const auto halves = [&](int64_t tiles) { return (double)((tiles + n - 1) / n) * half; };
     double tail = halves(lone * c);
@@ -148,24 +148,37 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     w.da = plan_product(M, K, w.ldd, true);
     w.db = plan_product(Nc, K, M, false);
     w.d_bytes = w.own_d ? region(M * w.ldd * 2) : 0;
-    w.sum_bytes = region(colsum_rows(M) * Nc * 4);
+    w.sum_bytes = colsum_rows(M) > 1 ? region(colsum_rows(M) * Nc * 4) : 0;
     w.part_bytes = std::max(w.da.part_bytes(M, K), w.db.part_bytes(Nc, K));
     return w;
+}
+
+// Whether the logits of T rows are for the few-rows kernel: up to kRowsMost always, and more of them where the
+// 128 x 128 tiles are so few that its 64 x 64 ones, two a CU and 0.38 us a step of 64, are done before.
+bool few_rows(int64_t T, int64_t V, int64_t K)
+{
+    if (T <= kRowsMost)
+        return true;
+    const int64_t steps = (K + 63) / 64, n = cus(), tiles = (T + kRowsMost - 1) / kRowsMost * ((V + 63) / 64);
+    return T <= 1024 && rows_cols(V, kRowsMost) == 64 &&
+           (double)((tiles + 2 * n - 1) / (2 * n)) * (0.38 * steps + 3) < tile_time(kTile128, T, V, steps, 1, n);
 }
 
 Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, false, false).tile; }
 
 int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
 {
-    if (T <= kRowsMost)
-        return (V + rows_cols(V, T) - 1) / rows_cols(V, T);
+    if (few_rows(T, V, K)) {
+        const int cols = rows_cols(V, std::min<int64_t>(T, kRowsMost));
+        return (V + cols - 1) / cols;
+    }
     const Tile t = xent_tile(T, V, K);
     return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
 }
 
 hipError_t launch_logits(Epi epi, const TileArgs& a, hipStream_t s)
 {
-    return a.M <= kRowsMost ? launch_rows(epi, a.M, a, s) : launch_nt(xent_tile(a.M, a.N, a.K), epi, a, s);
+    return few_rows(a.M, a.N, a.K) ? launch_rows(epi, std::min<int64_t>(a.M, kRowsMost), a, s) : launch_nt(xent_tile(a.M, a.N, a.K), epi, a, s);
 }
 
 struct XentBwd {
@@ -283,9 +296,10 @@ extern "C" int gemm_bias_act_bwd(const void* dC, const void* A, const void* B, c
         d = ws;
     if (want_d || dbias)
         LM_HIP(launch_act_bwd(static_cast<const __bf16*>(dC), static_cast<const __bf16*>(pre), act, M, Nc,
-                              want_d ? reinterpret_cast<__bf16*>(ws) : nullptr, w.ldd, dbias ? sum : nullptr, s),
+                              want_d ? reinterpret_cast<__bf16*>(ws) : nullptr, w.ldd, dbias ? sum : nullptr,
+                              static_cast<__bf16*>(dbias), s),
                "launch act_bwd");
-    if (dbias)
+    if (dbias && colsum_rows(M) != 1)
         LM_HIP(launch_colsum_join(sum, colsum_rows(M), Nc, static_cast<__bf16*>(dbias), s), "launch colsum_join");
     if (dA) {
         TileArgs a = product(d, w.ldd, B, K, M, K, w.ldd, dA, K);
@@ -302,11 +316,13 @@ static bool groups_ok(const void* ends, int32_t E, int64_t M, int64_t Nc, int64_
     return shapes_ok(M, Nc, K) && Nc % 8 == 0 && E >= 1 && !bad(ends, 1, 4);
 }
 
-// Tile of the products whose rows are grouped: the large one, whose weights are read half as often, once there
-// are two rounds of it, half of each group's last tile taken as empty.
-static Tile group_tile(int64_t M, int64_t N, int32_t E)
+// Tile of the products whose rows are grouped, a quarter of a large tile for each group's end taken as empty (only the
+// device knows the groups).  The large one from a round of it on: before that its halves, two of which make a unit,
+// leave CUs empty (1041 rows in 4 groups, 3528 x 416: 19 us against 11).
+static Tile group_tile(int64_t M, int64_t N, int64_t K, int32_t E)
 {
-    return (M / 256 + E / 2) * ((N + 255) / 256) >= 2 * cus() ? kTile256 : kTile128;
+    const int64_t rows = M + 64 * (int64_t)E;
+    return rows / 256 * ((N + 255) / 256) < cus() ? kTile128 : plan_product(rows, N, K, false, false).tile;
 }
 
 extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M, int64_t Nc, int64_t K,
@@ -326,7 +342,7 @@ extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, i
     a.group = kGroupRows;
     a.strideB = Nc * K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, Nc, E), kEpiLinear, a, s),
+    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, Nc, K, E), kEpiLinear, a, s),
            "launch gemm_grouped");
     return AG_OK;
 }
@@ -347,7 +363,7 @@ extern "C" int gemm_grouped_bwd(const void* dC, const void* A, const void* B, co
         a.E = E;
         a.group = kGroupRows;
         a.strideB = Nc * K;
-        LM_HIP(launch_nn(M / E <= 32 ? kTile32 : group_tile(M, K, E), a, s), "launch dA");
+        LM_HIP(launch_nn(M / E <= 32 ? kTile32 : group_tile(M, K, Nc, E), a, s), "launch dA");
     }
     if (dB && Nc > 0 && K > 0) {
         TileArgs a = product(dC, Nc, A, K, Nc, K, M, dB, K);

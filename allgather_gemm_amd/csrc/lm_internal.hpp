@@ -74,11 +74,11 @@ hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream);
 hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
                        hipStream_t stream);
 
-// d (M, ldd) = dC act'(pre), columns [N, ldd) zero (d may be null); colsum: null or fp32
-// [colsum_rows(M)][N] partial column sums of the unrounded products
+// d (M, ldd) = dC act'(pre), columns [N, ldd) zero (d may be null); dbias: null, or with colsum_rows(M) == 1 the
+// column sums of the unrounded products, with more colsum gets [colsum_rows(M)][N] partial ones in fp32
 int64_t colsum_rows(int64_t M);
 hipError_t launch_act_bwd(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N, __bf16* d, int64_t ldd,
-                          float* colsum, hipStream_t stream);
+                          float* colsum, __bf16* dbias, hipStream_t stream);
 hipError_t launch_colsum_join(const float* colsum, int64_t rows, int64_t N, __bf16* out, hipStream_t stream);
 
 // lse and loss of each row from its statistics

@@ -299,6 +299,10 @@ template <int FM, int EPI>
 hipError_t launch(bool wide, const TileArgs& a, hipStream_t stream)
 {
     constexpr int BM = FM * 16, D = FM > 2 ? 4 : FM == 2 ? 6 : 8;
+    int cus = 0;
+    hipError_t e = device_cus(&cus);
+    if (e != hipSuccess)
+        return e;
     const int bn = wide ? 64 : 16;
     const int64_t tiles_n = (a.N + bn - 1) / bn;
     int64_t tiles_m = (a.M + BM - 1) / BM;
@@ -310,8 +314,10 @@ hipError_t launch(bool wide, const TileArgs& a, hipStream_t stream)
     const dim3 grid((unsigned)tiles_n, (unsigned)tiles_m);
     if (wide)
         rows_wide_kernel<FM, EPI><<<grid, dim3(NT), 0, stream>>>(a);
-    else
+    else if (tiles_n * tiles_m <= cus)
         rows_kernel<FM, D, EPI><<<grid, dim3(W * 64), 0, stream>>>(a);
+    else        // a ring of half a CU's LDS: the workgroups past the first round start with it, not after it
+        rows_kernel<FM, 4, EPI><<<grid, dim3(W * 64), 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -59,7 +59,8 @@ constexpr int COLS = 256;      // columns of a workgroup of act_bwd_kernel: 32 l
 
 // d = dC act'(pre), rounded to bf16 for the two products; its column sums from the unrounded values.
 __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N,
-                                                     int64_t chunk, __bf16* d, int64_t ldd, float* colsum)
+                                                     int64_t chunk, __bf16* d, int64_t ldd, float* colsum,
+                                                     __bf16* dbias)
 {
     __shared__ float s_sum[8][COLS + 8];
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -67,31 +68,42 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
     const int64_t r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
     const int n = (int)max((int64_t)0, min((int64_t)8, N - col));
     float sum[8] = {};
+    // four rows of a thread at a time, their loads ahead of what is computed of the first
     auto rows = [&](auto load) {
-        for (int64_t row = r0 + rl; row < r1; row += 8) {
-            float x[8], z[8];
-            load(dC + row * N + col, x);
-            if (act != kActNone) {
-                load(pre + row * N + col, z);
-                act_slope8(x, z, act);
+        for (int64_t row0 = r0 + rl; row0 < r1; row0 += 32) {
+            float x[4][8], z[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = min(row0 + i * 8, r1 - 1);
+                load(dC + row * N + col, x[i]);
+                if (act != kActNone)
+                    load(pre + row * N + col, z[i]);
             }
-            if (d && col < ldd) {
-                bf16x8 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = row0 + i * 8;
+                if (row >= r1)
+                    break;
+                if (act != kActNone)
+                    act_slope8(x[i], z[i], act);
+                if (d && col < ldd) {
+                    bf16x8 o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = (__bf16)x[i][e];
+                    *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    o[e] = (__bf16)x[e];
-                *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+                    sum[e] += x[i][e];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum[e] += x[e];
         }
     };
     if (n < 8)
         rows([&](const __bf16* p, float* x) { load8(p, n, x); });
     else
         rows([](const __bf16* p, float* x) { load8(p, 8, x); });
-    if (!colsum)
+    if (!dbias)
         return;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -103,7 +115,10 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             s += s_sum[r][threadIdx.x];
-        colsum[blockIdx.y * N + c] = s;
+        if (gridDim.y == 1)
+            dbias[c] = (__bf16)s;
+        else
+            colsum[blockIdx.y * N + c] = s;
     }
 }
 
@@ -196,18 +211,19 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
     return hipGetLastError();
 }
 
-// Rows of one workgroup: a multiple of its 8 row lanes, at most 128 workgroups down the rows.
-static int64_t act_chunk(int64_t M) { return std::max<int64_t>(32, ((M + 127) / 128 + 7) / 8 * 8); }
+// Rows of one workgroup: a multiple of its 8 row lanes, at most 128 workgroups down the rows; one for few rows,
+// whose sums then need no joining.
+static int64_t act_chunk(int64_t M) { return std::max<int64_t>(M <= 64 ? 64 : 32, ((M + 127) / 128 + 7) / 8 * 8); }
 
 int64_t colsum_rows(int64_t M) { return (M + act_chunk(M) - 1) / act_chunk(M); }
 
 hipError_t launch_act_bwd(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N, __bf16* d, int64_t ldd,
-                          float* colsum, hipStream_t stream)
+                          float* colsum, __bf16* dbias, hipStream_t stream)
 {
     if (M <= 0 || N <= 0)
         return hipSuccess;
     const dim3 grid((unsigned)((N + COLS - 1) / COLS), (unsigned)colsum_rows(M));
-    act_bwd_kernel<<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum);
+    act_bwd_kernel<<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum, dbias);
     return hipGetLastError();
 }
 
