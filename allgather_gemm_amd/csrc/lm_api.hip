@@ -64,8 +64,8 @@ double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int
     return rounds * full + tail;
 }
 
-// The tile and the split that take the least time.  A split product writes and reads its fp32 sums, and joining
-// them is a launch.  (us, 128 x 128 against 256 x 256: 2048 x 2048 x 2048 23 | 31, 1024 x 4096 x 4096 37 | 52,
+// The tile and the split that take the least time.  A split product writes and reads its fp32 sums, at
+// 2 TB/s, and joining them is a launch.  (us, 128 x 128 against 256 x 256: 2048 x 2048 x 2048 23 | 31, 1024 x 4096 x 4096 37 | 52,
 // 3000 x 3000 x 3000 100 | 90; 128 x 4096 x 4096 33 in one part, 18.5 in four.)
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32, bool split = true)
 {
@@ -83,7 +83,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32, bool split = tru
             for (const int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
                 if (s > 1 && (!split || s * 2 > steps))
                     break;
-                const double us = tile_time(t, M, N, (steps + s - 1) / s, s, n) + (s > 1 ? 4 + 8e-6 / 5 * s * M * N : 0);
+                const double us = tile_time(t, M, N, (steps + s - 1) / s, s, n) + (s > 1 ? 4 + 4e-6 * s * M * N : 0);
                 if (us < best) {
                     best = us;
                     p.tile = t;
