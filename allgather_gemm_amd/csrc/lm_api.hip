@@ -45,17 +45,30 @@ struct Plan {
     int64_t part_bytes(int64_t M, int64_t N) const { return splits > 1 ? region(splits * M * up(N, 8) * 4) : 0; }
 };
 
-// Time of one product's tiles, us, by rates measured on this card: a 256 x 256 tile takes 1.6 us for a step of 64
-// and 6 us besides, its half 0.86 and 4, a 128 x 128 tile 0.44 and 3 (a fifth more once there is more than
-// a round of them, for it reads twice as much per product out of the caches).
-double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int64_t n)
+// What follows a product's sums, for the time that it adds to a tile.
+enum After { kSum = 0, kStatistics = 1, kActivation = 2 };
+
+// Time of one product's tiles, us, by rates measured on this card.  A 256 x 256 tile takes 1.6 us for a step of 64
+// and 6 us besides, its half 0.9 and 4, a 128 x 128 tile 0.44 and 3 (a fifth more once there is more than a round of
+// them, for it reads twice as much per product out of the caches).  Short tiles, four a CU at a time, take 0.49 and 1
+// each (0.6 where there are fewer), but 0.94 a step for one that is alone.  What follows the sums is the more
+// expensive the fewer workgroups a CU has to cover it.  (us, large | short tiles: 16384 x 4096 x 512 81 | 81, with
+// gelu 144 | 120; 16384 x 4096 x 128 46 | 36, 104 | 76; 8192 x 8192 x 1024 129 | 140, 191 | 174; 128 x 128 | short:
+// 2048 x 2048 x 2048 22 | 36.)
+double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int64_t n, After after)
 {
-    if (t == kTile128) {
-        const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) * parts + n - 1) / n;
-        return (double)rounds * (0.44 * steps + 3) * (rounds > 1 ? 1.2 : 1.0);
+    static const double kAfter[3][4] = {{0, 0, 0, 0}, {3, 1.6, 1.5, 0.3}, {12, 6.5, 3.5, 2.4}};
+    const double* const more = kAfter[after];
+    if (t == kTile128 || t == kTileShort) {
+        const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128) * parts;
+        if (t == kTile128)
+            return (double)((tiles + n - 1) / n) * (0.44 * steps + 3 + more[2]) * (tiles > n ? 1.2 : 1.0);
+        const double each = 0.49 * steps + 1 + more[3], fours = (double)(tiles / (4 * n) * 4);
+        const double rest = (double)tiles / n - fours;
+        return fours * each + (rest > 0 ? std::max(0.94 * steps + 3, rest * (each + 0.11 * steps)) : 0);
     }
     const int64_t c = (N + 255) / 256 * parts, units = M / 256 + (M % 256 > 128), lone = M % 256 > 0 && M % 256 <= 128;
-    const double full = 1.6 * steps + 6, half = 0.86 * steps + 4;
+    const double full = 1.6 * steps + 6 + more[0], half = 0.9 * steps + 4 + more[1];
     const int64_t rounds = units * c / n, last = units * c % n;
     const auto halves = [&](int64_t tiles) { return (double)((tiles + n - 1) / n) * half; };
     double tail = halves(lone * c);
@@ -64,33 +77,52 @@ double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int
     return rounds * full + tail;
 }
 
-// The tile and the split that take the least time.  A split product writes and reads its fp32 sums, at
-// 2 TB/s, and joining them is a launch.  (us, 128 x 128 against 256 x 256: 2048 x 2048 x 2048 23 | 31, 1024 x 4096 x 4096 37 | 52,
+// The tile and the split that take the least time.  A split product writes and reads its fp32 sums, at 2.7 TB/s, and
+// joining them is a launch.  (us, 128 x 128 against 256 x 256: 2048 x 2048 x 2048 23 | 31, 1024 x 4096 x 4096 37 | 52,
 // 3000 x 3000 x 3000 100 | 90; 128 x 4096 x 4096 33 in one part, 18.5 in four.)
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool rows32, bool split = true)
+Plan plan_product(int64_t M, int64_t N, int64_t K, After after, bool split = true, bool grouped = false)
 {
     Plan p;
     const int64_t steps = std::max<int64_t>(1, (K + 63) / 64), n = cus();
     int64_t parts = 1;
-    if (rows32 && M <= 32) {
-        p.tile = kTile32;
-        if (split)
-            parts = std::max<int64_t>(1, std::min(n / std::max<int64_t>(1, (N + 127) / 128), steps / 4));
-    } else {
-        p.tile = kTile128;
-        double best = 1e30;
-        for (const Tile t : {kTile128, kTile256})
-            for (const int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-                if (s > 1 && (!split || s * 2 > steps))
-                    break;
-                const double us = tile_time(t, M, N, (steps + s - 1) / s, s, n) + (s > 1 ? 4 + 4e-6 * s * M * N : 0);
-                if (us < best) {
-                    best = us;
-                    p.tile = t;
-                    parts = s;
-                }
+    p.tile = kTile128;
+    double best = 1e30;
+    for (const Tile t : {kTile128, kTile256, kTileShort}) {
+        if (t == kTileShort && grouped)
+            break;
+        for (const int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (s > 1 && (!split || t == kTileShort || s * 2 > steps))
+                break;
+            const double us =
+                tile_time(t, M, N, (steps + s - 1) / s, s, n, s > 1 ? kSum : after) + (s > 1 ? 4 + 3e-6 * s * M * N : 0);
+            if (us < best) {
+                best = us;
+                p.tile = t;
+                parts = s;
             }
+        }
     }
+    p.split_steps = (steps + parts - 1) / parts;
+    p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
+    return p;
+}
+
+// A linear layer's: split by its extents alone, which are what its workspace is asked for with.
+Plan plan_linear(int64_t M, int64_t N, int64_t K, After after)
+{
+    const Plan p = plan_product(M, N, K, kSum);
+    return p.splits > 1 || after == kSum ? p : plan_product(M, N, K, after, false);
+}
+
+// The same for X (M, K) times Y (K, N), whose few rows have a tile of 32 rows.
+Plan plan_nn(int64_t M, int64_t N, int64_t K)
+{
+    if (M > 32)
+        return plan_product(M, N, K, kSum);
+    Plan p;
+    p.tile = kTile32;
+    const int64_t steps = std::max<int64_t>(1, (K + 63) / 64);
+    const int64_t parts = std::max<int64_t>(1, std::min(cus() / std::max<int64_t>(1, (N + 127) / 128), steps / 4));
     p.split_steps = (steps + parts - 1) / parts;
     p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
     return p;
@@ -145,8 +177,8 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     LinearBwd w;
     w.own_d = act != kActNone || Nc % 8 != 0;
     w.ldd = up(Nc, 8);
-    w.da = plan_product(M, K, w.ldd, true);
-    w.db = plan_product(Nc, K, M, false);
+    w.da = plan_nn(M, K, w.ldd);
+    w.db = plan_product(Nc, K, M, kSum);
     w.d_bytes = w.own_d ? region(M * w.ldd * 2) : 0;
     w.sum_bytes = colsum_rows(M) > 1 ? region(colsum_rows(M) * Nc * 4) : 0;
     w.part_bytes = std::max(w.da.part_bytes(M, K), w.db.part_bytes(Nc, K));
@@ -161,10 +193,10 @@ bool few_rows(int64_t T, int64_t V, int64_t K)
         return true;
     const int64_t steps = (K + 63) / 64, n = cus(), tiles = (T + kRowsMost - 1) / kRowsMost * ((V + 63) / 64);
     return T <= 1024 && rows_cols(V, kRowsMost) == 64 &&
-           (double)((tiles + 2 * n - 1) / (2 * n)) * (0.38 * steps + 3) < tile_time(kTile128, T, V, steps, 1, n);
+           (double)((tiles + 2 * n - 1) / (2 * n)) * (0.38 * steps + 3) < tile_time(kTile128, T, V, steps, 1, n, kStatistics);
 }
 
-Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, false, false).tile; }
+Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, kStatistics, false).tile; }
 
 int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
 {
@@ -195,7 +227,7 @@ XentBwd plan_xent_bwd(int64_t T, int64_t V, int64_t K, int64_t piece)
     XentBwd w;
     w.piece = piece;
     w.pieces = (V + piece - 1) / piece;
-    w.da = plan_product(T, K, std::min(up(V, 8), piece), true);
+    w.da = plan_nn(T, K, std::min(up(V, 8), piece));
     w.part = w.pieces > 1 || w.da.splits > 1;
     w.part_bytes = w.part ? region((int64_t)w.da.splits * T * K * 4) : 0;
     w.db_part_bytes = 0;
@@ -236,7 +268,7 @@ extern "C" int64_t gemm_bias_act_workspace(int64_t M, int64_t Nc, int64_t K)
 {
     if (!shapes_ok(M, Nc, K) || too_large(M, Nc, K))
         return 0;
-    return M <= kRowsMost ? 0 : plan_product(M, Nc, K, false).part_bytes(M, Nc);
+    return M <= kRowsMost ? 0 : plan_linear(M, Nc, K, kSum).part_bytes(M, Nc);
 }
 
 extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, int64_t M, int64_t Nc,
@@ -251,7 +283,8 @@ extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, con
     if (too_large(M, Nc, K))
         return AG_EUNSUPPORTED;
     const bool few = M <= kRowsMost;
-    const Plan p = few ? Plan() : plan_product(M, Nc, K, false);
+    const Plan p = few ? Plan()
+                       : plan_linear(M, Nc, K, act != kActNone ? kActivation : bias || residual || pre ? kStatistics : kSum);
     const int64_t need = few ? 0 : p.part_bytes(M, Nc);
     if (work_bytes < need || bad(work, need))
         return AG_EINVAL;
@@ -322,7 +355,7 @@ static bool groups_ok(const void* ends, int32_t E, int64_t M, int64_t Nc, int64_
 static Tile group_tile(int64_t M, int64_t N, int64_t K, int32_t E)
 {
     const int64_t rows = M + 64 * (int64_t)E;
-    return rows / 256 * ((N + 255) / 256) < cus() ? kTile128 : plan_product(rows, N, K, false, false).tile;
+    return rows / 256 * ((N + 255) / 256) < cus() ? kTile128 : plan_product(rows, N, K, kSum, false, true).tile;
 }
 
 extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M, int64_t Nc, int64_t K,
@@ -459,7 +492,7 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         }
         if (dB) {
             a = product(ws, ldd, A, K, n, K, T, static_cast<char*>(dB) + v0 * K * 2, K);
-            const Plan p = plan_product(n, K, T, false, false);
+            const Plan p = plan_product(n, K, T, kSum, false);
             LM_HIP(launch_tn(p.tile, a, s), "launch dB");
         }
     }

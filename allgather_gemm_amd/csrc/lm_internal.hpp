@@ -15,7 +15,9 @@ constexpr int kRowsMost = 64;        // rows of X that the few-rows kernel takes
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Group { kGroupNone = 0, kGroupRows = 1, kGroupK = 2 };
 enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3 };
-enum Tile { kTile256 = 0, kTile128 = 1, kTile32 = 2 };
+// kTile128: four stages, one workgroup a CU; kTileShort: 128 x 128 with one stage, a workgroup for each tile and
+// four of them on a CU, no groups
+enum Tile { kTile256 = 0, kTile128 = 1, kTile32 = 2, kTileShort = 3 };
 
 // C = act(sum + bias) + residual, pre = sum + bias (pre, bias, residual may be null)
 struct LinearOut {

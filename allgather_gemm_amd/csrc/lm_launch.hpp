@@ -9,6 +9,8 @@
 namespace ag {
 namespace lm {
 
+constexpr int kEachTile = 1 << 20;             // per_cu: a workgroup for each tile
+
 // Workgroups of a launch: no more than stay resident, each walks the tiles in steps of the grid.  How many
 // tiles groups of rows make only the device knows.
 template <typename Kernel>

@@ -15,6 +15,11 @@ __global__ __launch_bounds__(NT, 1) void nn128_kernel(TileArgs a)
     tile_body<128, 128, 2, 2, 4, false, true, kEpiSum, false>(a);
 }
 
+__global__ __launch_bounds__(NT, 4) void nnshort_kernel(TileArgs a)
+{
+    tile_body<128, 128, 2, 2, 1, false, true, kEpiSum, false>(a);
+}
+
 __global__ __launch_bounds__(NT, 1) void nn32_kernel(TileArgs a)
 {
     tile_body<32, 128, 1, 4, 4, false, true, kEpiSum, false>(a);
@@ -27,6 +32,7 @@ hipError_t launch_nn(Tile t, TileArgs a, hipStream_t stream)
     switch (t) {
     case kTile256: return launch_tiles(nn256_kernel, 128, 256, 1, a, stream);
     case kTile32: return launch_tiles(nn32_kernel, 32, 128, 1, a, stream);
+    case kTileShort: return launch_tiles(nnshort_kernel, 128, 128, kEachTile, a, stream);
     default: return launch_tiles(nn128_kernel, 128, 128, 1, a, stream);
     }
 }

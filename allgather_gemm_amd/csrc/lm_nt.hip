@@ -18,10 +18,18 @@ __global__ __launch_bounds__(NT, 1) void nt128_kernel(TileArgs a)
 }
 
 template <int EPI>
+__global__ __launch_bounds__(NT, EPI == kEpiLinear ? 3 : 4) void ntshort_kernel(TileArgs a)
+{
+    tile_body<128, 128, 2, 2, 1, false, false, EPI, false>(a);
+}
+
+template <int EPI>
 hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 {
     if (t == kTile256)
         return launch_tiles(nt256_kernel<EPI>, 128, 256, 1, a, stream);
+    if (t == kTileShort)
+        return launch_tiles(ntshort_kernel<EPI>, 128, 128, kEachTile, a, stream);
     return launch_tiles(nt128_kernel<EPI>, 128, 128, 1, a, stream);
 }
 

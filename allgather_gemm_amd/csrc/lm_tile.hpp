@@ -988,60 +988,76 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        // A step out of stage c is four substeps; its barrier stands before the last one: there every wave
-        // has read all of stage c's fragments, and the next stage's loads have landed.  The last substep's
-        // MFMAs then cover the first fragment reads of the next step and the first half of the loads that
-        // refill stage c; the other half follows in the next step's first substep.
-        Dma d;
-        auto step = [&](int c) {
-            const int n = (c + 1) % S;
-            block(0, c, 1, d, ND / 2, ND);
-            block(1, c, 2, d, 0, 0);
-            block(0, c, 3, d, 0, 0);
-            wait_vmcnt<(S - 2) * ND>();
-            stage_barrier();
-            d = dma_setup(c);
-            block(1, n, 0, d, 0, ND / 2);
-        };
-        // the start of a tile: its first S - 1 steps into the stages from c on, half of the next one
-        auto start = [&](int c) {
+        if constexpr (S == 1) {
+            // one stage: what is loaded is waited for, while other workgroups of the CU compute and store
+            for (int64_t kb = kb0; kb < kb1; ++kb) {
+                issue_all(0);
+                wait_vmcnt0();
+                stage_barrier();
+                const Dma none = {};
+                first_frags(0);
+                block(0, 0, 1, none, 0, 0);
+                block(1, 0, 2, none, 0, 0);
+                block(0, 0, 3, none, 0, 0);
+                block(1, 0, -1, none, 0, 0);
+                stage_barrier();
+            }
+        } else {
+            // A step out of stage c is four substeps; its barrier stands before the last one: there every wave
+            // has read all of stage c's fragments, and the next stage's loads have landed.  The last substep's
+            // MFMAs then cover the first fragment reads of the next step and the first half of the loads that
+            // refill stage c; the other half follows in the next step's first substep.
+            Dma d;
+            auto step = [&](int c) {
+                const int n = (c + 1) % S;
+                block(0, c, 1, d, ND / 2, ND);
+                block(1, c, 2, d, 0, 0);
+                block(0, c, 3, d, 0, 0);
+                wait_vmcnt<(S - 2) * ND>();
+                stage_barrier();
+                d = dma_setup(c);
+                block(1, n, 0, d, 0, ND / 2);
+            };
+            // the start of a tile: its first S - 1 steps into the stages from c on, half of the next one
+            auto start = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < S - 1; ++i)
-                issue_all((c + i) % S);
-            wait_vmcnt<(S - 2) * ND>();
-            stage_barrier();
-            d = dma_setup((c + S - 1) % S);
+                for (int i = 0; i < S - 1; ++i)
+                    issue_all((c + i) % S);
+                wait_vmcnt<(S - 2) * ND>();
+                stage_barrier();
+                d = dma_setup((c + S - 1) % S);
 #pragma unroll
-            for (int q = 0; q < ND / 2; ++q)
-                dma_op(d, q);
-            first_frags(c);
-        };
-        int64_t kb = kb0;
-        if constexpr (S == 2) {
-            // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
-            // computes twice per iteration
-            if ((kb1 - kb0) & 1) {
-                start(1);
-                step(1);
-                ++kb;
+                for (int q = 0; q < ND / 2; ++q)
+                    dma_op(d, q);
+                first_frags(c);
+            };
+            int64_t kb = kb0;
+            if constexpr (S == 2) {
+                // with an odd number of steps the first runs alone out of stage 1, so the pair loop always
+                // computes twice per iteration
+                if ((kb1 - kb0) & 1) {
+                    start(1);
+                    step(1);
+                    ++kb;
+                } else if (kb1 > kb0) {
+                    start(0);
+                }
             } else if (kb1 > kb0) {
                 start(0);
             }
-        } else if (kb1 > kb0) {
-            start(0);
-        }
-        for (; kb + S <= kb1; kb += S) {
+            for (; kb + S <= kb1; kb += S) {
 #pragma unroll
-            for (int c = 0; c < S; ++c)
-                step(c);
-        }
-        if constexpr (S > 2) {               // what is left, out of the first stages
-            if (kb < kb1) {
-                step(0);
-                if (kb + 1 < kb1) {
-                    step(1);
-                    if (S > 3 && kb + 2 < kb1)
-                        step(2);
+                for (int c = 0; c < S; ++c)
+                    step(c);
+            }
+            if constexpr (S > 2) {               // what is left, out of the first stages
+                if (kb < kb1) {
+                    step(0);
+                    if (kb + 1 < kb1) {
+                        step(1);
+                        if (S > 3 && kb + 2 < kb1)
+                            step(2);
+                    }
                 }
             }
         }
@@ -1147,8 +1163,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     static_assert(!HALF || (AB == 32768 && BB == 32768), "256 x 256");
     __shared__ __attribute__((aligned(1024))) char sA0[HALF ? HALF_A : AB], sU0[HALF ? HALF_A : 16];
     __shared__ __attribute__((aligned(1024))) char sB0[BB];
-    __shared__ __attribute__((aligned(1024))) char sA1[AB];
-    __shared__ __attribute__((aligned(1024))) char sB1[BB];
+    __shared__ __attribute__((aligned(1024))) char sA1[S > 1 ? AB : 16];
+    __shared__ __attribute__((aligned(1024))) char sB1[S > 1 ? BB : 16];
     __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? AB : HALF ? HALF_A : 16];
     __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? BB : 16];
     __shared__ __attribute__((aligned(1024))) char sA3[S > 2 ? AB : 16];
@@ -1158,8 +1174,10 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     Stages<S> l;
     l.a[0] = {sA0, sU0};
     l.b[0] = {sB0, sB0 + 16384};
-    l.a[1] = {sA1, sA1 + AB / 2};
-    l.b[1] = {sB1, sB1 + 16384};
+    if constexpr (S > 1) {
+        l.a[1] = {sA1, sA1 + AB / 2};
+        l.b[1] = {sB1, sB1 + 16384};
+    }
     if constexpr (S == 4) {
 
         l.a[2].lo = sA2;
@@ -1173,14 +1191,16 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         l.slab = wave >= 2 ? sB0 + (wave - 2) * SLAB : !HALF ? sA0 + wave * SLAB : wave ? sU0 : sA0;
     }
     Stages<3> lh;
-    lh.a[0].lo = sA0;
-    lh.a[1].lo = sU0;
-    lh.a[2].lo = sA2;
-    lh.b[0] = l.b[0];
-    lh.b[1] = l.b[1];
-    lh.b[2] = l.a[1];
-    lh.slab = l.slab;
-    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum, ROWS = LIN && !TA, KS = LIN && TA;   // groups there can be
+    if constexpr (HALF) {
+        lh.a[0].lo = sA0;
+        lh.a[1].lo = sU0;
+        lh.a[2].lo = sA2;
+        lh.b[0] = l.b[0];
+        lh.b[1] = l.b[1];
+        lh.b[2] = l.a[1];
+        lh.slab = l.slab;
+    }
+    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum, ROWS = LIN && !TA && S > 1, KS = LIN && TA && S > 1;   // groups there can be
     __shared__ typename std::conditional<ROWS, Groups, typename std::conditional<KS, KGroups, int>::type>::type s_groups;
 
     const int G = gridDim.x;

@@ -15,12 +15,18 @@ __global__ __launch_bounds__(NT, 1) void tn128_kernel(TileArgs a)
     tile_body<128, 128, 2, 2, 4, true, true, kEpiSum, false>(a);
 }
 
+__global__ __launch_bounds__(NT, 4) void tnshort_kernel(TileArgs a)
+{
+    tile_body<128, 128, 2, 2, 1, true, true, kEpiSum, false>(a);
+}
+
 }  // namespace
 
 hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream)
 {
     switch (t) {
     case kTile256: return launch_tiles(tn256_kernel, 128, 256, 1, a, stream);
+    case kTileShort: return launch_tiles(tnshort_kernel, 128, 128, kEachTile, a, stream);
     default: return launch_tiles(tn128_kernel, 128, 128, 1, a, stream);
     }
 }
