@@ -1,6 +1,6 @@
 /*
- * aggemm.h -- C ABI of libaggemm: chunked AllGather fused with a bf16 GEMM, and TGATHER, on one
- * AMD Instinct MI355X (gfx950).
+ * aggemm.h -- C ABI of libaggemm: chunked AllGather fused with a bf16 GEMM, TGATHER, and a language
+ * model's operators around the gathered product, on one AMD Instinct MI355X (gfx950).
  *
  * Pages this library implements:
  *   [AGMM]  "Triton第四课：基于对称内存融合 AllGather 与 MatMul，提速1.56倍" (the fused
@@ -208,8 +208,8 @@ int ag_gemm_noalloc(const void *const *shards, int32_t N, int64_t M, int64_t K, 
  *     are independent, and a call may be captured into a graph.
  *   - Extents of 0 are valid everywhere but V: what remains of the formula is written (K == 0: the
  *     products are zero; a gradient summed over no rows is zero).
- * K % 8 == 0; matrices and bias 16-byte aligned.  K, Nc or V > 2^21 or rows > 2^30 return
- * AG_EUNSUPPORTED. */
+ * K % 8 == 0; matrices and bias 16-byte aligned (rows of Nc or V elements may have any length).  K, Nc
+ * or V > 2^21, rows > 2^30 or more than 2^28 tiles of 128 x 128 in an output return AG_EUNSUPPORTED. */
 
 /* Activations. */
 #define AG_ACT_NONE       0

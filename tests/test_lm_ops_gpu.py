@@ -125,6 +125,36 @@ def test_linear_activation_slope_at_zero_and_far_out():
         assert torch.allclose(got.cpu(), torch.tensor(want, dtype=torch.float64), atol=1e-6), (act, got)
 
 
+def test_offsets_past_32_bits():
+    """Outputs and weights of more than 2^32 bytes: the last rows and the last expert."""
+    g = gen(17)
+    M, K, Nc = 70000, 16, 32776
+    A, B, bias = normal(g, M, K), normal(g, Nc, K), normal(g, Nc)
+    print("linear", M, K, Nc, flush=True)
+    C = ag.gemm_bias_act(A, B, bias=bias, act="relu", residual=None)
+    for rows in (slice(0, 200), slice(65400, 65700), slice(M - 200, M)):
+        y, off, _, _ = ref.linear(A[rows], B, bias, "relu", None)
+        ref.near(C[rows], y, off, "C")
+    print("linear dA", flush=True)
+    dA = ag.gemm_bias_act_bwd(C, A, B, need_dB=False, need_dbias=False)[0]
+    ref.near(dA[-100:], *ref.linear_bwd(C[-100:], A[-100:], B, "none", None)[0], "dA")
+    del C, dA
+    E, K, Nc = 9, 16384, 16384
+    W = torch.zeros(E, Nc, K, dtype=BF16, device="cuda")
+    W[-1] = normal(g, Nc, 8).repeat(1, K // 8)
+    A, dC = normal(g, 40, K), normal(g, 40, Nc)
+    ends = torch.tensor([0, 10, 10, 10, 10, 10, 10, 10, 40], dtype=torch.int32, device="cuda")
+    print("grouped", E, K, Nc, flush=True)
+    got = ag.gemm_grouped(A, W, ends)
+    want, off = ref.product(A[10:].double(), W[-1].double())
+    ref.near(got[10:], want, off * (1 + ref.H) + ref.H * want.abs(), "grouped C")
+    assert not got[:10].any()
+    dW = ag.gemm_grouped_bwd(dC, A, W, ends, need_dA=False)[1]
+    want, off = ref.product(dC[10:].double().t().contiguous(), A[10:].double().t().contiguous())
+    ref.near(dW[-1], want, off * (1 + ref.H) + ref.H * want.abs(), "grouped dB")
+    assert not dW[0].any() and dW[1].any() and not dW[2:8].any()
+
+
 def ends_of(sizes):
     return torch.tensor(list(itertools.accumulate(sizes)), dtype=torch.int32, device="cuda")
 
