@@ -49,12 +49,12 @@ struct Plan {
 enum After { kSum = 0, kStatistics = 1, kActivation = 2 };
 
 // Time of one product's tiles, us, by rates measured on this card.  A 256 x 256 tile takes 1.6 us for a step of 64
-// and 6 us besides, its half 0.9 and 4, a 128 x 128 tile 0.44 and 3 (a fifth more once there is more than a round of
-// them, for it reads twice as much per product out of the caches).  Short tiles, four a CU at a time, take 0.49 and 1
-// each (0.6 where there are fewer), but 0.94 a step for one that is alone.  What follows the sums is the more
-// expensive the fewer workgroups a CU has to cover it.  (us, large | short tiles: 16384 x 4096 x 512 81 | 81, with
-// gelu 144 | 120; 16384 x 4096 x 128 46 | 36, 104 | 76; 8192 x 8192 x 1024 129 | 140, 191 | 174; 128 x 128 | short:
-// 2048 x 2048 x 2048 22 | 36.)
+// and 7 us besides, its half 0.9 and 4, its quarter and a 128 x 128 tile 0.44 and 3 (a fifth more once there is more
+// than a round of them, for they read twice as much per product out of the caches).  Short tiles, four a CU at a time,
+// take 0.49 and 1 each (0.6 where there are fewer), but 0.94 a step for one that is alone.  What follows the sums is
+// the more expensive the fewer workgroups a CU has to cover it.  (us, large | short tiles: 16384 x 4096 x 512 81 | 75,
+// with gelu 144 | 120; 16384 x 4096 x 128 46 | 36, 104 | 76; 8192 x 8192 x 1024 129 | 140, 191 | 174; 128 x 128 |
+// short: 2048 x 2048 x 2048 22 | 36.)
 double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int64_t n, After after)
 {
     static const double kAfter[3][4] = {{0, 0, 0, 0}, {3, 1.6, 1.5, 0.3}, {12, 6.5, 3.5, 2.4}};
@@ -68,12 +68,22 @@ double tile_time(Tile t, int64_t M, int64_t N, int64_t steps, int64_t parts, int
         return fours * each + (rest > 0 ? std::max(0.94 * steps + 3, rest * (each + 0.11 * steps)) : 0);
     }
     const int64_t c = (N + 255) / 256 * parts, units = M / 256 + (M % 256 > 128), lone = M % 256 > 0 && M % 256 <= 128;
-    const double full = 1.6 * steps + 6 + more[0], half = 0.9 * steps + 4 + more[1];
+    const double full = 1.6 * steps + 7 + more[0], half = 0.9 * steps + 4 + more[1];
     const int64_t rounds = units * c / n, last = units * c % n;
-    const auto halves = [&](int64_t tiles) { return (double)((tiles + n - 1) / n) * half; };
-    double tail = halves(lone * c);
-    if (last > 0)
-        tail = std::min(full + halves(std::max<int64_t>(0, lone * c - 2 * (n - last))), halves(lone * c + 2 * last));
+    // the tail as the kernel chooses it: whole, in halves or in quarters
+    const double quarter = 0.44 * steps + 3 + more[2];
+    const int64_t cq = (N + 127) / 128 * parts;
+    const auto halves = [&](int64_t tiles) { return (double)((std::max<int64_t>(0, tiles) + n - 1) / n) * half; };
+    const auto quarters = [&](int64_t tiles) {
+        return (double)((std::max<int64_t>(0, tiles) + n - 1) / n) * quarter * (tiles > n ? 1.2 : 1.0);
+    };
+    double tail = std::min(halves(lone * c), quarters(lone * cq));
+    if (last > 0) {
+        const int64_t d = (last + c - 1) / c, idle = d * c - last;
+        tail = full + std::min(halves(lone * c - 2 * (n - last)), quarters(lone * cq - 3 * (n - last)));
+        tail = std::min(tail, halves((lone + 2 * d) * c - 2 * idle));
+        tail = std::min(tail, quarters((lone + 2 * d) * cq - 3 * idle));
+    }
     return rounds * full + tail;
 }
 
@@ -204,8 +214,7 @@ int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
         const int cols = rows_cols(V, std::min<int64_t>(T, kRowsMost));
         return (V + cols - 1) / cols;
     }
-    const Tile t = xent_tile(T, V, K);
-    return (V + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
+    return (V + kStatCols - 1) / kStatCols;
 }
 
 hipError_t launch_logits(Epi epi, const TileArgs& a, hipStream_t s)

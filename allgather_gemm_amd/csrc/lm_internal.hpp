@@ -61,8 +61,7 @@ struct TileArgs {
 };
 
 int tile_m(Tile t);
-int tile_n(Tile t);
-int stat_cols(Tile t);       // columns that one statistics pair covers
+constexpr int kStatCols = 64;      // columns that one statistics pair of a tiled product covers
 
 // X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_n is filled in here.
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream);

@@ -28,7 +28,7 @@ hipError_t launch_tiles(Kernel kernel, int bm, int bn, int per_cu, TileArgs& a, 
     const int64_t tiles = rows * a.tiles_n * (a.group == kGroupK ? a.E : a.splits);
     if (tiles <= 0)
         return hipSuccess;
-    const int64_t grid = std::min<int64_t>(tiles, (int64_t)cus * per_cu);
+    const int64_t grid = std::min<int64_t>(tiles * (bn / 128), (int64_t)cus * per_cu);      // the smallest tiles are 128 wide
     kernel<<<dim3((unsigned)grid), dim3(NT), 0, stream>>>(a);
     return hipGetLastError();
 }

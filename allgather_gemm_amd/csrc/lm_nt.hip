@@ -36,14 +36,12 @@ hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 }  // namespace
 
 int tile_m(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 32; }
-int tile_n(Tile t) { return t == kTile256 ? 256 : 128; }
-int stat_cols(Tile t) { return t == kTile256 ? 128 : 64; }
 
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream)
 {
     switch (epi) {
     case kEpiStat:
-        a.stat_n = (a.N + tile_n(t) - 1) / tile_n(t) * (tile_n(t) / stat_cols(t));
+        a.stat_n = (a.N + kStatCols - 1) / kStatCols;
         return launch<kEpiStat>(t, a, stream);
     case kEpiGrad: return launch<kEpiGrad>(t, a, stream);
     default: break;

@@ -488,18 +488,37 @@ __device__ __forceinline__ void tile_of(int t, int rows, int cols, int& m, int& 
     m = first + in - n * here;
 }
 
-// Units (tile rows, or two halves) to be taken apart into halves so that a last round of tiles that fills few of G
-// workgroups becomes a shorter one: n units and `lone` halves of c tiles each.  A half tile takes about 12/20 of a
-// tile's time.
-__device__ __forceinline__ int units_to_halve(int n, int lone, int c, int G)
+// How the last tiles are cut: `cut` units (tile rows, or two halves) go in halves or, four for a tile, in quarters.
+struct Tail {
+    int cut;
+    bool quarters;
+};
+
+// A last round of tiles that fills few of G workgroups becomes a shorter one: n units and `lone` halves of c tiles, cq
+// columns of quarters each.  In twentieths of a tile's time a half takes about 12 and a quarter 6, 7 where there is
+// more than a round of them.
+__device__ __forceinline__ Tail tail_of(int n, int lone, int c, int cq, int G)
 {
-    const int last = (int)((int64_t)n * c % G);
-    if (last == 0)
-        return 0;
-    const int64_t keep = max((int64_t)0, (int64_t)lone * c - 2 * (G - last));        // halves left past the last round
-    const int d = (last + c - 1) / c;
-    const int64_t cut = max((int64_t)0, (int64_t)(lone + 2 * d) * c - 2 * (d * c - last));
-    return 20 + 12 * ((keep + G - 1) / G) > 12 * ((cut + G - 1) / G) ? d : 0;
+    const int last = (int)((int64_t)n * c % G), d = (last + c - 1) / c;
+    const int free0 = last ? G - last : 0, free1 = d * c - last;       // workgroups left idle without and with cutting
+    auto halves = [&](int rows, int idle) { return 12 * ((max((int64_t)0, (int64_t)rows * c - 2 * idle) + G - 1) / G); };
+    auto quarters = [&](int rows, int idle) {
+        const int64_t q = max((int64_t)0, (int64_t)rows * cq - 3 * idle);
+        return q > G ? 7 * ((q + G - 1) / G) : q > 0 ? (int64_t)6 : 0;
+    };
+    int64_t best = (last ? 20 : 0) + halves(lone, free0);
+    Tail t = {0, false};
+    if ((last ? 20 : 0) + quarters(lone, free0) < best) {
+        best = (last ? 20 : 0) + quarters(lone, free0);
+        t = {0, true};
+    }
+    if (last && halves(lone + 2 * d, free1) < best) {
+        best = halves(lone + 2 * d, free1);
+        t = {d, false};
+    }
+    if (last && quarters(lone + 2 * d, free1) < best)
+        t = {d, true};
+    return t;
 }
 
 // ------------------------------------------------------------------------------ cross entropy
@@ -867,7 +886,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int64_t m0 = w.m0, n0 = w.n0, M = w.M, K = w.K, grow0 = w.grow0, tn = w.tn, g = w.g, split = w.split;
+    const int64_t m0 = w.m0, n0 = w.n0, M = w.M, K = w.K, grow0 = w.grow0, g = w.g, split = w.split;
 
     SA sa;
     SB sb;
@@ -1140,7 +1159,12 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
                 const int64_t y = target[i] - a.col0 - wcol;
                 const int yo = y >= 0 && y < WNC ? (int)y : -1;
                 if constexpr (EPI == kEpiStat) {
-                    stat_block<FN>(a, acc[i], brow, M, cols, yo, tn * WN + wn, el);
+                    // a pair for each 64 columns, whatever the tile
+#pragma unroll
+                    for (int h = 0; h < FN / 2; ++h)
+                        if (cols > h * 64)
+                            stat_block<2>(a, acc[i] + h * 2, brow, M, min(64, cols - h * 64),
+                                          yo >= h * 64 && yo < h * 64 + 64 ? yo - h * 64 : -1, wcol / 64 + h, el);
                 } else {
                     const bool has = target[i] >= 0 && target[i] < a.vocab;
                     grad_block<FN>(a, acc[i], slab, ldc, brow, M, wcol, cols, yo, has, -row_lse[i] * 1.4426950408889634f,
@@ -1152,8 +1176,8 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
     }
 }
 
-// The tiles of one workgroup.  HALF: tiles of half the height exist too, for what is left of a group's rows and
-// for the last round of tiles.
+// The tiles of one workgroup.  HALF: tiles of half the height exist too, for what is left of a group's rows, and with
+// quarters for the last round of tiles.
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI, bool HALF>
 __device__ __forceinline__ void tile_body(const TileArgs& a)
 {
@@ -1203,6 +1227,20 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum, ROWS = LIN && !TA && S > 1, KS = LIN && TA && S > 1;   // groups there can be
     __shared__ typename std::conditional<ROWS, Groups, typename std::conditional<KS, KGroups, int>::type>::type s_groups;
 
+    // a quarter's four stages, each of one array (or two)
+    Stages<4> lq;
+    if constexpr (HALF) {
+        lq.a[0].lo = sA0;
+        lq.b[0].lo = sU0;
+        lq.a[1].lo = sB0;
+        lq.b[1].lo = sB0 + 16384;
+        lq.a[2].lo = sA1;
+        lq.b[2].lo = sA1 + 16384;
+        lq.a[3].lo = sB1;
+        lq.b[3].lo = sB1 + 16384;
+        lq.slab = l.slab;
+    }
+
     const int G = gridDim.x;
     // workgroups are dispatched round-robin over the 8 XCDs: each XCD takes a contiguous run of tiles
     const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
@@ -1227,12 +1265,14 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
         }
     }
     const int parts = by_k ? a.E : a.splits, lone = nh & 1;
-    const int all_units = nb + nh / 2, cut = HALF && !by_k ? units_to_halve(all_units, lone, cols * parts, G) : 0;
-    const int units = all_units - cut, halves = 2 * cut + lone;        // rows of tiles
+    const int all_units = nb + nh / 2, quarter_cols = (int)((a.N + BN / 2 - 1) / (BN / 2));
+    const Tail tail = HALF && !by_k ? tail_of(all_units, lone, cols * parts, quarter_cols * parts, G) : Tail{0, false};
+    const int cut = tail.cut, units = all_units - cut, halves = 2 * cut + lone;        // rows of tiles
+    const int tail_cols = tail.quarters ? quarter_cols : cols;
 
-    auto in_part = [&](int t, int rows, int& tm, Where& w) {           // tile t of `rows` rows for each part
-        const int per = rows * cols, part = t / per;
-        tile_of(t - part * per, rows, cols, tm, w.tn);
+    auto in_part = [&](int t, int rows, int columns, int& tm, Where& w) {   // tile t of rows x columns for each part
+        const int per = rows * columns, part = t / per;
+        tile_of(t - part * per, rows, columns, tm, w.tn);
         if constexpr (KS) {
             if (by_k) {
                 const int g = uniform(s_groups.order[part]);
@@ -1264,7 +1304,13 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
     };
 
     const int tiles = units * cols * parts, last = tiles % G, idle = last ? G - last : 0;
-    const int p = vid >= last ? vid - last : vid - last + G;
+    int p = vid >= last ? vid - last : vid - last + G;
+    const int tail_tiles = halves * tail_cols * parts;
+    if (last == 0 && tail_tiles < G && G % 8 == 0) {
+        // few tiles and no more: an eighth for each XCD, not all for the first ones
+        const int each_xcd = (tail_tiles + 7) / 8, y = blockIdx.x / 8;
+        p = y < each_xcd ? (int)(blockIdx.x % 8) * each_xcd + y : tail_tiles;
+    }
     bool whole = true;                                                 // units, then halves
     for (int i = 0;; ++i) {
         Where w = {0, 0, a.M, a.K, 0, 0, 0, 0, 0, false};
@@ -1300,24 +1346,25 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
                     }
                 }
             } else {
-                in_part(t, units, tm, w);
+                in_part(t, units, cols, tm, w);
             }
             w.m0 = (int64_t)tm * BM;
         } else {
-            // the workgroups that the last round left without a unit take two of the halves first
-            int h = 2 * idle + p + (i - 2) * G;
-            if (i < 2) {
+            // the workgroups that the last round left without a unit take two of the halves, or three quarters, first
+            const int ahead = tail.quarters ? 3 : 2;
+            int h = ahead * idle + p + (i - ahead) * G;
+            if (i < ahead) {
                 if (p >= idle)
                     continue;
                 h = p + i * idle;
             }
-            if (h >= halves * cols * parts)
+            if (h >= tail_tiles)
                 break;
             int hr = 0;
             if (by_rows) {
                 if constexpr (ROWS) {
-                    hr = h / cols;
-                    w.tn = h - hr * cols;
+                    hr = h / tail_cols;
+                    w.tn = h - hr * tail_cols;
                     if (hr == 2 * cut) {
                         group_half(nh - 1, w);
                     } else {
@@ -1331,14 +1378,19 @@ __device__ __forceinline__ void tile_body(const TileArgs& a)
                     }
                 }
             } else {
-                in_part(h, halves, hr, w);
+                in_part(h, halves, tail_cols, hr, w);
                 w.m0 = (int64_t)units * BM + (int64_t)hr * (BM / 2);
             }
         }
-        w.n0 = (int64_t)w.tn * BN;
+        const bool quarter = !whole && tail.quarters;
+        w.n0 = (int64_t)w.tn * (quarter ? BN / 2 : BN);
         if (full) {
             product_tile<BM, BN, WM, WN, S, TA, TB, EPI>(a, l, w);
         } else if constexpr (HALF) {
+            if (quarter) {
+                product_tile<BM / 2, BN / 2, WM, WN, 4, TA, TB, EPI>(a, lq, w);
+                continue;
+            }
             for (int q = 0; q < 2; ++q) {
                 if (two >= 0)
                     group_half(two + q, w);
