@@ -68,35 +68,25 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
     const int64_t r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
     const int n = (int)max((int64_t)0, min((int64_t)8, N - col));
     float sum[8] = {};
-    // four rows of a thread at a time, their loads ahead of what is computed of the first
+    // a row at a time: 8192 x 14336 gelu_tanh 131 us, 47 x 10749 relu 9.2; four unrolled 144 and 13.3
     auto rows = [&](auto load) {
-        for (int64_t row0 = r0 + rl; row0 < r1; row0 += 32) {
-            float x[4][8], z[4][8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = min(row0 + i * 8, r1 - 1);
-                load(dC + row * N + col, x[i]);
-                if (act != kActNone)
-                    load(pre + row * N + col, z[i]);
+        for (int64_t row = r0 + rl; row < r1; row += 8) {
+            float x[8], z[8];
+            load(dC + row * N + col, x);
+            if (act != kActNone) {
+                load(pre + row * N + col, z);
+                act_slope8(x, z, act);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = row0 + i * 8;
-                if (row >= r1)
-                    break;
-                if (act != kActNone)
-                    act_slope8(x[i], z[i], act);
-                if (d && col < ldd) {
-                    bf16x8 o;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[e] = (__bf16)x[i][e];
-                    *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
-                }
+            if (d && col < ldd) {
+                bf16x8 o;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    sum[e] += x[i][e];
+                    o[e] = (__bf16)x[e];
+                *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] += x[e];
         }
     };
     if (n < 8)
@@ -211,9 +201,9 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
     return hipGetLastError();
 }
 
-// Rows of one workgroup: a multiple of its 8 row lanes, at most 128 workgroups down the rows; one for few rows,
-// whose sums then need no joining.
-static int64_t act_chunk(int64_t M) { return std::max<int64_t>(M <= 64 ? 64 : 32, ((M + 127) / 128 + 7) / 8 * 8); }
+// Rows of one workgroup: a multiple of its 8 row lanes, at most 128 workgroups down the rows.  (With one the sums need
+// no joining.)
+static int64_t act_chunk(int64_t M) { return std::max<int64_t>(32, ((M + 127) / 128 + 7) / 8 * 8); }
 
 int64_t colsum_rows(int64_t M) { return (M + act_chunk(M) - 1) / act_chunk(M); }
 
