@@ -124,6 +124,17 @@ Plan plan_linear(int64_t M, int64_t N, int64_t K, After after)
     return p.splits > 1 || after == kSum ? p : plan_product(M, N, K, after, false);
 }
 
+// Whether a linear layer is for the few-rows kernel.  Where it would take 16 columns a workgroup, each of which goes
+// through all of K for the whole of X, long reductions are split over tiles instead.  Few rows | tiles, us for the whole
+// call, 97 columns: 64 rows, K = 2048 13.2 | 14.0, 4096 20.1 | 14.4, 6992 24.5 | 14.4; 32 rows, K = 4096 14.3 | 14.4,
+// 6992 16.4 | 14.5; 17 rows, K = 6992 13.9 | 14.4.
+bool few_linear(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 16 || M > kRowsMost || rows_cols(N, M) == 64)
+        return M <= kRowsMost;
+    return K * M <= 1 << 17;
+}
+
 // The same for X (M, K) times Y (K, N), whose few rows have a tile of 32 rows.
 Plan plan_nn(int64_t M, int64_t N, int64_t K)
 {
@@ -195,15 +206,18 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     return w;
 }
 
-// Whether the logits of T rows are for the few-rows kernel: up to kRowsMost always, and more of them where the
-// 128 x 128 tiles are so few that its 64 x 64 ones, two a CU and 0.38 us a step of 64, are done before.
+// Whether the logits of T rows are for the few-rows kernel: up to kRowsMost always, and more of them where its 64 x 64
+// tiles, two a CU and 0.38 us a step of 64, all run at once and are done before the 128 x 128 ones.  128 x 128 |
+// 64 x 64, us for loss and gradients: T = 384, V = 1003, K = 1280 47.4 | 39.0, K = 3176 79.9 | 59.5; in more than one
+// round, T = 1024, V = 4427, K = 1280 96.6 | 111.4.  A reduction of at most 8 steps over at most 128 of the 64 x 64
+// tiles gained 0.4 to 2.9 and stays with the 128 x 128 ones.
 bool few_rows(int64_t T, int64_t V, int64_t K)
 {
     if (T <= kRowsMost)
         return true;
     const int64_t steps = (K + 63) / 64, n = cus(), tiles = (T + kRowsMost - 1) / kRowsMost * ((V + 63) / 64);
-    return T <= 1024 && rows_cols(V, kRowsMost) == 64 &&
-           (double)((tiles + 2 * n - 1) / (2 * n)) * (0.38 * steps + 3) < tile_time(kTile128, T, V, steps, 1, n, kStatistics);
+    return T <= 1024 && (steps > 8 || tiles > 128) && tiles <= 2 * n &&
+           0.38 * steps + 3 < tile_time(kTile128, T, V, steps, 1, n, kStatistics);
 }
 
 Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, kStatistics, false).tile; }
@@ -211,7 +225,7 @@ Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, k
 int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
 {
     if (few_rows(T, V, K)) {
-        const int cols = rows_cols(V, std::min<int64_t>(T, kRowsMost));
+        const int cols = rows_cols(V, T);
         return (V + cols - 1) / cols;
     }
     return (V + kStatCols - 1) / kStatCols;
@@ -219,7 +233,7 @@ int64_t stat_pairs(int64_t T, int64_t V, int64_t K)
 
 hipError_t launch_logits(Epi epi, const TileArgs& a, hipStream_t s)
 {
-    return few_rows(a.M, a.N, a.K) ? launch_rows(epi, std::min<int64_t>(a.M, kRowsMost), a, s) : launch_nt(xent_tile(a.M, a.N, a.K), epi, a, s);
+    return few_rows(a.M, a.N, a.K) ? launch_rows(epi, a.M, a, s) : launch_nt(xent_tile(a.M, a.N, a.K), epi, a, s);
 }
 
 struct XentBwd {
@@ -277,7 +291,7 @@ extern "C" int64_t gemm_bias_act_workspace(int64_t M, int64_t Nc, int64_t K)
 {
     if (!shapes_ok(M, Nc, K) || too_large(M, Nc, K))
         return 0;
-    return M <= kRowsMost ? 0 : plan_linear(M, Nc, K, kSum).part_bytes(M, Nc);
+    return few_linear(M, Nc, K) ? 0 : plan_linear(M, Nc, K, kSum).part_bytes(M, Nc);
 }
 
 extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, int64_t M, int64_t Nc,
@@ -291,7 +305,7 @@ extern "C" int gemm_bias_act(const void* A, const void* B, const void* bias, con
         return AG_EINVAL;
     if (too_large(M, Nc, K))
         return AG_EUNSUPPORTED;
-    const bool few = M <= kRowsMost;
+    const bool few = few_linear(M, Nc, K);
     const Plan p = few ? Plan()
                        : plan_linear(M, Nc, K, act != kActNone ? kActivation : bias || residual || pre ? kStatistics : kSum);
     const int64_t need = few ? 0 : p.part_bytes(M, Nc);

@@ -293,7 +293,11 @@ __global__ __launch_bounds__(NT, 2) void rows_wide_kernel(TileArgs a)
 // 64 columns a workgroup once there are enough of them to keep the memory busy, by the columns and rows of X
 // (that narrow workgroups each read again).  Both sides, us, K = 4096, 16 | 64 columns: N = 4096: 1 row
 // 12 | 20, 64 rows 25 | 27; N = 14336: 1 row 33 | 28, 48 rows 67 | 30; N = 32000: 1 row 63 | 56, 64 rows 171 | 57.
-bool rows_wide(int64_t N, int64_t rows, int groups) { return (N + 63) / 64 * groups >= (rows <= 16 ? 128 : 72); }
+// More rows than a tile's are always for them.
+bool rows_wide(int64_t N, int64_t rows, int groups)
+{
+    return rows > kRowsMost || (N + 63) / 64 * groups >= (rows <= 16 ? 128 : 72);
+}
 
 template <int FM, int EPI>
 hipError_t launch(bool wide, const TileArgs& a, hipStream_t stream)

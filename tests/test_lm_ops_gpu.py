@@ -34,7 +34,7 @@ ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
 # over few tiles, none at all
 LINEAR = [(1, 8, 1), (1, 4096, 4096), (2, 64, 7), (3, 0, 9), (16, 2048, 130), (17, 72, 129), (31, 520, 255), (33, 64, 128),
           (48, 1024, 3001), (64, 8192, 40), (65, 320, 384), (129, 200, 257), (256, 128, 128), (300, 1000, 1003),
-          (513, 4096, 520), (2100, 256, 2304), (2049, 136, 2311)]
+          (513, 4096, 520), (2100, 256, 2304), (2049, 136, 2311), (60, 6992, 97), (17, 6992, 97), (33, 4000, 1503)]
 
 
 @pytest.mark.parametrize("i,shape", list(enumerate(LINEAR)))
@@ -221,7 +221,7 @@ def test_grouped_tables_that_are_no_running_sums_stay_in_bounds(table):
 
 
 XENT = [(1, 8, 1), (1, 1024, 5000), (3, 64, 2), (8, 256, 1003), (33, 128, 999), (100, 520, 2049), (130, 64, 300),
-        (257, 136, 1025), (300, 0, 17), (700, 264, 4099)]
+        (257, 136, 1025), (300, 0, 17), (700, 264, 4099), (107, 3176, 1003), (65, 1280, 4427), (1024, 640, 515)]
 
 
 @pytest.mark.parametrize("i,shape", list(enumerate(XENT)))
