@@ -58,6 +58,7 @@ __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits,
 constexpr int COLS = 256;      // columns of a workgroup of act_bwd_kernel: 32 lanes of 8
 
 // d = dC act'(pre), rounded to bf16 for the two products; its column sums from the unrounded values.
+template <int R>
 __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N,
                                                      int64_t chunk, __bf16* d, int64_t ldd, float* colsum,
                                                      __bf16* dbias)
@@ -68,25 +69,35 @@ __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __b
     const int64_t r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
     const int n = (int)max((int64_t)0, min((int64_t)8, N - col));
     float sum[8] = {};
-    // a row at a time: 8192 x 14336 gelu_tanh 131 us, 47 x 10749 relu 9.2; four unrolled 144 and 13.3
+    // R rows of a thread at a time, their loads ahead of what is computed of the first
     auto rows = [&](auto load) {
-        for (int64_t row = r0 + rl; row < r1; row += 8) {
-            float x[8], z[8];
-            load(dC + row * N + col, x);
-            if (act != kActNone) {
-                load(pre + row * N + col, z);
-                act_slope8(x, z, act);
+        for (int64_t row0 = r0 + rl; row0 < r1; row0 += 8 * R) {
+            float x[R][8], z[R][8];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int64_t row = min(row0 + i * 8, r1 - 1);
+                load(dC + row * N + col, x[i]);
+                if (act != kActNone)
+                    load(pre + row * N + col, z[i]);
             }
-            if (d && col < ldd) {
-                bf16x8 o;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int64_t row = row0 + i * 8;
+                if (row >= r1)
+                    break;
+                if (act != kActNone)
+                    act_slope8(x[i], z[i], act);
+                if (d && col < ldd) {
+                    bf16x8 o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = (__bf16)x[i][e];
+                    *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    o[e] = (__bf16)x[e];
-                *reinterpret_cast<bf16x8*>(d + row * ldd + col) = o;
+                    sum[e] += x[i][e];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum[e] += x[e];
         }
     };
     if (n < 8)
@@ -213,7 +224,12 @@ hipError_t launch_act_bwd(const __bf16* dC, const __bf16* pre, int act, int64_t 
     if (M <= 0 || N <= 0)
         return hipSuccess;
     const dim3 grid((unsigned)((N + COLS - 1) / COLS), (unsigned)colsum_rows(M));
-    act_bwd_kernel<<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum, dbias);
+    // rows in flight a thread, four | one, us: 8192 x 8192 gelu 75-80 | 82-86, 8192 x 14336 silu 121 | 129; where
+    // rows do not start on 16 bytes, 8191 x 8191 gelu 130 | 112-117, 47 x 10749 relu 11-12 | 7.5
+    if (N % 8 == 0)
+        act_bwd_kernel<4><<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum, dbias);
+    else
+        act_bwd_kernel<1><<<grid, dim3(NT), 0, stream>>>(dC, pre, act, M, N, act_chunk(M), d, ldd, colsum, dbias);
     return hipGetLastError();
 }
 
