@@ -11,6 +11,8 @@ namespace lm {
 
 constexpr int kMaxGroups = 1024;
 constexpr int kRowsMost = 64;        // rows of X that the few-rows kernel takes at a time
+// Workgroups of 256 threads in a launch: HIP counts its threads along x in 32 bits.  (A multiple of the 8 XCDs.)
+constexpr int64_t kMostWorkgroups = (1 << 24) - 8;
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Group { kGroupNone = 0, kGroupRows = 1, kGroupK = 2 };

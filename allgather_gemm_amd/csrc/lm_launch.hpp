@@ -9,7 +9,7 @@
 namespace ag {
 namespace lm {
 
-constexpr int kEachTile = 1 << 20;             // per_cu: a workgroup for each tile
+constexpr int kEachTile = 1 << 20;             // per_cu: a workgroup for each tile, as far as a launch can have them
 
 // Workgroups of a launch: no more than stay resident, each walks the tiles in steps of the grid.  How many
 // tiles groups of rows make only the device knows.
@@ -28,7 +28,8 @@ hipError_t launch_tiles(Kernel kernel, int bm, int bn, int per_cu, TileArgs& a, 
     const int64_t tiles = rows * a.tiles_n * (a.group == kGroupK ? a.E : a.splits);
     if (tiles <= 0)
         return hipSuccess;
-    const int64_t grid = std::min<int64_t>(tiles * (bn / 128), (int64_t)cus * per_cu);      // the smallest tiles are 128 wide
+    // the smallest tiles are 128 wide
+    const int64_t grid = std::min({tiles * (bn / 128), (int64_t)cus * per_cu, kMostWorkgroups});
     kernel<<<dim3((unsigned)grid), dim3(NT), 0, stream>>>(a);
     return hipGetLastError();
 }

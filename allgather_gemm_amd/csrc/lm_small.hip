@@ -12,16 +12,16 @@ namespace {
 
 // Eight columns of one row per unit: the fp32 sums of the splits.  L threads share a unit where there are
 // few units and many splits (thread l adds splits l, l + L, ... in that order, then the L sums are added in
-// theirs), so that enough loads are in flight: 64 splits of 33 x 1024 took 20 us with L = 1.
+// theirs), so that enough loads are in flight: 64 splits of 33 x 1024 took 20 us with L = 1.  u0: the launch's first unit.
 template <int L>
 __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits, int64_t M, int64_t N, int64_t ldp,
-                                                  LinearOut out)
+                                                  LinearOut out, int64_t u0)
 {
     constexpr int U = NT / L;                      // units of a workgroup
     __shared__ f32x4 s_sum[L > 1 ? L - 1 : 1][U][2];
     const int64_t units = ldp / 8;
     const int ul = threadIdx.x % U, sl = threadIdx.x / U;
-    const int64_t u = blockIdx.x * (int64_t)U + ul;
+    const int64_t u = u0 + blockIdx.x * (int64_t)U + ul;
     const bool there = u < M * units;
     const int64_t row = there ? u / units : 0, col = there ? (u - row * units) * 8 : 0;
     f32x4 s0 = {}, s1 = {};
@@ -202,14 +202,21 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
         return hipSuccess;
     // four threads a unit once that leaves the chip's CUs with less than four workgroups each, sixteen likewise
     const int L = splits >= 32 && units < 16384 ? 16 : splits >= 8 && units < 65536 ? 4 : 1;
-    const dim3 grid((unsigned)((units * L + NT - 1) / NT));
-    if (L == 16)
-        join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
-    else if (L == 4)
-        join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
-    else
-        join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out);
-    return hipGetLastError();
+    const int64_t groups = (units * L + NT - 1) / NT;
+    for (int64_t g = 0; g < groups; g += kMostWorkgroups) {
+        const dim3 grid((unsigned)std::min(groups - g, kMostWorkgroups));
+        const int64_t u0 = g * (NT / L);
+        if (L == 16)
+            join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+        else if (L == 4)
+            join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+        else
+            join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 // Rows of one workgroup: a multiple of its 8 row lanes, at most 128 workgroups down the rows.  (With one the sums need
@@ -244,14 +251,21 @@ hipError_t launch_colsum_join(const float* colsum, int64_t rows, int64_t N, __bf
 hipError_t launch_xent_join(const float* stat, int64_t stat_n, const float* hit, const int64_t* targets, int64_t T,
                             int64_t vocab, float* loss, float* lse, hipStream_t stream)
 {
-    if (T <= 0)
-        return hipSuccess;
-    if (stat_n > 512)
-        xent_join_kernel<4><<<dim3((unsigned)T), dim3(NT), 0, stream>>>(stat, stat_n, hit, targets, T, vocab, loss, lse);
-    else
-        xent_join_kernel<1><<<dim3((unsigned)((T + NT / 64 - 1) / (NT / 64))), dim3(NT), 0, stream>>>(
-            stat, stat_n, hit, targets, T, vocab, loss, lse);
-    return hipGetLastError();
+    const int64_t per = stat_n > 512 ? 1 : NT / 64;        // rows of a workgroup
+    for (int64_t r = 0; r < T; r += kMostWorkgroups * per) {
+        const int64_t rows = std::min(T - r, kMostWorkgroups * per);
+        const dim3 grid((unsigned)((rows + per - 1) / per));
+        if (per == 1)
+            xent_join_kernel<4><<<grid, dim3(NT), 0, stream>>>(stat + r * stat_n * 2, stat_n, hit + r, targets + r, rows,
+                                                               vocab, loss + r, lse + r);
+        else
+            xent_join_kernel<1><<<grid, dim3(NT), 0, stream>>>(stat + r * stat_n * 2, stat_n, hit + r, targets + r, rows,
+                                                               vocab, loss + r, lse + r);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace lm
