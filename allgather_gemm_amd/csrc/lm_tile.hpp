@@ -378,12 +378,12 @@ struct KGroups {
 
 // Tile rows of n rows: of BM rows, and (HALF) of BM / 2.
 template <int BM, bool HALF>
-__device__ __forceinline__ int big_rows(int n)
+__host__ __device__ __forceinline__ int big_rows(int n)
 {
     return HALF ? n / BM + (n % BM > BM / 2) : (n + BM - 1) / BM;
 }
 template <int BM, bool HALF>
-__device__ __forceinline__ int half_rows(int n)
+__host__ __device__ __forceinline__ int half_rows(int n)
 {
     return HALF && n % BM > 0 && n % BM <= BM / 2;
 }
@@ -497,7 +497,7 @@ struct Tail {
 // A last round of tiles that fills few of G workgroups becomes a shorter one: n units and `lone` halves of c tiles, cq
 // columns of quarters each.  In twentieths of a tile's time a half takes about 12 and a quarter 6, 7 where there is
 // more than a round of them.
-__device__ __forceinline__ Tail tail_of(int n, int lone, int c, int cq, int G)
+__host__ __device__ __forceinline__ Tail tail_of(int n, int lone, int c, int cq, int G)
 {
     const int last = (int)((int64_t)n * c % G), d = (last + c - 1) / c;
     const int free0 = last ? G - last : 0, free1 = d * c - last;       // workgroups left idle without and with cutting

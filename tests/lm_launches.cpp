@@ -2,8 +2,9 @@
 // launch code are the library's own, compiled for the host alone; a launch is written down and nothing runs.
 // Compiled and driven by lm_launches.py.
 #include "../allgather_gemm_amd/csrc/ag_internal.hpp"
-#include "../allgather_gemm_amd/csrc/lm_internal.hpp"
+#include "../allgather_gemm_amd/csrc/lm_tile.hpp"
 
+#include <iterator>
 #include <map>
 #include <string>
 #include <vector>
@@ -88,6 +89,20 @@ int rec_args(int i, int64_t* out)
         out[k] = v[k];
     return g_launches[i].tile;
 }
+
+// Every kernel that the library has, as the runtime is told of it.
+int rec_kernels() { return (int)names().size(); }
+const char* rec_kernel(int i) { return std::next(names().begin(), i)->second.c_str(); }
+
+// How a 256 x 256 kernel cuts what n units of a tile's time and `lone` halves leave for a last round
+void rec_tail(int n, int lone, int columns, int quarter_columns, int workgroups, int* out)
+{
+    const ag::lm::Tail t = ag::lm::tail_of(n, lone, columns, quarter_columns, workgroups);
+    out[0] = t.cut;
+    out[1] = t.quarters;
+}
+int rec_big_rows(int n) { return ag::lm::big_rows<256, true>(n); }
+int rec_half_rows(int n) { return ag::lm::half_rows<256, true>(n); }
 
 }  // extern "C"
 

@@ -101,3 +101,44 @@ def xent_bwd(T, K, V, work_bytes=None, dA=True, dB=True):
     n = recorder().gemm_xent_bwd_workspace(T, V, K) if work_bytes is None else work_bytes
     return _record(lambda L: L.gemm_xent_bwd(P[0], P[1], P[2], P[3], P[4], T, V, K, P[5] if dA else None, P[6] if dB else None,
                                              P[7], n, None))
+
+
+def kernels():
+    """Every kernel of the operators."""
+    L = recorder()
+    L.rec_kernel.restype = ctypes.c_char_p
+    return {_kernel(L.rec_kernel(i).decode()) for i in range(L.rec_kernels())}
+
+
+def _sizes(ends, limit):
+    """Rows of each group and, last, of none, a table's entries held to the range that their predecessors leave."""
+    out, prev = [], 0
+    for e in list(ends) + [limit]:
+        e = max(prev, min(int(e), limit))
+        out.append(e - prev)
+        prev = e
+    return out
+
+
+def pieces(launch, ends=()):
+    """What a 256 x 256 kernel's launch is cut into: tiles ("tile"), two groups' halves as one unit ("pair"), and in its
+    tail halves or quarters ("half", "quarter") of tiles ("... of tile"), of pairs, or left over ("lone ...")."""
+    L, a = recorder(), launch.args
+    assert "256" in launch.kernel
+    by_rows, by_k = a.group == 1, a.group == 2
+    units, halves = [], 0              # units in their order
+    for n in _sizes(ends, a.M) if by_rows else [a.M]:
+        units += ["tile"] * L.rec_big_rows(n)
+        if L.rec_half_rows(n):
+            halves += 1
+            if halves % 2 == 0:
+                units.append("pair")
+    if not by_rows:
+        assert halves < 2
+    parts = a.E if by_k else a.splits
+    cols, quarter_cols, cut = (a.N + 255) // 256, (a.N + 127) // 128, (ctypes.c_int * 2)(0, 0)
+    if not by_k:
+        L.rec_tail(len(units), halves & 1, cols * parts, quarter_cols * parts, launch.grid[0], cut)
+    kind = "quarter" if cut[1] else "half"
+    whole, tail = units[:len(units) - cut[0]], units[len(units) - cut[0]:]
+    return set(whole) | {"%s of %s" % (kind, u) for u in tail} | ({"lone " + kind} if halves & 1 else set())

@@ -1,4 +1,6 @@
-"""The launches of the language-model operators, recorded on the host (lm_launches.py): their sizes."""
+"""The launches of the language-model operators, recorded on the host (lm_launches.py): their sizes, and that the GPU
+tests between them launch every kernel in every way that it is used."""
+import itertools
 import os
 
 import pytest
@@ -54,3 +56,94 @@ def test_slices_of_a_join_cover_its_rows():
     assert len(joins) > 1 and sum(l.grid[0] for l in joins) == T // 4
     joins = [l for l in lm.xent(1 << 24, 8, 32769) if l.kernel == "xent_join<4>"]
     assert len(joins) > 1 and sum(l.grid[0] for l in joins) == 1 << 24
+
+
+class Reached:
+    """What the GPU tests' calls launch: kernels, and of products also what is done with them."""
+
+    def __init__(self):
+        self.what = set()
+
+    def add(self, launches, ends=()):
+        for l in launches:
+            self.what.add(l.kernel)
+            if l.args is None:
+                continue
+            group = {0: "", 1: "grouped ", 2: "k-grouped "}[l.args.group]
+            if group:
+                self.what.add(group + l.kernel)
+            if l.args.splits > 1:
+                self.what.add("split " + l.kernel)
+            if l.args.accumulate:
+                self.what.add("adding " + l.kernel)
+            if "256" in l.kernel:
+                self.what.update("%s%s: %s" % (group, l.kernel, p) for p in lm.pieces(l, ends))
+
+
+def reached_by_the_gpu_tests(tests):
+    r = Reached()
+    if "test_lm_ops_gpu" in tests:
+        import test_lm_ops_gpu as t
+        for i, (M, K, Nc) in enumerate(t.LINEAR):
+            options = itertools.cycle(itertools.product(t.ACTS, (True, False), (False, True)))
+            for act, b, res in itertools.islice(options, i, i + 4 * 5, 4):
+                r.add(lm.linear(M, K, Nc, act, b, res, True))
+        for i, (M, K, Nc) in enumerate(t.LARGE):
+            r.add(lm.linear(M, K, Nc))
+            r.add(lm.linear(M, K, Nc, t.ACTS[1 + i % 4], True, i % 2 == 0, True))
+            r.add(lm.linear_bwd(M, Nc // 8 * 8, K))
+            r.add(lm.linear_bwd(K, Nc // 8 * 8, M))
+        for M, K, Nc in t.LINEAR_BWD:
+            for act in t.ACTS:
+                r.add(lm.linear_bwd(M, K, Nc, act))
+        for sizes, spare, K, Nc in t.GROUPED:
+            ends = list(itertools.accumulate(sizes))
+            r.add(lm.grouped(len(sizes), ends[-1] + spare, K, Nc), ends)
+            r.add(lm.grouped_bwd(len(sizes), ends[-1] + spare, K, Nc), ends)
+        for T, K, V in t.XENT:
+            r.add(lm.xent(T, K, V))
+            r.add(lm.xent_bwd(T, K, V))
+            if T <= 300:
+                r.add(lm.xent_bwd(T, K, V, work_bytes=1 << 20))
+        for n in (900 << 10, 1200 << 10):
+            r.add(lm.xent_bwd(300, 264, 3001, work_bytes=n))
+    if "test_lm_kernels_gpu" in tests:
+        import test_lm_kernels_gpu as t
+        for case in t.LINEAR + [(4353, 1000, 4091, "gelu", True, True, True)]:
+            r.add(lm.linear(*case))
+        for case in t.LINEAR_BWD:
+            r.add(lm.linear_bwd(*case))
+        for cases, call in ((t.GROUPED_FWD + t.GROUPED_FEW, lm.grouped), (t.GROUPED_BWD + t.GROUPED_FEW, lm.grouped_bwd)):
+            for sizes, spare, K, Nc in cases:
+                ends = list(itertools.accumulate(sizes))
+                r.add(call(len(sizes), ends[-1] + spare, K, Nc), ends)
+        for case in t.XENT:
+            r.add(lm.xent(*case))
+            r.add(lm.xent_bwd(*case))
+        for case in t.XENT_PIECES:
+            r.add(lm.xent_bwd(*case))
+    return r.what
+
+
+GPU_TESTS = ("test_lm_ops_gpu", "test_lm_kernels_gpu")
+
+
+def test_every_kernel_is_launched_by_a_gpu_test():
+    """The shapes of the GPU tests go where the plans send them: a changed plan that leaves a kernel to no test fails
+    here, and so does a kernel that no call reaches."""
+    missing = lm.kernels() - reached_by_the_gpu_tests(GPU_TESTS)
+    assert not missing, sorted(missing)
+
+
+def test_every_use_of_a_product_is_launched_by_a_gpu_test():
+    cuts = ["tile", "half of tile", "lone half", "quarter of tile", "lone quarter"]
+    want = ["%s: %s" % (k, c) for k in ("nt256<0>", "nt256<1>", "nt256<2>", "nt256<3>", "nn256", "tn256") for c in cuts]
+    want += ["grouped %s: %s" % (k, c) for k in ("nt256<3>", "nn256")
+             for c in cuts + ["pair", "half of pair", "quarter of pair"]]
+    want += ["k-grouped tn256: " + c for c in ("tile", "lone half")]
+    want += ["grouped " + k for k in ("nt128<3>", "nn128", "nn32", "rows<1,4,0>", "rows<1,8,0>", "rows<2,4,0>", "rows<2,6,0>",
+                                      "rows_wide<1,0>", "rows_wide<2,0>")] + ["k-grouped tn128"]
+    want += ["split " + k for k in ("nt128<3>", "nn256", "nn128", "nn32", "tn128")]
+    want += ["adding " + k for k in ("nn256", "nn128", "nnshort", "nn32")]
+    missing = set(want) - reached_by_the_gpu_tests(GPU_TESTS)
+    assert not missing, sorted(missing)

@@ -57,7 +57,7 @@ def test_linear_forward(i, shape):
         assert ok_c() and ok_p()
 
 
-# enough output for the tallest tiles, in whole, cut and partial rounds over the CUs
+# enough output for a round of tiles and more (those that the plans send to the tallest ones: test_lm_kernels_gpu.py)
 LARGE = [(4100, 72, 4360), (2200, 136, 8200), (5000, 64, 6001), (4353, 200, 4090), (300, 64, 33000)]
 
 
@@ -164,7 +164,7 @@ GROUPED = [([1], 0, 8, 8), ([0, 0, 3], 2, 64, 40), ([5, 0, 1, 0, 0, 9, 2], 0, 72
            ([2] * 16, 0, 2048, 512), ([33, 1, 0, 200, 31], 7, 136, 264), ([130, 127, 128, 129], 1, 520, 384),
            ([700, 0, 5, 300, 256], 90, 264, 520), ([64, 0, 3, 100] * 80, 11, 64, 72), ([1] * 1024, 3, 64, 16),
            ([900, 257, 256, 255], 0, 0, 48)]
-# enough rows for the tallest tiles, groups that end inside one; weights large enough for the tallest tiles of dB
+# groups that end inside a tile, many rows; weights large enough for the tallest tiles of dB
 GROUPED += [([700, 513, 0, 1200, 130, 2, 128, 384, 640, 1], 33, 136, 2056), ([257] * 12, 0, 72, 1544),
             ([300, 0, 1, 511, 64, 900, 256], 5, 2056, 1288)]
 
