@@ -206,18 +206,18 @@ LinearBwd plan_linear_bwd(int64_t M, int64_t Nc, int64_t K, int act)
     return w;
 }
 
-// Whether the logits of T rows are for the few-rows kernel: up to kRowsMost always, and more of them where its 64 x 64
-// tiles, two a CU and 0.38 us a step of 64, all run at once and are done before the 128 x 128 ones.  128 x 128 |
-// 64 x 64, us for loss and gradients: T = 384, V = 1003, K = 1280 47.4 | 39.0, K = 3176 79.9 | 59.5; in more than one
-// round, T = 1024, V = 4427, K = 1280 96.6 | 111.4.  A reduction of at most 8 steps over at most 128 of the 64 x 64
-// tiles gained 0.4 to 2.9 and stays with the 128 x 128 ones.
+// Whether the logits of T rows are for the few-rows kernel: up to kRowsMost always, and any number of them where there
+// is at most one of its 64 x 64 tiles for a CU, or two in a reduction of up to 16 steps: two on a CU share its way to
+// the caches.  128 x 128 | 64 x 64, us.  At most one, statistics and join: T = 384, V = 1003, K = 256 10.2 | 8.2,
+// K = 4096 30.0 | 24.1; T = 2048, V = 500, K = 256 10.6 | 8.7, K = 4096 31.7 | 27.6; T = 16384, V = 64, K = 2048
+// 23.4 | 21.9.  Two, loss and gradients: T = 200, V = 4427, K = 1024 49.0 | 45.8, K = 2048 63.7 | 69.8; T = 1024,
+// V = 2048, K = 1024 56.5 | 53.6, K = 2048 69.9 | 72.1; T = 4096, V = 500, K = 512 60.6 | 56.3, K = 1024 66.1 | 69.2.
 bool few_rows(int64_t T, int64_t V, int64_t K)
 {
     if (T <= kRowsMost)
         return true;
-    const int64_t steps = (K + 63) / 64, n = cus(), tiles = (T + kRowsMost - 1) / kRowsMost * ((V + 63) / 64);
-    return T <= 1024 && (steps > 8 || tiles > 128) && tiles <= 2 * n &&
-           0.38 * steps + 3 < tile_time(kTile128, T, V, steps, 1, n, kStatistics);
+    const int64_t tiles = (T + kRowsMost - 1) / kRowsMost * ((V + 63) / 64);
+    return tiles <= (K <= 16 * 64 ? 2 : 1) * cus();
 }
 
 Tile xent_tile(int64_t T, int64_t V, int64_t K) { return plan_product(T, V, K, kStatistics, false).tile; }

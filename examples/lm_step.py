@@ -82,7 +82,8 @@ def batch(ranks=4, rows=96, width=256, vocab=1003, seed=1):
 
 def main(steps=8):
     model, (shards, targets) = Model(), batch()
-    losses = [model.step(shards, targets, rate=1.0) for _ in range(steps)]
+    # small enough that the loss falls on every step whatever order the sums are taken in (at 1.0 it wanders near 0.03)
+    losses = [model.step(shards, targets, rate=0.3) for _ in range(steps)]
     losses = [float(x) for x in losses]
     print("mean loss by step:", " ".join("%.3f" % x for x in losses))
     return losses

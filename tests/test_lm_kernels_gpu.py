@@ -33,8 +33,8 @@ GROUPED_BWD = [(sizes, spare, wide, k) for sizes, spare, wide in TALL_GROUPS for
 GROUPED_FEW = [([4, 0, 9], 2, 264, 1624), ([4, 3], 0, 200, 2504), ([49, 65, 13, 0, 24], 0, 136, 392), ([34, 0], 3, 72, 40),
                ([0, 64, 20, 15], 20, 136, 2056), ([1, 0, 2, 60, 0, 0, 9, 3], 1, 328, 1032)]
 # T, K, V
-XENT = [(6041, 1320, 1228), (2169, 1544, 3247), (4454, 472, 4109), (3983, 536, 3793), (7198, 688, 2740), (2600, 1000, 6001),
-        (19, 264, 4266), (17, 136, 200), (56, 200, 333), (5, 264, 9001), (27, 520, 4611), (36, 264, 4750), (2, 72, 36001)]
+XENT = [(2100, 72, 3001), (4100, 8, 500), (6041, 1320, 1228), (2169, 1544, 3247), (4454, 472, 4109), (3983, 536, 3793), (7198, 688, 2740), (2600, 1000, 6001),
+        (16000, 136, 60), (2000, 200, 501), (200, 328, 8000), (1000, 1032, 1500), (19, 264, 4266), (17, 136, 200), (56, 200, 333), (5, 264, 9001), (27, 520, 4611), (36, 264, 4750), (2, 72, 36001)]
 # T, K, V, bytes of scratch memory: several pieces of the vocabulary, whose dA are added up by each kernel of dA
 XENT_PIECES = [(3247, 1184, 8574, 61594368), (7198, 688, 2740, 24400000), (3, 72, 700, 4096), (20, 200, 3000, 200000),
                (300, 264, 3001, 1 << 20)]

@@ -147,3 +147,20 @@ def test_every_use_of_a_product_is_launched_by_a_gpu_test():
     want += ["adding " + k for k in ("nn256", "nn128", "nnshort", "nn32")]
     missing = set(want) - reached_by_the_gpu_tests(GPU_TESTS)
     assert not missing, sorted(missing)
+
+
+def logits_kernel(T, K, V):
+    return lm.xent(T, K, V)[0].kernel
+
+
+def test_logits_of_few_tiles_go_to_the_few_rows_kernel():
+    """By the number of its tiles and the reduction's length alone, in the backward pass as in the forward one."""
+    for T, V in ((65, 1), (384, 1003), (1024, 500), (2048, 500), (4096, 200), (16384, 64), (512, 2048)):
+        for K in (8, 256, 576, 4096):
+            assert logits_kernel(T, K, V) == "rows_wide<4,1>", (T, K, V)
+            assert lm.xent_bwd(T, K, V)[0].kernel == "rows_wide<4,2>", (T, K, V)
+    for T, V in ((200, 8000), (1024, 2048), (384, 4427)):        # up to two tiles for a CU
+        assert logits_kernel(T, 1024, V) == "rows_wide<4,1>"
+        assert logits_kernel(T, 1032, V) == "nt128<1>"
+    for T, V in ((1024, 2049), (8192, 300), (65, 1 << 20)):
+        assert not logits_kernel(T, 8, V).startswith("rows")
