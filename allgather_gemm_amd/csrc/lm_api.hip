@@ -381,6 +381,16 @@ static Tile group_tile(int64_t M, int64_t N, int64_t K, int32_t E)
     return rows / 256 * ((N + 255) / 256) < cus() ? kTile128 : plan_product(rows, N, K, kSum, false, true).tile;
 }
 
+// Whether products grouped by rows are for the few-rows kernel, by the groups' mean rows: only the device knows more.  Each
+// of its workgroups goes over the groups' ends by itself, 64 at a time, and in a short reduction over many groups that
+// takes more than the product.  Tiles | few rows, us, for rows spread evenly, by weights r^4 with r uniform, all in one
+// group: 16 groups, K = 4096, N = 2048, 32 rows each 44 | 46, -, 32 | 23; 64, K = 2048, N = 768, 4 rows 42 | 36,
+// 26 | 30, 19 | 11, 32 rows 44 | 44, 41 | 50, 24 | 26; 256, K = 4096, N = 1024, 4 rows 524 | 419, 232 | 238, 35 | 69.
+// Above a mean of 32: 64, K = 2048, N = 1024, 48 rows 49 | 58, -, 22 | 34.  More groups than K / 8: 512, K = 1024, N = 512,
+// 4 rows 112 | 135, 65 | 94, 20 | 72; 256, K = 512, N = 2048, 32 rows 131 | 196, 97 | 187, 31 | 168; up to 64 groups
+// that does not show: K = 64, N = 512, 32 rows 8.0 | 7.8, 8.0 | 8.5, 8.1 | 7.7.
+static bool few_groups(int64_t M, int64_t K, int32_t E) { return M / E <= 32 && E <= std::max<int64_t>(64, K / 8); }
+
 extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, int32_t E, int64_t M, int64_t Nc, int64_t K,
                             void* C, void* stream)
 {
@@ -398,7 +408,7 @@ extern "C" int gemm_grouped(const void* A, const void* B, const int32_t* ends, i
     a.group = kGroupRows;
     a.strideB = Nc * K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    LM_HIP(M / E <= 32 ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, Nc, K, E), kEpiLinear, a, s),
+    LM_HIP(few_groups(M, K, E) ? launch_rows(kEpiLinear, M / E, a, s) : launch_nt(group_tile(M, Nc, K, E), kEpiLinear, a, s),
            "launch gemm_grouped");
     return AG_OK;
 }

@@ -31,7 +31,8 @@ GROUPED_FWD = [(sizes, spare, k, wide) for sizes, spare, wide in TALL_GROUPS for
 GROUPED_BWD = [(sizes, spare, wide, k) for sizes, spare, wide in TALL_GROUPS for k in (72, 392)]
 # few rows a group: sizes, rows of none, K, Nc
 GROUPED_FEW = [([4, 0, 9], 2, 264, 1624), ([4, 3], 0, 200, 2504), ([49, 65, 13, 0, 24], 0, 136, 392), ([34, 0], 3, 72, 40),
-               ([0, 64, 20, 15], 20, 136, 2056), ([1, 0, 2, 60, 0, 0, 9, 3], 1, 328, 1032)]
+               ([0, 64, 20, 15], 20, 136, 2056), ([3, 0, 1, 17, 0] * 30, 9, 1208, 72), ([2, 0, 5, 0] * 25, 4, 1032, 40),
+               ([9, 0, 2] * 70, 3, 512, 136), ([1, 0, 2, 60, 0, 0, 9, 3], 1, 328, 1032)]
 # T, K, V
 XENT = [(2100, 72, 3001), (4100, 8, 500), (6041, 1320, 1228), (2169, 1544, 3247), (4454, 472, 4109), (3983, 536, 3793), (7198, 688, 2740), (2600, 1000, 6001),
         (16000, 136, 60), (2000, 200, 501), (200, 328, 8000), (1000, 1032, 1500), (19, 264, 4266), (17, 136, 200), (56, 200, 333), (5, 264, 9001), (27, 520, 4611), (36, 264, 4750), (2, 72, 36001)]

@@ -164,3 +164,13 @@ def test_logits_of_few_tiles_go_to_the_few_rows_kernel():
         assert logits_kernel(T, 1032, V) == "nt128<1>"
     for T, V in ((1024, 2049), (8192, 300), (65, 1 << 20)):
         assert not logits_kernel(T, 8, V).startswith("rows")
+
+
+def test_many_groups_of_a_short_reduction_go_to_tiles():
+    """Whatever the skew: all rows of 1024 groups may be one group's."""
+    few = lambda E, M, K, Nc: lm.grouped(E, M, K, Nc)[0].kernel.startswith("rows")
+    for E, K in ((1024, 512), (1024, 8184), (65, 512), (129, 1024), (256, 2040)):
+        for rows in (1, E, 32 * E):
+            assert not few(E, rows, K, 512), (E, K, rows)
+    for E, K in ((1, 8), (64, 8), (64, 512), (128, 1024), (1024, 8192)):
+        assert few(E, 1, K, 512) and few(E, 33 * E - 1, K, 512) and not few(E, 33 * E, K, 512), (E, K)
