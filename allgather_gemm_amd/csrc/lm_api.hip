@@ -429,6 +429,9 @@ extern "C" int gemm_grouped_bwd(const void* dC, const void* A, const void* B, co
         a.E = E;
         a.group = kGroupRows;
         a.strideB = Nc * K;
+        // tiles of 32 rows by the groups' mean (128 or 256 | 32 rows, us, even groups): 16 groups, 2048 to 4096, 32 rows
+        // each 46.4 | 43.5, 48 rows 47.1 | 52.0; 256 groups, 512 to 1024, 32 rows 60 | 57, 48 rows 63 | 85; all in one of
+        // 256 groups, 8 rows 13.8 | 13.8, 32 rows 19 | 39
         LM_HIP(launch_nn(M / E <= 32 ? kTile32 : group_tile(M, K, Nc, E), a, s), "launch dA");
     }
     if (dB && Nc > 0 && K > 0) {
@@ -436,7 +439,11 @@ extern "C" int gemm_grouped_bwd(const void* dC, const void* A, const void* B, co
         a.ends = ends;
         a.E = E;
         a.group = kGroupK;
-        LM_HIP(launch_tn(((Nc + 255) / 256) * ((K + 255) / 256) * E * 2 >= cus() ? kTile256 : kTile128, a, s), "launch dB");
+        // 256 x 256 tiles from a round of them on, by both sides (128 x 128 | 256 x 256, us, uneven groups): 8 groups,
+        // 1024 x 1024, half a round: 64 rows each 12 | 16, 1000 rows 25 | 45; 16 groups, a round: 19 | 16, 48 | 62;
+        // 8 groups, 2048 x 2048, two rounds: 32 | 25, 88 | 69
+        const int64_t tiles = (Nc + 255) / 256 * ((K + 255) / 256) * E;
+        LM_HIP(launch_tn(tiles >= cus() ? kTile256 : kTile128, a, s), "launch dB");
     }
     return AG_OK;
 }

@@ -174,3 +174,10 @@ def test_many_groups_of_a_short_reduction_go_to_tiles():
             assert not few(E, rows, K, 512), (E, K, rows)
     for E, K in ((1, 8), (64, 8), (64, 512), (128, 1024), (1024, 8192)):
         assert few(E, 1, K, 512) and few(E, 33 * E - 1, K, 512) and not few(E, 33 * E, K, 512), (E, K)
+
+
+def test_gradients_of_experts_weights_take_the_tallest_tiles_from_a_round_of_them_on():
+    for E, M, K, Nc in ((8, 8000, 1024, 1024), (4, 64, 1024, 1024), (100, 100, 256, 256), (1, 5000, 512, 512), (255, 255, 8, 8)):
+        assert lm.grouped_bwd(E, M, K, Nc)[1].kernel == "tn128", (E, K, Nc)
+    for E, M, K, Nc in ((16, 16, 1024, 1024), (8, 8000, 2048, 2048), (256, 300, 8, 8)):
+        assert lm.grouped_bwd(E, M, K, Nc)[1].kernel == "tn256", (E, K, Nc)
