@@ -124,15 +124,22 @@ Plan plan_linear(int64_t M, int64_t N, int64_t K, After after)
     return p.splits > 1 || after == kSum ? p : plan_product(M, N, K, after, false);
 }
 
-// Whether a linear layer is for the few-rows kernel.  Where it would take 16 columns a workgroup, each of which goes
-// through all of K for the whole of X, long reductions are split over tiles instead.  Few rows | tiles, us for the whole
-// call, 97 columns: 64 rows, K = 2048 13.2 | 14.0, 4096 20.1 | 14.4, 6992 24.5 | 14.4; 32 rows, K = 4096 14.3 | 14.4,
-// 6992 16.4 | 14.5; 17 rows, K = 6992 13.9 | 14.4.
+// Whether a linear layer is for the few-rows kernel, each of whose workgroups goes through all of K for its columns: long
+// reductions are split over tiles instead, which takes a second launch.  Tiles | few rows, us on the device.  16 columns a
+// workgroup, 97 | 1000 columns: 1 row, K = 8192 9.0 | 7.8, 9.9 | 8.1, K = 32768 12.7 | 18.7, 17.2 | 18.9; 16 rows,
+// K = 4096 8.9 | 9.2, 9.9 | 9.4, K = 8192 9.6 | 13.4, 10.9 | 13.6; 32 rows, K = 2048 8.7 | 9.7, 9.5 | 10.0, K = 4096
+// 9.1 | 14.2, 10.2 | 14.4; 64 rows, K = 1024 8.8 | 10.4, 9.8 | 10.8, K = 2048 8.8 | 12.8, 10.5 | 13.1 (the launch saved
+// is worth 3 us to a host that waits for nothing else: 64 rows, K = 1024 13.1 | 10.0, K = 2048 12.8 | 12.5).  64 columns
+// a workgroup, 4600 | 10000 | 14336 columns: 32 rows, K = 4096 13.8 | 15.8, 20.4 | 17.1, 24.4 | 20.3, K = 8192
+// 19.0 | 27.7, 30.9 | 32.1, 39.5 | 37.4; 64 rows, K = 2048 13.4 | 12.1, 15.9 | 13.6, 16.0 | 13.7, K = 4096 15.3 | 20.5,
+// 21.7 | 21.6, 25.6 | 23.2, K = 16384 30.9 | 68.2, 68.8 | 99.8, 106.6 | 116.6.
 bool few_linear(int64_t M, int64_t N, int64_t K)
 {
-    if (M <= 16 || M > kRowsMost || rows_cols(N, M) == 64)
-        return M <= kRowsMost;
-    return K * M <= 1 << 17;
+    if (M > kRowsMost)
+        return false;
+    if (rows_cols(N, M) == 16)
+        return K * std::max<int64_t>(M, 4) <= 1 << 16;
+    return K * std::max<int64_t>(M, 32) <= 1 << 17 || (N + 63) / 64 * 4 >= cus() * 3;
 }
 
 // The same for X (M, K) times Y (K, N), whose few rows have a tile of 32 rows.

@@ -18,6 +18,8 @@ LINEAR = [(6041, 1320, 1228, "gelu", True, True, True), (8992, 824, 1570, "relu"
           (7198, 688, 2740, "gelu_tanh", False, True, False), (6381, 832, 2750, "silu", True, True, True),
           (5325, 744, 1482, "none", False, False, False), (1660, 1920, 2712, "none", False, False, False),
           (4353, 1000, 4090, "none", True, True, False),
+          (1, 32768, 97, "silu", True, True, True), (9, 8200, 1001, "gelu", True, False, True),
+          (40, 16392, 4601, "relu", False, True, False),
           (52, 200, 70, "gelu", True, True, True), (36, 264, 4750, "silu", True, True, True),
           (51, 136, 4923, "relu", False, True, True), (11, 328, 5003, "gelu", True, False, False),
           (19, 200, 4266, "gelu_tanh", True, True, True), (23, 136, 4700, "none", False, True, False)]

@@ -181,3 +181,13 @@ def test_gradients_of_experts_weights_take_the_tallest_tiles_from_a_round_of_the
         assert lm.grouped_bwd(E, M, K, Nc)[1].kernel == "tn128", (E, K, Nc)
     for E, M, K, Nc in ((16, 16, 1024, 1024), (8, 8000, 2048, 2048), (256, 300, 8, 8)):
         assert lm.grouped_bwd(E, M, K, Nc)[1].kernel == "tn256", (E, K, Nc)
+
+
+def test_long_reductions_of_few_rows_are_split_over_tiles():
+    few = lambda M, K, Nc: lm.linear(M, K, Nc)[0].kernel.startswith("rows")
+    for M, K, Nc in ((1, 32768, 97), (16, 8192, 1000), (32, 4096, 97), (64, 2048, 2000), (17, 16384, 4600), (64, 4096, 7000),
+                     (64, 16384, 10000), (1, 8192, 8192), (65, 64, 64)):
+        assert not few(M, K, Nc), (M, K, Nc)
+    for M, K, Nc in ((1, 4096, 4096), (1, 16384, 97), (16, 4096, 1000), (32, 2048, 97), (64, 1024, 2000), (32, 4096, 4600),
+                     (64, 2048, 7000), (48, 4096, 14336), (64, 16384, 14336), (1, 4096, 8192), (64, 8, 1)):
+        assert few(M, K, Nc), (M, K, Nc)
