@@ -3,6 +3,9 @@ and a language model's operators around the gathered product, on one MI355X.
 
 Argument marshalling only: every step of the path runs in the library's gfx950 kernels.  Tensors
 are torch CUDA (HIP) tensors; the library is given their device pointers and the current stream.
+Autograd records none of the calls: what they return has no gradient function, whatever its inputs
+require; gradients come from the ..._bwd calls (or a torch.autograd.Function of the caller's around
+both).
 The library must have been built (``python allgather_gemm_amd/build.py`` or
 ``__graft_entry__.build()``); there is no fallback implementation.
 """
@@ -370,12 +373,20 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _written(t):
+    """A tensor of the caller's that a call has written counts as changed in place: autograd then refuses to use it
+    where it was saved before."""
+    if t is not None:
+        torch.autograd.graph.increment_version(t)
+
+
 def gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
                   residual: torch.Tensor | None = None, C: torch.Tensor | None = None,
                   pre: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """C (M, Nc) = act(A @ B^T + bias) + residual, all bf16, sums in fp32.  A (M, K), B (Nc, K), bias (Nc),
     residual (M, Nc); act: "none" | "relu" | "silu" | "gelu" (erf) | "gelu_tanh".  pre: optional (M, Nc)
-    output that receives A @ B^T + bias, which gemm_bias_act_bwd needs.  residual may be C itself."""
+    output that receives A @ B^T + bias, which gemm_bias_act_bwd needs.  residual may be C itself.  C and pre, where
+    given, are written in place; the result has no gradient function."""
     M, K = _dims(A, "A", 2)
     Nc = _dims(B, "B", 2)[0]
     dev = A.device
@@ -385,12 +396,13 @@ def gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = 
     a, b = _need(A, "A", (M, K)), _need(B, "B", (Nc, K), device=dev)
     bi, r = _need(bias, "bias", (Nc,), device=dev), _need(residual, "residual", (M, Nc), device=dev)
     pr = _need(pre, "pre", (M, Nc), device=dev)
-    if C is None:
-        C = A.new_empty((M, Nc))
-    c = _need(C, "C", (M, Nc), device=dev)
+    out = A.new_empty((M, Nc)) if C is None else C
+    c = _need(out, "C", (M, Nc), device=dev)
     w, n = _work("gemm_bias_act", dev, M, Nc, K)
     _done(lib().gemm_bias_act(a, b, bi, r, M, Nc, K, _ACTS[act], c, pr, _p(w), n, _stream_of(dev)), "gemm_bias_act")
-    return C
+    _written(C)
+    _written(pre)
+    return out
 
 
 def gemm_bias_act_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, act: str = "none",
@@ -422,7 +434,7 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, C: torch.
                  stream=None) -> torch.Tensor:
     """Rows [ends[e-1], ends[e]) of C (M, Nc) = the same rows of A (M, K) @ B[e]^T, B (E, Nc, K), all bf16;
     rows past ends[-1] are zero.  ends: (E,) int32 on the device, the running sums of the experts' row
-    counts; it is not read on the host."""
+    counts; it is not read on the host.  C, where given, is written in place; the result has no gradient function."""
     M, K = _dims(A, "A", 2)
     E, Nc, _ = _dims(B, "B", 3)
     dev = A.device
@@ -431,11 +443,11 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, C: torch.
             return gemm_grouped(A, B, ends, C)
     a, b = _need(A, "A", (M, K)), _need(B, "B", (E, Nc, K), device=dev)
     en = _need(ends, "ends", (E,), torch.int32, dev)
-    if C is None:
-        C = A.new_empty((M, Nc))
-    c = _need(C, "C", (M, Nc), device=dev)
+    out = A.new_empty((M, Nc)) if C is None else C
+    c = _need(out, "C", (M, Nc), device=dev)
     _done(lib().gemm_grouped(a, b, en, E, M, Nc, K, c, _stream_of(dev)), "gemm_grouped")
-    return C
+    _written(C)
+    return out
 
 
 def gemm_grouped_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ends: torch.Tensor, need_dA: bool = True,
@@ -458,7 +470,7 @@ def gemm_grouped_bwd(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ends: t
 def gemm_xent(A: torch.Tensor, B: torch.Tensor, targets: torch.Tensor, stream=None):
     """Cross entropy of the logits A @ B^T, which are never stored: (loss, lse), both (T,) fp32, for A (T, K),
     B (V, K) bf16 and targets (T,) int64.  A target outside [0, V) marks a row without one: loss 0, no
-    gradient."""
+    gradient.  The results have no gradient function."""
     T, K = _dims(A, "A", 2)
     V = _dims(B, "B", 2)[0]
     dev = A.device
