@@ -191,3 +191,28 @@ def test_long_reductions_of_few_rows_are_split_over_tiles():
     for M, K, Nc in ((1, 4096, 4096), (1, 16384, 97), (16, 4096, 1000), (32, 2048, 97), (64, 1024, 2000), (32, 4096, 4600),
                      (64, 2048, 7000), (48, 4096, 14336), (64, 16384, 14336), (1, 4096, 8192), (64, 8, 1)):
         assert few(M, K, Nc), (M, K, Nc)
+
+
+@pytest.mark.parametrize("T,V,K", [(1, 1, 8), (33, 50257, 1024), (4096, 65536, 64), (4096, 65537, 64), (4096, 50257, 2048),
+                                   (8192, 32769, 128), (8192, 128256, 4096), (8192, 1 << 20, 4096), (1 << 20, 257, 1024),
+                                   (1 << 20, 1 << 17, 1024), (1 << 22, 600, 64)])
+def test_workspace_of_the_gradient_is_a_piece_of_d_logits_and_the_sums_of_dA(T, V, K):
+    """To the byte: pieces of at most 512 MiB (256 columns where that is more), in as few as that takes, and the fp32 sums
+    that the launches write."""
+    launches = lm.xent_bwd(T, K, V)
+    logits = [l for l in launches if l.args and l.args.K == K and l.args.M == T and not l.args.part and "<" in l.kernel]
+    dA = [l for l in launches if l.kernel.startswith("nn")]
+    pieces, most = len(logits), max(256, (512 << 20) // (2 * T) // 256 * 256)
+    assert sum(l.args.N for l in logits) == V and pieces == -(-V // most) == len(dA)
+    piece = -(-(-(-V // pieces)) // 256) * 256
+    assert piece <= most and all(l.args.N == piece for l in logits[:-1])
+    splits = dA[0].args.splits
+    assert all(l.args.splits == splits and l.args.part == (pieces > 1 or splits > 1) for l in dA)
+    assert [l.args.accumulate for l in dA] == [0] + [1] * (pieces - 1)
+    region = lambda n: -(-n // 256) * 256
+    want = region(T * piece * 2) + (region(splits * T * K * 4) if pieces > 1 or splits > 1 else 0)
+    assert lm.recorder().gemm_xent_bwd_workspace(T, V, K) == want
+    # an eighth of that is enough where it holds the narrowest piece, and then only makes more of them
+    least = region(T * 512) + region(64 * T * K * 4)
+    if want // 8 >= least:
+        assert len([l for l in lm.xent_bwd(T, K, V, work_bytes=want // 8) if l.kernel.startswith("nn")]) > pieces
