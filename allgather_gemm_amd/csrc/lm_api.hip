@@ -248,8 +248,8 @@ struct XentBwd {
     int64_t pieces;
     Plan da;
     bool part;               // dA is summed in fp32 in the workspace
-    int64_t part_bytes, db_part_bytes;
-    int64_t bytes(int64_t T) const { return region(T * piece * 2) + part_bytes + db_part_bytes; }
+    int64_t part_bytes;
+    int64_t bytes(int64_t T) const { return region(T * piece * 2) + part_bytes; }
 };
 
 XentBwd plan_xent_bwd(int64_t T, int64_t V, int64_t K, int64_t piece)
@@ -260,7 +260,6 @@ XentBwd plan_xent_bwd(int64_t T, int64_t V, int64_t K, int64_t piece)
     w.da = plan_nn(T, K, std::min(up(V, 8), piece));
     w.part = w.pieces > 1 || w.da.splits > 1;
     w.part_bytes = w.part ? region((int64_t)w.da.splits * T * K * 4) : 0;
-    w.db_part_bytes = 0;
     return w;
 }
 

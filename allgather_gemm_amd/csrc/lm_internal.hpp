@@ -15,7 +15,7 @@ constexpr int kRowsMost = 64;        // rows of X that the few-rows kernel takes
 constexpr int64_t kMostWorkgroups = (1 << 24) - 8;
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
-enum Group { kGroupNone = 0, kGroupRows = 1, kGroupK = 2 };
+enum Group { kGroupRows = 1, kGroupK = 2 };     // 0: no groups
 enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3 };
 // kTile128: four stages, one workgroup a CU; kTileShort: 128 x 128 with one stage, a workgroup for each tile and
 // four of them on a CU, no groups
@@ -62,7 +62,6 @@ struct TileArgs {
     int64_t vocab, col0;     // size of the vocabulary; its first column in this piece
 };
 
-int tile_m(Tile t);
 constexpr int kStatCols = 64;      // columns that one statistics pair of a tiled product covers
 
 // X (M, K) Y (N, K); X (M, K) Y (K, N); X (K, M) Y (K, N).  tiles_n is filled in here.

@@ -35,8 +35,6 @@ hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
 
 }  // namespace
 
-int tile_m(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 32; }
-
 hipError_t launch_nt(Tile t, Epi epi, TileArgs a, hipStream_t stream)
 {
     switch (epi) {

@@ -2,6 +2,7 @@
 tests between them launch every kernel in every way that it is used."""
 import itertools
 import os
+import re
 
 import pytest
 
@@ -216,3 +217,19 @@ def test_workspace_of_the_gradient_is_a_piece_of_d_logits_and_the_sums_of_dA(T, 
     least = region(T * 512) + region(64 * T * K * 4)
     if want // 8 >= least:
         assert len([l for l in lm.xent_bwd(T, K, V, work_bytes=want // 8) if l.kernel.startswith("nn")]) > pieces
+
+
+def test_nothing_is_declared_that_nothing_uses():
+    """Functions, constants and enumerators that the operators' files share each stand in a use outside their declaration."""
+    csrc = os.path.join(lm.ROOT, "allgather_gemm_amd", "csrc")
+    text = {f: re.sub(r"//.*", "", open(os.path.join(csrc, f), encoding="utf-8").read())
+            for f in os.listdir(csrc) if f.startswith("lm_")}
+    shared = text["lm_internal.hpp"]
+    functions = re.findall(r"^(?:int|int64_t|hipError_t) (\w+)\(", shared, re.M)
+    constants = re.findall(r"constexpr \w+ (\w+) =", shared) + re.findall(r"\b(k\w+) = \d", shared)
+    assert len(functions) > 8 and len(constants) > 12
+    code = "\n".join(text.values())
+    for f in functions:                # neither declared nor defined there, but called
+        assert re.search(r"(?<!^int )(?<!^int64_t )(?<!^hipError_t )\b%s\(" % f, code, re.M), f
+    for c in constants:
+        assert any(re.search(r"\b%s\b" % c, text[f]) for f in text if f != "lm_internal.hpp"), c
