@@ -142,7 +142,12 @@ bool few_linear(int64_t M, int64_t N, int64_t K)
     return K * std::max<int64_t>(M, 32) <= 1 << 17 || (N + 63) / 64 * 4 >= cus() * 3;
 }
 
-// The same for X (M, K) times Y (K, N), whose few rows have a tile of 32 rows.
+// The same for X (M, K) times Y (K, N), whose few rows have a tile of 32 rows, a workgroup for each CU as far as parts of
+// four steps allow.  128 x 128 tiles by their plan | 32 rows, us: 1 | 32 rows of N = 1024, K = 512 7.1, 7.3 | 6.6, 7.3,
+// K = 8192 9.7, 12.2 | 7.7, 10.4; N = 4096, K = 2048 10.0, 12.0 | 8.0, 10.4, K = 32000 45.2, 47.5 | 44.8, 46.7; N = 14336,
+// K = 64 5.0, 5.3 | 4.0, 4.1, K = 512 7.7, 8.1 | 7.6, 9.5, K = 8192 40.7, 41.6 | 39.6, 40.2.  With 48 rows, two tiles of
+// 32: N = 4096, K = 2048 12.5 | 14.0, K = 32000 48.2 | 52.7.  Parts of at least eight steps: K = 512 5.3, 5.4 instead of
+// 6.6, 7.3 (one part, no join), K = 2048 7.7, 8.2 instead of 7.1, 7.8 at N = 1024.
 Plan plan_nn(int64_t M, int64_t N, int64_t K)
 {
     if (M > 32)

@@ -57,7 +57,9 @@ __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits,
 
 constexpr int COLS = 256;      // columns of a workgroup of act_bwd_kernel: 32 lanes of 8
 
-// d = dC act'(pre), rounded to bf16 for the two products; its column sums from the unrounded values.
+// d = dC act'(pre), rounded to bf16 (at most 2^-8 of it) for the two products, whose matrix instructions take both
+// factors so; its column sums from the unrounded values.  The gradients of 8192 x 8192 x 8192 with gelu are then 0.00233
+// of their norm off, 0.00166 if d were not rounded; two bf16 parts of it would double the products.
 template <int R>
 __global__ __launch_bounds__(NT) void act_bwd_kernel(const __bf16* dC, const __bf16* pre, int act, int64_t M, int64_t N,
                                                      int64_t chunk, __bf16* d, int64_t ldd, float* colsum,
