@@ -526,12 +526,15 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         a.targets = targets;
         a.lse = lse;
         a.dloss = dloss;
+        a.dloss_rows = T;
         a.vocab = V;
         a.col0 = v0;
         LM_HIP(launch_logits(kEpiGrad, a, s), "launch d logits");
         if (dA) {
             a = product(ws, ldd, Bp, K, T, K, up(n, 8), dA, K);
             a.k_valid = n;
+            a.dloss = dloss;
+            a.dloss_rows = T;
             if (w.part) {
                 a.splits = w.da.splits;
                 a.split_steps = w.da.split_steps;
@@ -543,6 +546,8 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         }
         if (dB) {
             a = product(ws, ldd, A, K, n, K, T, static_cast<char*>(dB) + v0 * K * 2, K);
+            a.dloss = dloss;
+            a.dloss_rows = T;
             const Plan p = plan_product(n, K, T, kSum, false);
             LM_HIP(launch_tn(p.tile, a, s), "launch dB");
         }
@@ -551,7 +556,7 @@ extern "C" int gemm_xent_bwd(const float* dloss, const void* A, const void* B, c
         LinearOut out = {};
         out.C = static_cast<__bf16*>(dA);
         out.ldc = K;
-        LM_HIP(launch_join(part, w.da.splits, T, K, K, out, s), "launch dA join");
+        LM_HIP(launch_join(part, w.da.splits, T, K, K, out, s, dloss, T), "launch dA join");
     }
     return AG_OK;
 }

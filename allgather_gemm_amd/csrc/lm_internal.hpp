@@ -16,7 +16,7 @@ constexpr int64_t kMostWorkgroups = (1 << 24) - 8;
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Group { kGroupRows = 1, kGroupK = 2 };     // 0: no groups
-enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3 };
+enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3, kEpiScaled = 4 };
 // kTile128: four stages, one workgroup a CU; kTileShort: 128 x 128 with one stage, a workgroup for each tile and
 // four of them on a CU, no groups
 enum Tile { kTile256 = 0, kTile128 = 1, kTile32 = 2, kTileShort = 3 };
@@ -56,9 +56,11 @@ struct TileArgs {
     int64_t stat_n;
     float* hit;              // the target's logit
     const int64_t* targets;
-    // d logits into out.C
+    // d logits into out.C, in units of a value of dloss (loss_unit); launch_nn, launch_tn: the sums are in units of it
+    // where dloss_rows > 0, and so is what goes to `part`
     const float* lse;
     const float* dloss;
+    int64_t dloss_rows;
     int64_t vocab, col0;     // size of the vocabulary; its first column in this piece
 };
 
@@ -72,9 +74,9 @@ hipError_t launch_rows(Epi epi, int64_t rows, TileArgs a, hipStream_t stream);
 hipError_t launch_nn(Tile t, TileArgs a, hipStream_t stream);
 hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream);
 
-// out = epilogue of the sum over splits of part[s][row][col]
+// out = epilogue of the sum over splits of part[s][row][col], in units of a value of dloss where dloss_rows > 0
 hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
-                       hipStream_t stream);
+                       hipStream_t stream, const float* dloss = nullptr, int64_t dloss_rows = 0);
 
 // d (M, ldd) = dC act'(pre), columns [N, ldd) zero (d may be null); dbias: null, or with colsum_rows(M) == 1 the
 // column sums of the unrounded products, with more colsum gets [colsum_rows(M)][N] partial ones in fp32

@@ -65,13 +65,13 @@ __device__ bool find_rows(const int32_t* ends, int E, int64_t limit, int bm, int
 // Eight columns of a row, summed: what follows the product.
 template <int EPI, int LPR>
 __device__ __forceinline__ void finish8(const TileArgs& a, int64_t mrow, bool valid, int64_t col, int64_t slot, int lane,
-                                        float* x)
+                                        float* x, float unit)
 {
     const int n = (int)max((int64_t)0, min((int64_t)8, a.N - col));
     if constexpr (EPI == kEpiStat) {
         stat8<LPR>(a, mrow, a.M, col, n, slot, lane, x);
     } else if constexpr (EPI == kEpiGrad) {
-        grad8(a, mrow, a.M, col, n, x);
+        grad8(a, mrow, a.M, col, n, x, unit);
     } else if (valid && n > 0) {
         linear8(a.out, mrow, col, n, x);
     }
@@ -115,6 +115,7 @@ __global__ __launch_bounds__(W * 64, 1) void rows_kernel(TileArgs a)
     const int steps = (int)((K + 63) / 64);
     const uint32_t frag = r16 * 128 + wave * SLOT, sw = swz(r16);
 
+    const float sample = EPI == kEpiGrad ? loss_sample(a.dloss, a.dloss_rows) : 1.0f;
     i32x4 xa[D][FM][2];
     f32x4 acc[FM];
 #pragma unroll
@@ -171,6 +172,7 @@ __global__ __launch_bounds__(W * 64, 1) void rows_kernel(TileArgs a)
     wait_vmcnt0();                   // loads past the last step have landed too
     asm volatile("" ::: "memory");
 
+    const float counted = EPI == kEpiGrad ? loss_unit(sample) : 1.0f;
     // lane l has row l % 16 and four columns from 4 (l / 16) of each 16 x 16 block; block row i of a wave goes
     // to its part of stage i, 16-byte units swizzled by the row
     constexpr uint32_t UM = BN / 4 - 1;
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(W * 64, 1) void rows_kernel(TileArgs a)
             x1 += *unit(w, i, r, c + 1);
         }
         float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-        finish8<EPI, LPR>(a, row0 + i * 16 + r, i * 16 + r < rows, n0 + c * 4, blockIdx.x, lane, x);
+        finish8<EPI, LPR>(a, row0 + i * 16 + r, i * 16 + r < rows, n0 + c * 4, blockIdx.x, lane, x, counted);
     }
 }
 
@@ -230,6 +232,7 @@ __global__ __launch_bounds__(NT, 2) void rows_wide_kernel(TileArgs a)
     const int32_t r16 = lane & 15;
     const uint32_t sw = swz(r16);
 
+    const float sample = EPI == kEpiGrad ? loss_sample(a.dloss, a.dloss_rows) : 1.0f;
     f32x4 acc[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -273,6 +276,7 @@ __global__ __launch_bounds__(NT, 2) void rows_wide_kernel(TileArgs a)
     wait_vmcnt0();                   // loads past the last step have landed too
     barrier_after_lds_write();
 
+    const float counted = EPI == kEpiGrad ? loss_unit(sample) : 1.0f;
     // 16 rows a stage, 16-byte units swizzled by the row
     auto unit = [&](int i, int r, int u) { return reinterpret_cast<f32x4*>(stage(i) + r * 256 + ((u ^ r) * 16)); };
 #pragma unroll
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(NT, 2) void rows_wide_kernel(TileArgs a)
         const int u = tid & 127, r = u >> 3, c = (u & 7) * 2;
         const f32x4 x0 = *unit(i, r, c), x1 = *unit(i, r, c + 1);
         float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-        finish8<EPI, 8>(a, row0 + i * 16 + r, i * 16 + r < rows, n0 + c * 4, blockIdx.x, lane, x);
+        finish8<EPI, 8>(a, row0 + i * 16 + r, i * 16 + r < rows, n0 + c * 4, blockIdx.x, lane, x, counted);
     }
 }
 

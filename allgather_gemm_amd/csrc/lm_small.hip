@@ -15,8 +15,10 @@ namespace {
 // theirs), so that enough loads are in flight: 64 splits of 33 x 1024 took 20 us with L = 1.  u0: the launch's first unit.
 template <int L>
 __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits, int64_t M, int64_t N, int64_t ldp,
-                                                  LinearOut out, int64_t u0)
+                                                  LinearOut out, int64_t u0, const float* dloss,
+                                                  int64_t dloss_rows)
 {
+    const float unit = loss_unit(loss_sample(dloss, dloss_rows));
     constexpr int U = NT / L;                      // units of a workgroup
     __shared__ f32x4 s_sum[L > 1 ? L - 1 : 1][U][2];
     const int64_t units = ldp / 8;
@@ -48,7 +50,8 @@ __global__ __launch_bounds__(NT) void join_kernel(const float* part, int splits,
             s1 += s_sum[l][ul][1];
         }
     }
-    float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+    float x[8] = {s0[0] * unit, s0[1] * unit, s0[2] * unit, s0[3] * unit,
+                  s1[0] * unit, s1[1] * unit, s1[2] * unit, s1[3] * unit};
     const int n = (int)min((int64_t)8, N - col);
     if (!there || n <= 0)
         return;
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(NT) void xent_join_kernel(const float* stat, int64_
 }  // namespace
 
 hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int64_t ldp, const LinearOut& out,
-                       hipStream_t stream)
+                       hipStream_t stream, const float* dloss, int64_t dloss_rows)
 {
     const int64_t units = M * (ldp / 8);
     if (units <= 0)
@@ -209,11 +212,11 @@ hipError_t launch_join(const float* part, int splits, int64_t M, int64_t N, int6
         const dim3 grid((unsigned)std::min(groups - g, kMostWorkgroups));
         const int64_t u0 = g * (NT / L);
         if (L == 16)
-            join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+            join_kernel<16><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0, dloss, dloss_rows);
         else if (L == 4)
-            join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+            join_kernel<4><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0, dloss, dloss_rows);
         else
-            join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0);
+            join_kernel<1><<<grid, dim3(NT), 0, stream>>>(part, splits, M, N, ldp, out, u0, dloss, dloss_rows);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;

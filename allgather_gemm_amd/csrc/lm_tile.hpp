@@ -567,16 +567,32 @@ __device__ __forceinline__ void stat8(const TileArgs& a, int64_t mrow, int64_t M
     }
 }
 
-// d logits = dloss (softmax - one at the target), rounded to bf16 for the products that follow (each is a
-// sum of many such terms, and 2^-9 of a term is what the products' other operand is rounded to);
-// padding columns of the buffer are zero.
-__device__ __forceinline__ void grad8(const TileArgs& a, int64_t mrow, int64_t M, int64_t col, int n, const float* x)
+// d logits are rounded to bf16 for the products that follow, whose matrix instructions take both factors so.  They are
+// counted in units of one of dloss's values, which multiplies the sums: where all rows have the same (a mean's 1 / n),
+// what is rounded is softmax - 1 at the targets, next to -1 and exact there, and not -1 / n, whose error every row would
+// have alike (the gradients' norm was up to 2^-8 too large or too small).  The unit is the first of 64 evenly spread
+// rows' values between 2^-40 and 2^40, or 1.  What a lane has read of them, loaded ahead of its use:
+__device__ __forceinline__ float loss_sample(const float* dloss, int64_t rows)
+{
+    return rows > 0 ? fabsf(dloss[(int64_t)(threadIdx.x & 63) * rows >> 6]) : 1.0f;
+}
+// All lanes of the wave.
+__device__ __forceinline__ float loss_unit(float sample)
+{
+    const uint64_t fit = __ballot(sample >= 0x1p-40f && sample <= 0x1p40f);
+    return fit ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sample), __builtin_ctzll(fit)))
+               : 1.0f;
+}
+
+// d logits = dloss / unit (softmax - one at the target); padding columns of the buffer are zero.
+__device__ __forceinline__ void grad8(const TileArgs& a, int64_t mrow, int64_t M, int64_t col, int n, const float* x,
+                                      float unit)
 {
     if (mrow >= M || col >= a.out.ldc)
         return;
     const int64_t y = a.targets[mrow];
     const bool has = y >= 0 && y < a.vocab;
-    const float lse = a.lse[mrow], w = has ? a.dloss[mrow] : 0.0f;
+    const float lse = a.lse[mrow], w = has ? a.dloss[mrow] / unit : 0.0f;
     const int64_t hit = y - a.col0 - col;
     bf16x8 o;
 #pragma unroll
@@ -701,8 +717,8 @@ __device__ __forceinline__ void half_slab_out(const char* slab, __bf16* p, int64
     __builtin_amdgcn_wave_barrier();
 }
 
-// d logits of the same block, w (softmax - one at the target), rounded to bf16 for the products that follow;
-// zero in rows without a target.  neg_lse2: -lse log2(e).
+// d logits of the same block, w (softmax - one at the target) with w = dloss / unit, rounded to bf16; zero in rows
+// without a target.  neg_lse2: -lse log2(e).
 template <int FN>
 __device__ __forceinline__ void grad_block(const TileArgs& a, const f32x16* acc, char* slab, int64_t ldc, int64_t row0, int64_t rows,
                                            int64_t col0, int n, int yo, bool has, float neg_lse2, float w, int lane)
@@ -870,7 +886,8 @@ struct Where {
 };
 
 // One tile.  EPI: kEpiLinear, kEpiSum (the sums alone: a kernel without the activations' code
-// takes 37 us instead of 41 for 16384 x 4096 x 8), kEpiStat (softmax statistics of a row's columns), kEpiGrad (d logits).
+// takes 37 us instead of 41 for 16384 x 4096 x 8), kEpiScaled (the sums times the unit of the d logits), kEpiStat (softmax
+// statistics of a row's columns), kEpiGrad (d logits).
 template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
 __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>& l, const Where& w)
 {
@@ -880,7 +897,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
     typedef Side<BN, TB> SB;
     constexpr int ND = SA::OPS + SB::OPS;
     constexpr int WNC = FN * 32;                       // columns of a wave's block
-    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum;
+    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum || EPI == kEpiScaled;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -922,7 +939,9 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
         // cross entropy: what a lane's rows need in the epilogue is on its way during the K loop
         const uint32_t fr = lane & 31;
         int64_t target[FM];
-        float row_lse[FM], row_w[FM];
+        float row_lse[FM], row_w[FM], sample = 1.0f;
+        if constexpr (EPI == kEpiGrad || EPI == kEpiScaled)
+            sample = loss_sample(a.dloss, a.dloss_rows);
         if constexpr (!LIN) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
@@ -1113,18 +1132,21 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
             const int c8 = (el % (WNC / 8)) * 8, n = min(8, wcols - c8);
             if (EPI == kEpiLinear && a.out.bias && n > 0)
                 load8(a.out.bias + wcol + c8, n, bias);
-            if (a.plain) {
+            if (EPI == kEpiScaled || a.plain) {
+                const float unit = EPI == kEpiScaled ? loss_unit(sample) : 1.0f;
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     int cols = wcols;
                     one_block(acc[i], el, cols);
+                    auto value = [&](int j, int e) {
+                        return (__bf16)(EPI == kEpiScaled ? acc[i][j][e] * unit : acc[i][j][e]);
+                    };
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             *half_slab_at<FN>(slab, j, q, el & 31, (uint32_t)el >> 5) =
-                                bf16x4{(__bf16)acc[i][j][q * 4 + 0], (__bf16)acc[i][j][q * 4 + 1],
-                                       (__bf16)acc[i][j][q * 4 + 2], (__bf16)acc[i][j][q * 4 + 3]};
+                                bf16x4{value(j, q * 4 + 0), value(j, q * 4 + 1), value(j, q * 4 + 2), value(j, q * 4 + 3)};
                     half_slab_out<FN, true>(slab, C + i * WM * 32 * ldc, ldc, M - mrow0 - i * WM * 32, cols, el);
                 }
             } else {
@@ -1151,6 +1173,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
                 }
             }
         } else {
+            const float unit = EPI == kEpiGrad ? loss_unit(sample) : 1.0f;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 int cols = wcols;
@@ -1168,7 +1191,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
                 } else {
                     const bool has = target[i] >= 0 && target[i] < a.vocab;
                     grad_block<FN>(a, acc[i], slab, ldc, brow, M, wcol, cols, yo, has, -row_lse[i] * 1.4426950408889634f,
-                                   row_w[i], el);
+                                   row_w[i] / unit, el);
                 }
             }
         }

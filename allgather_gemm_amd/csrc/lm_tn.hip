@@ -5,30 +5,39 @@ namespace ag {
 namespace lm {
 namespace {
 
+template <int EPI>
 __global__ __launch_bounds__(NT, 1) void tn256_kernel(TileArgs a)
 {
-    tile_body<256, 256, 2, 2, 2, true, true, kEpiSum, true>(a);
+    tile_body<256, 256, 2, 2, 2, true, true, EPI, true>(a);
 }
 
+template <int EPI>
 __global__ __launch_bounds__(NT, 1) void tn128_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 4, true, true, kEpiSum, false>(a);
+    tile_body<128, 128, 2, 2, 4, true, true, EPI, false>(a);
 }
 
+template <int EPI>
 __global__ __launch_bounds__(NT, 4) void tnshort_kernel(TileArgs a)
 {
-    tile_body<128, 128, 2, 2, 1, true, true, kEpiSum, false>(a);
+    tile_body<128, 128, 2, 2, 1, true, true, EPI, false>(a);
+}
+
+template <int EPI>
+hipError_t launch(Tile t, TileArgs& a, hipStream_t stream)
+{
+    switch (t) {
+    case kTile256: return launch_tiles(tn256_kernel<EPI>, 128, 256, 1, a, stream);
+    case kTileShort: return launch_tiles(tnshort_kernel<EPI>, 128, 128, kEachTile, a, stream);
+    default: return launch_tiles(tn128_kernel<EPI>, 128, 128, 1, a, stream);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_tn(Tile t, TileArgs a, hipStream_t stream)
 {
-    switch (t) {
-    case kTile256: return launch_tiles(tn256_kernel, 128, 256, 1, a, stream);
-    case kTileShort: return launch_tiles(tnshort_kernel, 128, 128, kEachTile, a, stream);
-    default: return launch_tiles(tn128_kernel, 128, 128, 1, a, stream);
-    }
+    return a.dloss_rows > 0 && !a.part ? launch<kEpiScaled>(t, a, stream) : launch<kEpiSum>(t, a, stream);
 }
 
 }  // namespace lm

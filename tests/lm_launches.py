@@ -14,7 +14,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["lm_api", "lm_nt", "lm_nn", "lm_tn", "lm_rows", "lm_small"]
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
-# kernel: its name and template arguments ("nt256<1>"), as the source has them; args: M, N, K and what else the
+# kernel: its name and template arguments ("nt256<1>"), as the source has them, or "nn256", "nn256 scaled"; args: M, N, K and what else the
 # product's arguments say (None for kernels that are no product)
 Launch = collections.namedtuple("Launch", "kernel grid block args")
 Args = collections.namedtuple("Args", "M N K group E splits part accumulate")
@@ -57,6 +57,8 @@ def recorder():
 
 def _kernel(mangled):
     name, targs = re.match(r".*_GLOBAL__N_1\d+(\w+?)_kernel(?:I((?:L[ib]\d+E)+)E)?", mangled).groups()
+    if name[:2] in ("nn", "tn"):         # the sums alone, or times the unit of the d logits
+        return name + {"Li3E": "", "Li4E": " scaled"}[targs]
     return name + ("<%s>" % ",".join(re.findall(r"L[ib](\d+)E", targs)) if targs else "")
 
 
