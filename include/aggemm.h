@@ -272,9 +272,8 @@ int gemm_xent(const void *A, const void *B, const int64_t *targets, int64_t T, i
  * D[t,v] = dloss[t] (exp(a_t . b_v - lse[t]) - [v = y]),  dA = D B (T, K),  dB = D^T A (V, K).
  * D is formed a piece of the vocabulary at a time, rounded to bf16 in units of one of dloss's values, by
  * which the sums are multiplied: a dloss common to all rows is not rounded with it.
- * gemm_xent_bwd_workspace() asks for pieces of
- * up to 512 MiB, and a smaller workspace, down to 256 columns a piece, only makes more of them.  dA or
- * dB may be NULL.
+ * gemm_xent_bwd_workspace() asks for pieces of up to 512 MiB, and a smaller workspace, down to 256
+ * columns a piece, only makes more of them.  dA or dB may be NULL.
  */
 int64_t gemm_xent_bwd_workspace(int64_t T, int64_t V, int64_t K);
 int gemm_xent_bwd(const float *dloss, const void *A, const void *B, const int64_t *targets,
