@@ -89,8 +89,15 @@ def lib() -> ctypes.CDLL:
         L.gemm_grouped_bwd.argtypes = [_vp] * 4 + [_i32] + [_i64] * 3 + [_vp, _vp, _vp]
         L.gemm_xent.argtypes = [_vp] * 3 + [_i64] * 3 + [_vp] * 3 + [_i64, _vp]
         L.gemm_xent_bwd.argtypes = [_vp] * 5 + [_i64] * 3 + [_vp] * 3 + [_i64, _vp]
+        L.layer_norm.argtypes = [_vp] * 4 + [_i64] * 2 + [ctypes.c_float] + [_vp] * 5
+        L.layer_norm_bwd_workspace.argtypes = [_i64] * 2
+        L.layer_norm_bwd_workspace.restype = _i64
+        L.layer_norm_bwd.argtypes = [_vp] * 6 + [_i64] * 2 + [_vp] * 4 + [_i64, _vp]
+        L.newton_schulz_workspace.argtypes = [_i64] * 3
+        L.newton_schulz_workspace.restype = _i64
+        L.newton_schulz.argtypes = [_vp, _i32] + [_i64] * 3 + [_vp, _i32, ctypes.c_float, _vp, _vp, _i64, _vp]
         for name in ("gemm_bias_act", "gemm_bias_act_bwd", "gemm_grouped", "gemm_grouped_bwd", "gemm_xent",
-                     "gemm_xent_bwd"):
+                     "gemm_xent_bwd", "layer_norm", "layer_norm_bwd", "newton_schulz"):
             getattr(L, name).restype = ctypes.c_int
         L.ag_check.argtypes = [_vp, ctypes.POINTER(_i64)]
         L.ag_check.restype = ctypes.c_int
@@ -304,6 +311,7 @@ def tgather(shards, valid_rows: int, valid_cols: int, dst: torch.Tensor | None =
 
 # ------------------------------------------------------------------------ language-model operators
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+TYPE_BF16, TYPE_F32 = 0, 1
 _ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
 
 
@@ -509,6 +517,92 @@ def gemm_xent_bwd(dloss: torch.Tensor, A: torch.Tensor, B: torch.Tensor, targets
         w = torch.empty(n, dtype=torch.uint8, device=dev)
     _done(lib().gemm_xent_bwd(g, a, b, y, ls, T, V, K, _p(dA), _p(dB), _p(w), n, _stream_of(dev)), "gemm_xent_bwd")
     return dA, dB
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               residual: torch.Tensor | None = None, y: torch.Tensor | None = None, h: torch.Tensor | None = None,
+               mean: torch.Tensor | None = None, rstd: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y (rows, width) = (s - mean) rstd weight + bias over each row of s = x, or of x + residual rounded to bf16.  x, residual
+    (rows, width), weight, bias (width) bf16.  Optional outputs, which layer_norm_bwd needs: h (rows, width) bf16 receives
+    the sum (it may be x or residual itself; without a residual s is x), mean and rstd (rows,) fp32 the statistics.  y, h, mean
+    and rstd, where given, are written in place; the result has no gradient function."""
+    rows, width = _dims(x, "x", 2)
+    dev = x.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return layer_norm(x, weight, bias, eps, residual, y, h, mean, rstd)
+    if h is not None and residual is None:
+        raise ValueError("h receives x + residual: without a residual there is nothing to keep")
+    xp, rp = _need(x, "x", (rows, width)), _need(residual, "residual", (rows, width), device=dev)
+    wp, bp = _need(weight, "weight", (width,), device=dev), _need(bias, "bias", (width,), device=dev)
+    hp = _need(h, "h", (rows, width), device=dev)
+    mp, sp = _need(mean, "mean", (rows,), torch.float32, dev), _need(rstd, "rstd", (rows,), torch.float32, dev)
+    out = x.new_empty((rows, width)) if y is None else y
+    yp = _need(out, "y", (rows, width), device=dev)
+    _done(lib().layer_norm(xp, rp, wp, bp, rows, width, eps, yp, hp, mp, sp, _stream_of(dev)), "layer_norm")
+    for t in (y, h, mean, rstd):
+        _written(t)
+    return out
+
+
+def layer_norm_bwd(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   weight: torch.Tensor | None = None, dh: torch.Tensor | None = None, need_dx: bool = True,
+                   need_dweight: bool = True, need_dbias: bool = True, stream=None):
+    """Gradients of layer_norm: (dx (rows, width), dweight (width), dbias (width)) for dy (rows, width), None where not needed.
+    h: what was normalised (layer_norm's h, or its x without a residual), mean and rstd as it wrote them.  dx is the gradient
+    of x and of residual; dh, the gradient that reaches h on its other way, is added to it."""
+    rows, width = _dims(h, "h", 2)
+    dev = h.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return layer_norm_bwd(dy, h, mean, rstd, weight, dh, need_dx, need_dweight, need_dbias)
+    dyp, hp = _need(dy, "dy", (rows, width), device=dev), _need(h, "h", (rows, width))
+    mp, sp = _need(mean, "mean", (rows,), torch.float32, dev), _need(rstd, "rstd", (rows,), torch.float32, dev)
+    wp, dhp = _need(weight, "weight", (width,), device=dev), _need(dh, "dh", (rows, width), device=dev)
+    dx = torch.empty_like(h) if need_dx else None
+    dweight = h.new_empty((width,)) if need_dweight else None
+    dbias = h.new_empty((width,)) if need_dbias else None
+    w, n = _work("layer_norm_bwd", dev, rows, width) if need_dweight or need_dbias else (None, 0)
+    _done(lib().layer_norm_bwd(dyp, hp, mp, sp, wp, dhp, rows, width, _p(dx), _p(dweight), _p(dbias), _p(w), n,
+                               _stream_of(dev)), "layer_norm_bwd")
+    return dx, dweight, dbias
+
+
+# (a, b, c) of five steps that take singular values from about 0.003 of a matrix's norm on to between 0.7 and 1.2
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+@functools.lru_cache(maxsize=256)
+def _steps(coefficients: tuple):
+    return (ctypes.c_float * (3 * len(coefficients)))(*[x for abc in coefficients for x in abc])
+
+
+def newton_schulz(G: torch.Tensor, coefficients=NEWTON_SCHULZ, eps: float = 1e-7, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """G (R, C) or each matrix of G (E, R, C), bf16 or fp32, made nearly orthogonal: X = G / (|G| + eps), then for each step's
+    (a, b, c) X = a X + (b A + c A A) X with A = X X^T (from the right where R > C).  out: bf16, G's shape; it may be G
+    itself where that is bf16.  Written in place where given; the result has no gradient function.  Coefficients under which
+    X could grow past fp16 are refused (aggemm.h has the bounds)."""
+    if G.dim() not in (2, 3):
+        raise ValueError("G must have 2 or 3 dimensions")
+    if G.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("G must be bfloat16 or float32, not %s" % G.dtype)
+    dev = G.device
+    if _elsewhere(stream, dev):
+        with _on(stream, dev):
+            return newton_schulz(G, coefficients, eps, out)
+    coefficients = tuple(tuple(float(x) for x in abc) for abc in coefficients)
+    if not coefficients or any(len(abc) != 3 for abc in coefficients):
+        raise ValueError("coefficients must be (a, b, c) for each of at least one step")
+    E, R, C = (1,) * (3 - G.dim()) + tuple(G.shape)
+    g = _need(G, "G", G.shape, G.dtype)
+    res = torch.empty(G.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    o = _need(res, "out", G.shape, device=dev)
+    w, n = _work("newton_schulz", dev, E, R, C)
+    _done(lib().newton_schulz(g, TYPE_F32 if G.dtype == torch.float32 else TYPE_BF16, E, R, C, _steps(coefficients),
+                              len(coefficients), eps, o, _p(w), n, _stream_of(dev)), "newton_schulz")
+    _written(out)
+    return res
 
 
 def check(stream=None) -> tuple[int, list[int]]:

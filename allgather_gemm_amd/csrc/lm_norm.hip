@@ -1,0 +1,628 @@
+// lm_norm.hip -- layer norm over rows, with the residual stream added in front, and its gradients: kernels and entry
+// points.  All of it is bound by the bytes it moves.
+//
+//   h = bf16(x + residual),  m = mean(h),  r = 1 / sqrt(mean((h - m)^2) + eps),  y = (h - m) r w + b
+//   xh = (h - m) r,  g = dy w:   dx = r (g - mean(g) - xh mean(g xh)) + dh,  dw = sum dy xh,  db = sum dy
+//
+// A row stays in registers between its one read and its one write: TPR threads have it in C pieces of eight columns each,
+// so mean and variance are two sums over the same values and the variance is that of differences from the mean.  Rows
+// wider than that go through memory (the caches) once for each sum.
+#include "../../include/aggemm.h"
+#include "ag_internal.hpp"
+#include "lm_tile.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace ag {
+namespace lm {
+namespace {
+
+constexpr int kNormWidest = 16384;     // columns of a row in registers
+
+struct NormArgs {
+    const __bf16 *x, *residual, *w, *b;
+    int64_t rows;
+    int width;
+    float eps;
+    __bf16 *y, *h;
+    float *mean, *rstd;
+};
+
+struct NormBwdArgs {
+    const __bf16 *dy, *h, *w, *dh;
+    const float *mean, *rstd;
+    int64_t rows;
+    int width;
+    __bf16* dx;
+    __bf16 *dw, *db;         // written by the kernel itself where one workgroup (row of them) has all rows
+    float* part;             // [2][parts][width]: partial sums of dw and db; null: neither is wanted
+    int64_t parts;
+};
+
+// The eight columns of a thread's piece, which may start anywhere: their last n are loaded from `lo` on, so that what is read
+// ends with the row, and moved down by the s = 8 - n others, which come out as zeros.  No lane takes a way of its own (eight
+// loads of one element each were that, and the registers for them).
+struct Piece {
+    int lo, s;
+    __device__ __forceinline__ Piece(int col, int width) : lo(min(col, width - 8)), s(min(col - lo, 8)) {}
+    __device__ __forceinline__ int n() const { return 8 - s; }
+    __device__ __forceinline__ bf16x8 take(const __bf16* row) const
+    {
+        i32x4 v = *reinterpret_cast<const i32x4_any*>(row + lo);
+        if (s & 8)
+            v = i32x4{};
+        if (s & 4)
+            v = i32x4{v[2], v[3], 0, 0};
+        if (s & 2)
+            v = i32x4{v[1], v[2], v[3], 0};
+        if (s & 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = (int)((uint32_t)v[i] >> 16 | (i < 3 ? (uint32_t)v[i < 3 ? i + 1 : i] << 16 : 0u));
+        return __builtin_bit_cast(bf16x8, v);
+    }
+};
+
+// Eight columns of rows of any length, zeros past the n that are valid.
+__device__ __forceinline__ bf16x8 take8(const __bf16* p, int n)
+{
+    if (n >= 8)
+        return *reinterpret_cast<const bf16x8_any*>(p);
+    bf16x8 v = load8_few(p, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = e < n ? v[e] : (__bf16)0.0f;
+    return v;
+}
+
+__device__ __forceinline__ void give8(__bf16* p, int n, bf16x8 v)
+{
+    if (n >= 8) {
+        *reinterpret_cast<bf16x8_any*>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            p[e] = v[e];
+}
+
+__device__ __forceinline__ bf16x8 ones()
+{
+    const __bf16 x = (__bf16)1.0f;
+    return bf16x8{x, x, x, x, x, x, x, x};
+}
+
+// (a, b) summed over the TPR threads of a row; every one of them gets the sums.  `turn` counts the sums taken: two
+// buffers in turn need one barrier each, for whoever writes one again has passed the barrier behind its last reads.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*s_sum)[16], int& turn)
+{
+#pragma unroll
+    for (int s = 1; s < (TPR < 64 ? TPR : 64); s <<= 1) {
+        a += __shfl_xor(a, s);
+        b += __shfl_xor(b, s);
+    }
+    if constexpr (TPR > 64) {
+        float2* const buf = s_sum[turn++ & 1];
+        if ((threadIdx.x & 63) == 0)
+            buf[threadIdx.x >> 6] = make_float2(a, b);
+        barrier_after_lds_write();
+        a = b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) {
+            a += buf[i].x;
+            b += buf[i].y;
+        }
+    }
+    return make_float2(a, b);
+}
+
+template <int TPR>
+constexpr int kThreads = TPR > 256 ? TPR : 256;
+
+// ------------------------------------------------------------------------------------------ forward
+template <int TPR, int C>
+__global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a)
+{
+    constexpr int RPW = kThreads<TPR> / TPR;            // rows of a workgroup at a time
+    __shared__ float2 s_sum[2][16];
+    int turn = 0;
+    const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
+    bf16x8 w[C], b[C];
+    auto piece = [&](int c) { return Piece((c * TPR + t) * 8, a.width); };
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        w[c] = a.w ? piece(c).take(a.w) : ones();
+        b[c] = a.b ? piece(c).take(a.b) : bf16x8{};
+    }
+    const float count = (float)a.width;
+    for (int64_t row = blockIdx.x * (int64_t)RPW + rl; row < a.rows; row += gridDim.x * (int64_t)RPW) {
+        const int64_t at = row * a.width;
+        bf16x8 v[C], r[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            v[c] = piece(c).take(a.x + at);
+        if (a.residual) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                r[c] = piece(c).take(a.residual + at);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[c][e] = (__bf16)((float)v[c][e] + (float)r[c][e]);
+            if (a.h) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    give8(a.h + at + (c * TPR + t) * 8, piece(c).n(), v[c]);
+            }
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += (float)v[c][e];
+        const float mean = row_sum<TPR>(sum, 0.0f, s_sum, turn).x / count;
+        float sq = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = e < piece(c).n() ? (float)v[c][e] - mean : 0.0f;
+                sq = fmaf(d, d, sq);
+            }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, 0.0f, s_sum, turn).x / count + a.eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            bf16x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = (__bf16)fmaf(((float)v[c][e] - mean) * rstd, (float)w[c][e], (float)b[c][e]);
+            give8(a.y + at + (c * TPR + t) * 8, piece(c).n(), o);
+        }
+        if (t == 0) {
+            if (a.mean)
+                a.mean[row] = mean;
+            if (a.rstd)
+                a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Rows wider than kNormWidest: a workgroup of 1024 threads a row, three times over it.  A thread sees the same columns each
+// time, and where h is kept reads the sum back from there (h may be x's or residual's own buffer).
+__global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a)
+{
+    constexpr int TPR = 1024;
+    __shared__ float2 s_sum[2][16];
+    int turn = 0;
+    const float count = (float)a.width;
+    const bool add = a.residual != nullptr, kept = add && a.h;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const int64_t at = row * a.width;
+        auto sum_at = [&](int col, int n) {
+            bf16x8 v = take8(a.x + at + col, n);
+            if (add) {
+                const bf16x8 r = take8(a.residual + at + col, n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = (__bf16)((float)v[e] + (float)r[e]);
+            }
+            return v;
+        };
+        auto again = [&](int col, int n) { return kept ? take8(a.h + at + col, n) : sum_at(col, n); };
+        float sum = 0.0f;
+        for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
+            const int n = min(a.width - col, 8);
+            const bf16x8 v = sum_at(col, n);
+            if (kept)
+                give8(a.h + at + col, n, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += (float)v[e];
+        }
+        const float mean = row_sum<TPR>(sum, 0.0f, s_sum, turn).x / count;
+        float sq = 0.0f;
+        for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
+            const int n = min(a.width - col, 8);
+            const bf16x8 v = again(col, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = e < n ? (float)v[e] - mean : 0.0f;
+                sq = fmaf(d, d, sq);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, 0.0f, s_sum, turn).x / count + a.eps);
+        for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
+            const int n = min(a.width - col, 8);
+            const bf16x8 v = again(col, n);
+            float w[8], b[8] = {};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = 1.0f;
+            if (a.w)
+                load8(a.w + col, n, w);
+            if (a.b)
+                load8(a.b + col, n, b);
+            bf16x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = (__bf16)fmaf(((float)v[e] - mean) * rstd, w[e], b[e]);
+            give8(a.y + at + col, n, o);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean)
+                a.mean[row] = mean;
+            if (a.rstd)
+                a.rstd[row] = rstd;
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------------------- gradients
+// A workgroup's rows, and its share of the column sums in registers; `part` gets one row of them for each workgroup.
+template <int TPR, int C>
+__global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
+{
+    constexpr int NTH = kThreads<TPR>, RPW = NTH / TPR;
+    __shared__ float2 s_sum[2][16];
+    int turn = 0;
+    const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
+    bf16x8 w[C];
+    float dw[C][8], db[C][8];
+    auto piece = [&](int c) { return Piece((c * TPR + t) * 8, a.width); };
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        w[c] = a.w ? piece(c).take(a.w) : ones();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            dw[c][e] = db[c][e] = 0.0f;
+    }
+    const float count = (float)a.width;
+    for (int64_t row = blockIdx.x * (int64_t)RPW + rl; row < a.rows; row += gridDim.x * (int64_t)RPW) {
+        const int64_t at = row * a.width;
+        bf16x8 dy[C], h[C], dh[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            dy[c] = piece(c).take(a.dy + at);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            h[c] = piece(c).take(a.h + at);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        if (a.dx && a.dh) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                dh[c] = piece(c).take(a.dh + at);
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = ((float)h[c][e] - mean) * rstd, d = (float)dy[c][e];
+                const float g = d * (float)w[c][e];
+                s1 += g;
+                s2 = fmaf(g, xh, s2);
+                dw[c][e] = fmaf(d, xh, dw[c][e]);
+                db[c][e] += d;
+            }
+        if (!a.dx)
+            continue;
+        const float2 s = row_sum<TPR>(s1, s2, s_sum, turn);
+        const float m1 = s.x / count, m2 = s.y / count;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            bf16x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = ((float)h[c][e] - mean) * rstd, g = (float)dy[c][e] * (float)w[c][e];
+                o[e] = (__bf16)fmaf(rstd, g - m1 - xh * m2, a.dh ? (float)dh[c][e] : 0.0f);
+            }
+            give8(a.dx + at + (c * TPR + t) * 8, piece(c).n(), o);
+        }
+    }
+    if (!a.part)
+        return;
+    float* const out = a.part + blockIdx.x * (int64_t)a.width;
+    const int64_t second = a.parts * a.width;              // from dw's sums to db's
+    if constexpr (TPR >= 256) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < piece(c).n()) {
+                    const int col = (c * TPR + t) * 8 + e;
+                    out[col] = dw[c][e];
+                    out[second + col] = db[c][e];
+                }
+    } else {
+        // rows that lanes of a wave have side by side, then those of the four waves
+        __shared__ float s_col[4][TPR * C * 8];
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v = k ? db[c][e] : dw[c][e];
+#pragma unroll
+                    for (int s = TPR; s < 64; s <<= 1)
+                        v += __shfl_xor(v, s);
+                    if ((threadIdx.x & 63) < TPR)
+                        s_col[wave][(c * TPR + t) * 8 + e] = v;
+                }
+            barrier_after_lds_write();
+            for (int col = threadIdx.x; col < a.width; col += NTH)
+                out[k * second + col] = (s_col[0][col] + s_col[1][col]) + (s_col[2][col] + s_col[3][col]);
+            barrier_after_lds_write();
+        }
+    }
+}
+
+// dx of rows wider than kNormWidest
+__global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdArgs a)
+{
+    constexpr int TPR = 1024;
+    __shared__ float2 s_sum[2][16];
+    int turn = 0;
+    const float count = (float)a.width;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const int64_t at = row * a.width;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        auto values = [&](int col, int n, float* g, float* xh) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = 1.0f;
+            load8(a.dy + at + col, n, g);
+            load8(a.h + at + col, n, xh);
+            if (a.w)
+                load8(a.w + col, n, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                g[e] *= w[e];
+                xh[e] = (xh[e] - mean) * rstd;
+            }
+        };
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
+            float g[8], xh[8];
+            values(col, min(a.width - col, 8), g, xh);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s1 += g[e];
+                s2 = fmaf(g[e], xh[e], s2);
+            }
+        }
+        const float2 s = row_sum<TPR>(s1, s2, s_sum, turn);
+        const float m1 = s.x / count, m2 = s.y / count;
+        for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
+            const int n = min(a.width - col, 8);
+            float g[8], xh[8], dh[8] = {};
+            values(col, n, g, xh);
+            if (a.dh)
+                load8(a.dh + at + col, n, dh);
+            bf16x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = (__bf16)fmaf(rstd, g[e] - m1 - xh[e] * m2, dh[e]);
+            give8(a.dx + at + col, n, o);
+        }
+    }
+}
+
+// Column sums of rows wider than kNormWidest: 256 columns a workgroup (32 lanes of eight), eight rows at a time out of a
+// chunk of them.
+__global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a, int64_t chunk)
+{
+    __shared__ float s_sum[8][256 + 8];
+    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int col = blockIdx.x * 256 + cl * 8;
+    const int n = min(max(a.width - col, 0), 8);
+    const int64_t r0 = blockIdx.y * chunk, r1 = min(a.rows, r0 + chunk);
+    float dw[8] = {}, db[8] = {};
+    if (n > 0)
+        for (int64_t row = r0 + rl; row < r1; row += 8) {
+            float d[8], h[8];
+            load8(a.dy + row * a.width + col, n, d);
+            load8(a.h + row * a.width + col, n, h);
+            const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[e] = fmaf(d[e], (h[e] - mean) * rstd, dw[e]);
+                db[e] += d[e];
+            }
+        }
+    const int mine = blockIdx.x * 256 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s_sum[rl][cl * 8 + e] = k ? db[e] : dw[e];
+        barrier_after_lds_write();
+        if (mine < a.width) {
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                s += s_sum[r][threadIdx.x];
+            a.part[(k * a.parts + blockIdx.y) * a.width + mine] = s;
+        }
+        barrier_after_lds_write();
+    }
+}
+
+// dw and db from their partial sums: 32 columns of a workgroup, each summed by eight threads.
+__global__ __launch_bounds__(256) void norm_join_kernel(const float* part, int64_t parts, int width, __bf16* dw, __bf16* db)
+{
+    __shared__ float s_sum[8][32];
+    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + cl;
+    __bf16* const out = blockIdx.y ? db : dw;
+    if (!out)
+        return;
+    const float* p = part + blockIdx.y * parts * width + col;
+    float s = 0.0f;
+    if (col < width) {
+#pragma unroll 8
+        for (int64_t r = rl; r < parts; r += 8)
+            s += p[r * width];
+    }
+    s_sum[rl][cl] = s;
+    barrier_after_lds_write();
+    if (rl == 0 && col < width) {
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+            s += s_sum[r][cl];
+        out[col] = (__bf16)s;
+    }
+}
+
+// rows of less than one piece go the way of the widest ones
+bool in_registers(int64_t width) { return width >= 8 && width <= kNormWidest; }
+
+int64_t cus()
+{
+    int n = 0;
+    if (device_cus(&n) != hipSuccess || n <= 0)
+        n = 256;
+    return n;
+}
+
+// f(TPR, C) with the threads and pieces for rows of `width` <= kNormWidest columns
+template <typename F>
+auto by_width(int64_t width, F f)
+{
+    using std::integral_constant;
+#define AG_NORM(TPR, C) return f(integral_constant<int, TPR>(), integral_constant<int, C>())
+    if (width <= 128)
+        AG_NORM(16, 1);
+    if (width <= 256)
+        AG_NORM(32, 1);
+    if (width <= 512)
+        AG_NORM(64, 1);
+    if (width <= 1024)
+        AG_NORM(64, 2);
+    if (width <= 2048)
+        AG_NORM(256, 1);
+    if (width <= 4096)
+        AG_NORM(256, 2);
+    if (width <= 8192)
+        AG_NORM(256, 4);
+    AG_NORM(512, 4);
+#undef AG_NORM
+}
+
+int64_t bwd_parts(int64_t rows, int64_t width)
+{
+    if (rows <= 0 || width <= 0)
+        return 0;
+    if (!in_registers(width))
+        return std::min<int64_t>((rows + 31) / 32, 32);
+    return by_width(width, [&](auto tpr, auto) {
+        constexpr int T = decltype(tpr)::value, rpw = kThreads<T> / T;
+        return std::min((rows + rpw - 1) / rpw, cus() * (T > 256 ? 1 : 2));
+    });
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool bad(const void* p, uintptr_t n) { return !p || !aligned(p, n); }
+
+bool norm_too_large(int64_t rows, int64_t width) { return width > 1 << 21 || rows > (int64_t)1 << 30; }
+
+}  // namespace
+}  // namespace lm
+}  // namespace ag
+
+using namespace ag;
+using namespace ag::lm;
+
+#define NORM_HIP(what)                      \
+    do {                                    \
+        const hipError_t e_ = hipGetLastError(); \
+        if (e_ != hipSuccess)               \
+            return hip_error(e_, what);     \
+    } while (0)
+
+extern "C" int layer_norm(const void* x, const void* residual, const void* weight, const void* bias, int64_t rows,
+                          int64_t width, float eps, void* y, void* h, float* mean, float* rstd, void* stream)
+{
+    if (rows < 0 || width < 0 || !(eps >= 0.0f) || std::isinf(eps))
+        return AG_EINVAL;
+    if (rows == 0 || width == 0)
+        return AG_OK;
+    if (bad(x, 16) || bad(y, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(bias, 16) ||
+        !aligned(h, 16) || !aligned(mean, 4) || !aligned(rstd, 4) || (h && !residual))
+        return AG_EINVAL;
+    if (norm_too_large(rows, width))
+        return AG_EUNSUPPORTED;
+    const NormArgs a = {static_cast<const __bf16*>(x), static_cast<const __bf16*>(residual),
+                        static_cast<const __bf16*>(weight), static_cast<const __bf16*>(bias), rows, (int)width, eps,
+                        static_cast<__bf16*>(y), static_cast<__bf16*>(h), mean, rstd};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!in_registers(width))
+        norm_wide_kernel<<<dim3((unsigned)std::min(rows, cus() * 2)), dim3(1024), 0, s>>>(a);
+    else
+        by_width(width, [&](auto tpr, auto c) {
+            constexpr int T = decltype(tpr)::value, C = decltype(c)::value, rpw = kThreads<T> / T;
+            const int64_t grid = std::min((rows + rpw - 1) / rpw, cus() * (T > 256 ? 2 : 8));
+            norm_kernel<T, C><<<dim3((unsigned)grid), dim3(kThreads<T>), 0, s>>>(a);
+        });
+    NORM_HIP("launch layer_norm");
+    return AG_OK;
+}
+
+extern "C" int64_t layer_norm_bwd_workspace(int64_t rows, int64_t width)
+{
+    if (rows < 0 || width < 0 || norm_too_large(rows, width))
+        return 0;
+    return bwd_parts(rows, width) * width * 8;
+}
+
+extern "C" int layer_norm_bwd(const void* dy, const void* h, const float* mean, const float* rstd, const void* weight,
+                              const void* dh, int64_t rows, int64_t width, void* dx, void* dweight, void* dbias, void* work,
+                              int64_t work_bytes, void* stream)
+{
+    if (rows < 0 || width < 0)
+        return AG_EINVAL;
+    if (width == 0)
+        return AG_OK;
+    if ((rows > 0 && (bad(dy, 16) || bad(h, 16) || bad(mean, 4) || bad(rstd, 4))) || !aligned(weight, 16) ||
+        !aligned(dh, 16) || !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(dbias, 16))
+        return AG_EINVAL;
+    if (norm_too_large(rows, width))
+        return AG_EUNSUPPORTED;
+    const int64_t parts = bwd_parts(rows, width);
+    const bool sums = dweight || dbias;
+    if (sums && (work_bytes < parts * width * 8 || (parts > 0 && bad(work, 16))))
+        return AG_EINVAL;
+    if (!dx && !sums)
+        return AG_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const NormBwdArgs a = {static_cast<const __bf16*>(dy), static_cast<const __bf16*>(h), static_cast<const __bf16*>(weight),
+                           static_cast<const __bf16*>(dh), mean, rstd, rows, (int)width, static_cast<__bf16*>(dx),
+                           static_cast<__bf16*>(dweight), static_cast<__bf16*>(dbias),
+                           sums ? static_cast<float*>(work) : nullptr, parts};
+    if (rows > 0 && !in_registers(width)) {
+        if (dx)
+            norm_bwd_wide_kernel<<<dim3((unsigned)std::min(rows, cus() * 2)), dim3(1024), 0, s>>>(a);
+        if (sums)
+            norm_cols_kernel<<<dim3((unsigned)((width + 255) / 256), (unsigned)parts), dim3(256), 0, s>>>(
+                a, (rows + parts - 1) / parts);
+    } else if (rows > 0) {
+        by_width(width, [&](auto tpr, auto c) {
+            constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
+            norm_bwd_kernel<T, C><<<dim3((unsigned)parts), dim3(kThreads<T>), 0, s>>>(a);
+        });
+    }
+    NORM_HIP("launch layer_norm_bwd");
+    if (sums) {
+        norm_join_kernel<<<dim3((unsigned)((width + 31) / 32), 2), dim3(256), 0, s>>>(
+            static_cast<const float*>(work), parts, (int)width, static_cast<__bf16*>(dweight), static_cast<__bf16*>(dbias));
+        NORM_HIP("launch layer_norm join");
+    }
+    return AG_OK;
+}

@@ -1,0 +1,592 @@
+// lm_ortho.hip -- Newton-Schulz orthogonalisation of a matrix or a stack of them: kernels and entry points.
+//
+//   X = G / (|G| + eps), turned so that it is m x n with m <= n; for each (a, b, c):  A = X X^T,  B = b A + c A A,
+//   X = a X + B X.
+//
+// Products by fp16 matrix instructions with fp32 sums: the iterates' singular values stay below a bound that the
+// coefficients give (checked by the entry point), so fp16 with a fixed scale holds them, with three bits more than bf16.
+// What a rounding of X does is not the same everywhere: an error e among X's small left and right singular directions comes
+// out multiplied by the remaining steps' a's (3.4445^4 after the first of five), any other by about one.  Through the products
+// a rounding reaches those directions only as B e or (e X^T) X, both small there; directly it does as a X.  So the
+// iterates are kept as two fp16, value and remainder, as long as the remaining gain is large, the addend a X takes both and the
+// products the value alone.  (Error of 1024 x 1024 with singular values i^-1.5, of the result's norm: with one fp16 1.2e-2,
+// with bf16 9e-2, so 2.0e-3, of which 1.66e-3 is the result's own rounding to bf16.)
+//
+// A and A A are symmetric: their tiles at and below the diagonal are computed, and each is stored on both sides of it.  All
+// extents are padded to whole tiles of 128 with zeros, which the steps keep.
+#include "../../include/aggemm.h"
+#include "ag_internal.hpp"
+#include "lm_tile.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace ag {
+namespace lm {
+
+struct OrthoArgs : TileArgs {
+    float alpha, beta;       // out = alpha sums + beta addend, of which
+    const float* scale;      // the first step's rest of the norm, a factor for each matrix: squared in A, once in X (null: 1)
+    const _Float16 *add, *add_lo;      // addend and its remainder, or null
+    _Float16 *hi, *lo;       // the result and (unless null) its remainder
+    int64_t ldo, stride;     // of addend and result: rows, matrices
+    // the last step's result, m x n unpadded (null: hi), or its transpose
+    __bf16* last;
+    int64_t m, n;
+    bool turned;
+    int tiles_m;
+};
+
+namespace {
+
+constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;   // stored = true x this
+constexpr int PAD = 128;
+
+// 32 rows x 32 FN columns of 16 bits from memory into a wave's slab, as half_slab_at() has them
+template <int FN>
+__device__ __forceinline__ void half_slab_in(char* slab, const _Float16* p, int64_t ld, int lane)
+{
+    constexpr uint32_t RB = FN * 64, UN = RB / 16;
+    constexpr int RPI = 64 / UN;
+    const uint32_t u = lane % UN, r0 = lane / UN;
+    p += r0 * ld + u * 8;
+    i32x4 x[32 / RPI];
+#pragma unroll
+    for (int it = 0; it < 32 / RPI; ++it)
+        x[it] = *reinterpret_cast<const i32x4*>(p + it * RPI * ld);
+#pragma unroll
+    for (int it = 0; it < 32 / RPI; ++it) {
+        const uint32_t r = it * RPI + r0;
+        const i32x4 y = it * RPI >= 16 ? i32x4{x[it][2], x[it][3], x[it][0], x[it][1]} : x[it];
+        *reinterpret_cast<i32x4*>(slab + r * RB + ((u ^ (r & (UN - 1))) * 16)) = y;
+    }
+}
+
+// The slab's transpose to memory: the transposing LDS reads give a lane eight rows of its column.  p: where the block's first
+// element goes, cols: valid columns of the block (rows there), rows: valid rows.
+template <int FN>
+__device__ __forceinline__ void half_slab_turned(const char* slab, __bf16* p, int64_t ld, int64_t rows, int64_t cols, int lane)
+{
+    constexpr uint32_t RB = FN * 64, UN = RB / 16;
+    const uint32_t g = lane >> 4, i = lane & 15;
+    const int n = (int)min((int64_t)8, rows - (int64_t)g * 8);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
+    __builtin_amdgcn_wave_barrier();
+    auto four = [&](uint32_t r, uint32_t cb) {
+        const uint32_t piece = cb * 4 + (i & 3);
+        const char* at = slab + r * RB + (((piece & 1) ^ (r >> 4)) * 8) + (((piece >> 1) ^ (r & (UN - 1))) * 16);
+        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)const_cast<char*>(at)));
+    };
+#pragma unroll
+    for (int cb = 0; cb < FN * 2; ++cb) {
+        const bf16x4 lo = four(g * 8 + (i >> 2), cb), hi = four(g * 8 + 4 + (i >> 2), cb);
+        const bf16x8 y = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        const int64_t row = cb * 16 + i;
+        __bf16* const out = p + row * ld + g * 8;
+        if (row < cols) {
+            if (n >= 8)
+                *reinterpret_cast<bf16x8_any*>(out) = y;
+            else
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (e < n)
+                        out[e] = y[e];
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // reads done before the slab is rewritten
+    __builtin_amdgcn_wave_barrier();
+}
+
+}  // namespace
+
+// What follows the sums of a wave's FM blocks of 32 rows, WM * 32 rows apart from row0 on, and 32 FN columns from col0 on.
+template <int EPI, int FM, int FN, int WM, typename Acc>
+__device__ __forceinline__ void after_sums(const OrthoArgs& a, const Where& w, Acc acc, char* slab, int64_t row0, int64_t col0,
+                                           int lane)
+{
+    constexpr int SLAB = 32 * FN * 64;                 // bytes of a slab of 16 bits
+    const uint32_t fr = lane & 31, fh = lane >> 5;
+    const float r = a.scale ? a.scale[w.g] : 1.0f;
+    const float alpha = a.alpha * (EPI == kEpiGram ? r * r : EPI == kEpiUpdate ? r : 1.0f);
+    const float beta = a.beta * (EPI == kEpiUpdate ? r : 1.0f);
+    const bool keep = EPI == kEpiUpdate && a.lo, two = EPI == kEpiUpdate && a.add_lo;
+    if (col0 >= a.N)
+        return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const f32x16* const x = acc(i);
+        const int64_t row = row0 + i * WM * 32;
+        if (row >= w.M)
+            break;
+        const int64_t at = w.g * a.stride + row * a.ldo + col0;
+        if constexpr (EPI != kEpiGram) {
+            half_slab_in<FN>(slab, a.add + at, a.ldo, lane);
+            if (two)
+                half_slab_in<FN>(slab + SLAB, a.add_lo + at, a.ldo, lane);
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            __builtin_amdgcn_wave_barrier();
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f16x4* const p = reinterpret_cast<f16x4*>(half_slab_at<FN>(slab, j, q, fr, fh));
+                f16x4* const p2 = reinterpret_cast<f16x4*>(half_slab_at<FN>(slab + SLAB, j, q, fr, fh));
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = alpha * x[j][q * 4 + e];
+                if constexpr (EPI != kEpiGram) {
+                    const f16x4 y = *p;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = fmaf(beta, (float)y[e], v[e]);
+                    if (two) {
+                        const f16x4 z = *p2;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = fmaf(beta, (float)z[e], v[e]);
+                    }
+                }
+                if (EPI == kEpiUpdate && a.last) {
+                    *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+                    continue;
+                }
+                const f16x4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+                *p = h;
+                if (keep)
+                    *p2 = f16x4{(_Float16)(v[0] - (float)h[0]), (_Float16)(v[1] - (float)h[1]), (_Float16)(v[2] - (float)h[2]),
+                                (_Float16)(v[3] - (float)h[3])};
+            }
+        if (EPI == kEpiUpdate && a.last) {
+            __bf16* const out = a.last + w.g * a.m * a.n;
+            if (a.turned)
+                half_slab_turned<FN>(slab, out + col0 * a.m + row, a.m, a.m - row, a.n - col0, lane);
+            else
+                half_slab_out<FN, true>(slab, out + row * a.n + col0, a.n, a.m - row, a.n - col0, lane);
+            continue;
+        }
+        half_slab_out<FN, false>(slab, reinterpret_cast<__bf16*>(a.hi + at), a.ldo, 32, FN * 32, lane);
+        if (keep)
+            half_slab_out<FN, false>(slab + SLAB, reinterpret_cast<__bf16*>(a.lo + at), a.ldo, 32, FN * 32, lane);
+        if (EPI != kEpiUpdate && w.m0 > w.n0)  // a tile below the diagonal
+            half_slab_turned<FN>(slab, reinterpret_cast<__bf16*>(a.hi + w.g * a.stride + col0 * a.ldo + row), a.ldo, 32, FN * 32,
+                                 lane);
+    }
+}
+
+namespace {
+
+// Tile t at or below the diagonal of rows x rows tiles: GROUP_M tile rows at a time, column by column, so that the tiles in
+// flight share rows in the caches.
+__device__ __forceinline__ void lower_tile(int t, int rows, int& m, int& n)
+{
+    int first = 0;
+    while (true) {
+        const int h = min(rows - first, GROUP_M), here = h * first + h * (h + 1) / 2;
+        if (t < here) {
+            if (t < h * first) {
+                n = t / h;
+                m = first + t - n * h;
+            } else {
+                t -= h * first;
+                int r = 0;
+                while (t > r)
+                    t -= ++r;
+                m = first + r;
+                n = first + t;
+            }
+            return;
+        }
+        t -= here;
+        first += h;
+    }
+}
+
+template <int BM, int S, bool TB, int EPI>
+__device__ __forceinline__ void ortho_body(const OrthoArgs& a)
+{
+    constexpr int BYTES = BM * BK * 2, SLAB = 32 * (BM / 2) * 4;
+    __shared__ __attribute__((aligned(1024))) char sA0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char sB0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char sA1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char sB1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sA3[S > 2 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sB3[S > 2 ? BYTES : 16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Stages<S> l;
+    l.a[0] = {sA0, sA0 + BYTES / 2};
+    l.b[0] = {sB0, sB0 + BYTES / 2};
+    l.a[1] = {sA1, sA1 + BYTES / 2};
+    l.b[1] = {sB1, sB1 + BYTES / 2};
+    if constexpr (S == 4) {
+        l.a[2] = {sA2, sA2 + BYTES / 2};
+        l.b[2] = {sB2, sB2 + BYTES / 2};
+        l.a[3] = {sA3, sA3 + BYTES / 2};
+        l.b[3] = {sB3, sB3 + BYTES / 2};
+    }
+    static_assert(2 * SLAB <= BYTES, "two slabs in a stage of one operand");
+    l.slab = (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
+    const int G = gridDim.x, rows = a.tiles_m, cols = (int)a.tiles_n;
+    // workgroups are dispatched round-robin over the 8 XCDs: each XCD takes a contiguous run of tiles
+    const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+    const int per = EPI == kEpiUpdate ? rows * cols : rows * (rows + 1) / 2, all = per * a.E;
+    for (int t = vid; t < all; t += G) {
+        const int e = t / per;
+        int tm, tn;
+        if (EPI == kEpiUpdate)
+            tile_of(t - e * per, rows, cols, tm, tn);
+        else
+            lower_tile(t - e * per, rows, tm, tn);
+        const Where w = {(int64_t)tm * BM, (int64_t)tn * BM, a.M, a.K, 0, e * a.M, tn, e, 0, false};
+        product_tile<BM, BM, 2, 2, S, false, TB, EPI>(a, l, w);
+    }
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 1) void ortho256_kernel(OrthoArgs a)
+{
+    ortho_body<256, 2, EPI == kEpiUpdate, EPI>(a);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 1) void ortho128_kernel(OrthoArgs a)
+{
+    ortho_body<128, 4, EPI == kEpiUpdate, EPI>(a);
+}
+
+// ------------------------------------------------------------------------------------------- what comes first
+// Sums of squares in fp64: squares of any fp32 neither overflow nor vanish there.
+template <typename T>
+__global__ __launch_bounds__(256) void ortho_norm_kernel(const T* G, int64_t elements, double* part)
+{
+    __shared__ double s_sum[4];
+    const T* p = G + blockIdx.y * elements;
+    double sum = 0.0;
+    typedef T vec __attribute__((ext_vector_type(8)));
+    typedef vec vec_any __attribute__((aligned(sizeof(T))));
+    for (int64_t i = (blockIdx.x * 256 + threadIdx.x) * (int64_t)8; i < elements; i += gridDim.x * (int64_t)2048) {
+        if (i + 8 <= elements) {
+            const vec v = *reinterpret_cast<const vec_any*>(p + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum = fma((double)(float)v[e], (double)(float)v[e], sum);
+        } else {
+            for (int e = 0; e < 8; ++e)
+                if (i + e < elements)
+                    sum = fma((double)(float)p[i + e], (double)(float)p[i + e], sum);
+        }
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1)
+        sum += __shfl_xor(sum, s);
+    if ((threadIdx.x & 63) == 0)
+        s_sum[threadIdx.x >> 6] = sum;
+    barrier_after_lds_write();
+    if (threadIdx.x == 0)
+        part[blockIdx.y * (int64_t)gridDim.x + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+}
+
+struct StartArgs {
+    int64_t R, C;            // extents of G
+    int64_t mp, np;          // padded extents of X
+    int parts;               // sums of squares for each matrix
+    float eps;
+    const double* part;
+    float* scale;
+    _Float16 *hi, *lo;       // lo may be null
+};
+
+// X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G.  `scale` gets the
+// rest of the norm.
+template <typename T, bool TURN>
+__global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs a)
+{
+    __shared__ double s_sum[4];
+    __shared__ float s_tile[TURN ? 64 : 1][65];
+    const int64_t e = blockIdx.y;
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.parts; i += 256)
+        sum += a.part[e * a.parts + i];
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1)
+        sum += __shfl_xor(sum, s);
+    if ((threadIdx.x & 63) == 0)
+        s_sum[threadIdx.x >> 6] = sum;
+    barrier_after_lds_write();
+    const double norm = sqrt((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3])) + (double)a.eps;
+    const bool fine = norm > 0.0 && norm < (double)INFINITY;
+    int k = 0;
+    const double part = fine ? frexp(norm, &k) : (double)NAN;           // norm = part 2^k, part in [1/2, 1)
+    const int tiles = (int)(a.np / 64);
+    const int64_t i0 = blockIdx.x / tiles * 64, j0 = (int64_t)(blockIdx.x % tiles) * 64;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        a.scale[e] = (float)(1.0 / part);
+    const int64_t g0 = TURN ? j0 : i0, h0 = TURN ? i0 : j0;             // the tile's first row and column in G
+    const T* p = G + e * a.R * a.C;
+    const int rl = threadIdx.x >> 2, cl = (threadIdx.x & 3) * 16;
+    float x[16];
+    {
+        const int64_t row = g0 + rl;
+        const int n = row < a.R && fine ? (int)max((int64_t)0, min((int64_t)16, a.C - h0 - cl)) : 0;
+        typedef T vec __attribute__((ext_vector_type(8)));
+        typedef vec vec_any __attribute__((aligned(sizeof(T))));
+        const T* q = p + row * a.C + h0 + cl;
+#pragma unroll
+        for (int c = 0; c < 16; c += 8) {
+            if (c + 8 <= n) {
+                const vec v = *reinterpret_cast<const vec_any*>(q + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[c + i] = ldexpf((float)v[i], 12 - k);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[c + i] = c + i < n ? ldexpf((float)q[c + i], 12 - k) : 0.0f;
+            }
+        }
+    }
+    if constexpr (TURN) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            s_tile[rl][cl + i] = x[i];
+        barrier_after_lds_write();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = s_tile[cl + i][rl];
+    }
+    const int64_t at = (e * a.mp + i0 + rl) * a.np + j0 + cl;
+#pragma unroll
+    for (int c = 0; c < 16; c += 8) {
+        f16x8 h, r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[i] = (_Float16)x[c + i];
+            r[i] = (_Float16)(x[c + i] - (float)h[i]);
+        }
+        *reinterpret_cast<f16x8*>(a.hi + at + c) = h;
+        if (a.lo)
+            *reinterpret_cast<f16x8*>(a.lo + at + c) = r;
+    }
+}
+
+// --------------------------------------------------------------------------------------------- host
+int64_t up(int64_t x, int64_t n) { return (x + n - 1) / n * n; }
+
+struct Ortho {
+    int64_t m, n, mp, np;
+    int parts;
+    int64_t part, scale, x0, x1, lo, a, b, bytes;      // offsets in the workspace
+};
+
+Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
+{
+    Ortho o;
+    o.m = std::min(R, C);
+    o.n = std::max(R, C);
+    o.mp = up(o.m, PAD);
+    o.np = up(o.n, PAD);
+    o.parts = (int)std::max<int64_t>(1, std::min<int64_t>(256, R * C / 8192));
+    int64_t at = 0;
+    auto region = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    o.part = region(E * o.parts * 8);
+    o.scale = region(E * 4);
+    o.x0 = region(E * o.mp * o.np * 2);
+    o.x1 = region(E * o.mp * o.np * 2);
+    o.lo = region(E * o.mp * o.np * 2);
+    o.a = region(E * o.mp * o.mp * 2);
+    o.b = region(E * o.mp * o.mp * 2);
+    o.bytes = at;
+    return o;
+}
+
+bool ortho_too_large(int64_t E, int64_t R, int64_t C)
+{
+    const int64_t m = std::min(R, C), n = std::max(R, C);
+    return n > 1 << 20 || E > 65535 || m * n > (int64_t)1 << 36 || E * ((m + 127) / 128) * ((n + 127) / 128) > 1 << 26;
+}
+
+// The largest |s (a + b t + c t^2)| (in: t = s^2 in [0, top^2]) and |b t + c t^2| there, in doubles.
+void bounds(const float* q, double top, double* x, double* b)
+{
+    const double A = q[0], B = q[1], C = q[2], T = top * top;
+    double t[4] = {0.0, T, T, T};
+    int n = 2;
+    const double disc = 9 * B * B - 20 * A * C;                          // a + 3 b t + 5 c t^2 = 0
+    if (C != 0 && disc >= 0) {
+        t[n++] = (-3 * B + std::sqrt(disc)) / (10 * C);
+        t[n++] = (-3 * B - std::sqrt(disc)) / (10 * C);
+    } else if (C == 0 && B != 0) {
+        t[n++] = -A / (3 * B);
+    }
+    *x = 0;
+    for (int i = 0; i < n; ++i)
+        if (t[i] >= 0 && t[i] <= T)
+            *x = std::max(*x, std::fabs(std::sqrt(t[i]) * (A + B * t[i] + C * t[i] * t[i])));
+    *b = std::fabs(B * T + C * T * T);
+    if (C != 0 && -B / (2 * C) > 0 && -B / (2 * C) < T)
+        *b = std::max(*b, B * B / std::fabs(4 * C));
+}
+
+// kGram, kSquare: at and below the diagonal; kUpdate: all tiles.
+template <int EPI>
+hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
+{
+    int cus = 0;
+    hipError_t e = device_cus(&cus);
+    if (e != hipSuccess)
+        return e;
+    const int64_t t256 = EPI == kEpiUpdate ? up(a.M, 256) / 256 * (up(a.N, 256) / 256) : up(a.M, 256) / 256 * (up(a.M, 256) / 256 + 1) / 2;
+    const bool large = t256 * a.E >= cus;
+    const int bm = large ? 256 : 128;
+    a.tiles_m = (int)((a.M + bm - 1) / bm);
+    a.tiles_n = (a.N + bm - 1) / bm;
+    const int64_t tiles = a.E * (EPI == kEpiUpdate ? a.tiles_m * a.tiles_n : (int64_t)a.tiles_m * (a.tiles_m + 1) / 2);
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, cus));
+    if (large)
+        ortho256_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
+    else
+        ortho128_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+void launch_start(const void* G, const Ortho& o, const StartArgs& a, int64_t E, hipStream_t s)
+{
+    const T* g = static_cast<const T*>(G);
+    ortho_norm_kernel<T><<<dim3((unsigned)o.parts, (unsigned)E), dim3(256), 0, s>>>(g, a.R * a.C, const_cast<double*>(a.part));
+    const dim3 grid((unsigned)(o.mp / 64 * (o.np / 64)), (unsigned)E);
+    if (a.R > a.C)
+        ortho_start_kernel<T, true><<<grid, dim3(256), 0, s>>>(g, a);
+    else
+        ortho_start_kernel<T, false><<<grid, dim3(256), 0, s>>>(g, a);
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace ag
+
+using namespace ag;
+using namespace ag::lm;
+
+#define ORTHO_HIP(call, what)           \
+    do {                                \
+        const hipError_t e_ = (call);   \
+        if (e_ != hipSuccess)           \
+            return hip_error(e_, what); \
+    } while (0)
+
+extern "C" int64_t newton_schulz_workspace(int64_t E, int64_t R, int64_t C)
+{
+    if (E <= 0 || R <= 0 || C <= 0 || ortho_too_large(E, R, C))
+        return 0;
+    return plan_ortho(E, R, C).bytes;
+}
+
+extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R, int64_t C, const float* coefficients,
+                             int32_t steps, float eps, void* out, void* work, int64_t work_bytes, void* stream)
+{
+    if (E < 0 || R < 0 || C < 0 || steps < 1 || !coefficients || !(eps >= 0.0f) || std::isinf(eps) ||
+        (g_type != AG_TYPE_BF16 && g_type != AG_TYPE_F32))
+        return AG_EINVAL;
+    for (int64_t i = 0; i < 3 * (int64_t)steps; ++i)
+        if (!std::isfinite(coefficients[i]))
+            return AG_EINVAL;
+    if (E == 0 || R == 0 || C == 0)
+        return AG_OK;
+    const auto bad = [](const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15); };
+    if (bad(G) || bad(out))
+        return AG_EINVAL;
+    if (ortho_too_large(E, R, C))
+        return AG_EUNSUPPORTED;
+    // stored values: X, A and B of every step within fp16
+    double top = 1.0;
+    for (int32_t i = 0; i < steps; ++i) {
+        double x, b;
+        bounds(coefficients + 3 * i, top, &x, &b);
+        if (top > 3.5 || b > 28.0)
+            return AG_EUNSUPPORTED;
+        top = x;
+    }
+    const Ortho o = plan_ortho(E, R, C);
+    if (work_bytes < o.bytes || bad(work))
+        return AG_EINVAL;
+    char* const ws = static_cast<char*>(work);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    auto half = [&](int64_t at) { return reinterpret_cast<_Float16*>(ws + at); };
+    // what the steps after each multiply a rounding of its result by, among small singular directions
+    auto keeps = [&](int32_t step) {
+        double gain = 1.0;
+        for (int32_t i = step + 1; i < steps; ++i)
+            gain *= std::fabs((double)coefficients[3 * i]);
+        return gain > 16.0;
+    };
+    bool kept = g_type == AG_TYPE_F32 && keeps(-1);
+    float* const scale = reinterpret_cast<float*>(ws + o.scale);
+    const StartArgs st = {R, C, o.mp, o.np, o.parts, eps, reinterpret_cast<double*>(ws + o.part), scale, half(o.x0),
+                          kept ? half(o.lo) : nullptr};
+    if (g_type == AG_TYPE_F32)
+        launch_start<float>(G, o, st, E, s);
+    else
+        launch_start<__bf16>(G, o, st, E, s);
+    ORTHO_HIP(hipGetLastError(), "launch newton_schulz start");
+    int64_t cur = o.x0, next = o.x1;
+    const int64_t xs = o.mp * o.np, as = o.mp * o.mp;
+    for (int32_t i = 0; i < steps; ++i) {
+        const float a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
+        const bool keep = i + 1 < steps && keeps(i);
+        auto product = [&](int64_t A, int64_t lda, int64_t B, int64_t ldb, int64_t M, int64_t N, int64_t K, int64_t strideB) {
+            OrthoArgs p = {};
+            p.A = reinterpret_cast<const __bf16*>(ws + A);
+            p.B = reinterpret_cast<const __bf16*>(ws + B);
+            p.lda = lda;
+            p.ldb = ldb;
+            p.M = M;
+            p.N = N;
+            p.K = p.k_valid = K;
+            p.E = (int)E;
+            p.splits = 1;
+            p.strideB = strideB;
+            p.ldo = N;
+            p.stride = M * N;
+            return p;
+        };
+        OrthoArgs p = product(cur, o.np, cur, o.np, o.mp, o.mp, o.np, xs);
+        p.alpha = kScaleA / (kScaleX * kScaleX);
+        p.scale = i == 0 ? scale : nullptr;
+        p.hi = half(o.a);
+        ORTHO_HIP(launch_ortho<kEpiGram>(p, s), "launch newton_schulz X X^T");
+        p = product(o.a, o.mp, o.a, o.mp, o.mp, o.mp, o.mp, as);
+        p.alpha = c * (kScaleB / (kScaleA * kScaleA));
+        p.beta = b * (kScaleB / kScaleA);
+        p.add = half(o.a);
+        p.hi = half(o.b);
+        ORTHO_HIP(launch_ortho<kEpiSquare>(p, s), "launch newton_schulz A A");
+        p = product(o.b, o.mp, cur, o.np, o.mp, o.np, o.mp, xs);
+        p.alpha = 1.0f / kScaleB;
+        p.beta = a;
+        p.scale = i == 0 ? scale : nullptr;
+        p.add = half(cur);
+        p.add_lo = kept ? half(o.lo) : nullptr;
+        p.hi = half(next);
+        p.lo = keep ? half(o.lo) : nullptr;
+        if (i + 1 == steps) {
+            p.alpha /= kScaleX;
+            p.beta /= kScaleX;
+            p.last = static_cast<__bf16*>(out);
+            p.m = o.m;
+            p.n = o.n;
+            p.turned = R > C;
+        }
+        ORTHO_HIP(launch_ortho<kEpiUpdate>(p, s), "launch newton_schulz B X");
+        kept = keep;
+        std::swap(cur, next);
+    }
+    return AG_OK;
+}

@@ -885,11 +885,16 @@ struct Where {
     bool zero;                                         // rows past the last group
 };
 
+struct OrthoArgs;
+template <int EPI, int FM, int FN, int WM, typename Acc>
+__device__ void after_sums(const OrthoArgs& a, const Where& w, Acc acc, char* slab, int64_t row0, int64_t col0, int lane);
+
 // One tile.  EPI: kEpiLinear, kEpiSum (the sums alone: a kernel without the activations' code
 // takes 37 us instead of 41 for 16384 x 4096 x 8), kEpiScaled (the sums times the unit of the d logits), kEpiStat (softmax
-// statistics of a row's columns), kEpiGrad (d logits).
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI>
-__device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>& l, const Where& w)
+// statistics of a row's columns), kEpiGrad (d logits).  From kEpiGram on the factors are fp16 and what follows is
+// after_sums(), which lm_ortho.hip has.
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int EPI, typename Args = TileArgs>
+__device__ __forceinline__ void product_tile(const Args& a, const Stages<S>& l, const Where& w)
 {
     static_assert(WM * WN == 4, "four waves");
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32, NM = FM * FN;
@@ -897,7 +902,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
     typedef Side<BN, TB> SB;
     constexpr int ND = SA::OPS + SB::OPS;
     constexpr int WNC = FN * 32;                       // columns of a wave's block
-    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum || EPI == kEpiScaled;
+    constexpr bool LIN = EPI == kEpiLinear || EPI == kEpiSum || EPI == kEpiScaled, FP16 = EPI >= kEpiGram;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -942,7 +947,7 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
         float row_lse[FM], row_w[FM], sample = 1.0f;
         if constexpr (EPI == kEpiGrad || EPI == kEpiScaled)
             sample = loss_sample(a.dloss, a.dloss_rows);
-        if constexpr (!LIN) {
+        if constexpr (!LIN && !FP16) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int64_t mrow = min(m0 + (i * WM + wm) * 32 + fr, M - 1);
@@ -997,7 +1002,11 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
 #pragma unroll
             for (int gi = 0; gi < NM; ++gi) {
                 const int i = gi / FN, j = gi % FN;
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[set][j], af[set][i], acc[i][j], 0, 0, 0);
+                if constexpr (FP16)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, bf[set][j]),
+                                                                       __builtin_bit_cast(f16x8, af[set][i]), acc[i][j], 0, 0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[set][j], af[set][i], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
                 constexpr int NR = FM + FN;
                 constexpr int RS = NM >= NR ? NR : NM;            // MFMAs that a read follows
@@ -1122,7 +1131,13 @@ __device__ __forceinline__ void product_tile(const TileArgs& a, const Stages<S>&
         asm volatile("" : "+v"(el), "+s"(ldc), "+s"(ldp));
         const int64_t wcol = n0 + wn * WNC;                            // the wave's first column
         const int wcols = (int)max((int64_t)0, min((int64_t)WNC, a.N - wcol));
-        if constexpr (LIN) {
+        if constexpr (FP16) {
+            after_sums<EPI, FM, FN, WM>(a, w, [&](int i) {
+                int flag = 0;
+                one_block(acc[i], el, flag);
+                return acc[i];
+            }, slab, m0 + wm * 32, wcol, el);
+        } else if constexpr (LIN) {
             const int64_t mrow0 = m0 + wm * 32;                        // blocks WM x 32 rows apart
             const int64_t at = (grow0 + mrow0) * ldc + wcol;
             __bf16* const C = a.out.C + (a.group == kGroupK ? g * a.M * ldc : 0) + at;

@@ -280,6 +280,49 @@ int gemm_xent_bwd(const float *dloss, const void *A, const void *B, const int64_
                   const float *lse, int64_t T, int64_t V, int64_t K, void *dA, void *dB, void *work,
                   int64_t work_bytes, void *stream);
 
+/*
+ * Layer norm of each row, with the residual stream added in front:
+ *   h = x + residual (rounded to bf16; x itself without a residual),  m = mean(h),
+ *   r = 1 / sqrt(mean((h - m)^2) + eps),  y = (h - m) r weight + bias.
+ *   x, residual, y, h (rows, width); weight, bias (width); mean, rstd (rows) fp32: m and r.
+ * residual, weight (then 1), bias (then 0), h, mean and rstd may be NULL; h needs a residual and may be the same buffer as
+ * x or residual.  eps >= 0.  width > 2^21 or rows > 2^30 return AG_EUNSUPPORTED.  Rows may have any length.
+ */
+int layer_norm(const void *x, const void *residual, const void *weight, const void *bias, int64_t rows, int64_t width,
+               float eps, void *y, void *h, float *mean, float *rstd, void *stream);
+
+/*
+ * Its gradients, with xh = (h - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + dh   (for x and residual alike),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ *   dy, h, dh, dx (rows, width); mean, rstd as layer_norm wrote them; dh: NULL, or the gradient that reaches h on its other
+ *   way; dx may be the same buffer as dh.
+ * Each output may be NULL: it is then not computed.  `work` serves the sums over rows: without dweight and dbias it may
+ * be NULL.
+ */
+int64_t layer_norm_bwd_workspace(int64_t rows, int64_t width);
+int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float *rstd, const void *weight, const void *dh,
+                   int64_t rows, int64_t width, void *dx, void *dweight, void *dbias, void *work, int64_t work_bytes,
+                   void *stream);
+
+/*
+ * Newton-Schulz orthogonalisation of each matrix of a stack, as an optimiser does with a weight's update:
+ *   X = G / (|G| + eps), |G| the Frobenius norm; for each step's (a, b, c):
+ *   X = a X + (b A + c A A) X with A = X X^T  (X^T X from the right, if R > C: the same result).
+ *   G (E, R, C) in g_type; out (E, R, C) bf16, may be G's buffer where that is bf16; coefficients: steps x 3 floats on the
+ *   HOST, read during the call.
+ * Every singular value s of X becomes s (a + b s^2 + c s^4), step by step.  The products take fp16 of X, A and b A + c A A, with
+ * fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.  Coefficients whose X could
+ * have a singular value above 3.5 on the way, or whose |b t + c t^2| could exceed 28 (t: the squares), return
+ * AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, more than 2^36 elements of a matrix or 2^26 tiles of 128 x 128.  A matrix
+ * with an infinity or NaN gives NaN throughout.
+ */
+#define AG_TYPE_BF16  0
+#define AG_TYPE_F32   1
+int64_t newton_schulz_workspace(int64_t E, int64_t R, int64_t C);
+int newton_schulz(const void *G, int32_t g_type, int64_t E, int64_t R, int64_t C, const float *coefficients, int32_t steps,
+                  float eps, void *out, void *work, int64_t work_bytes, void *stream);
+
 /* Waits for `stream`, then reads and clears the current device's status words (the workspace's,
  * then ag_gemm_noalloc's).  Returns AG_OK, or AG_ETIMEOUT with info = {code, chunk, tile, epoch}
  * for the first flag wait that gave up since the last ag_check (epoch: the failing call's flag
