@@ -47,9 +47,13 @@ struct Piece {
     int lo, s;
     __device__ __forceinline__ Piece(int col, int width) : lo(min(col, width - 8)), s(min(col - lo, 8)) {}
     __device__ __forceinline__ int n() const { return 8 - s; }
-    __device__ __forceinline__ bf16x8 take(const __bf16* row) const
+    __device__ __forceinline__ i32x4 load(const __bf16* row) const { return *reinterpret_cast<const i32x4_any*>(row + lo); }
+    __device__ __forceinline__ bf16x8 take(const __bf16* row) const 
     {
-        i32x4 v = *reinterpret_cast<const i32x4_any*>(row + lo);
+        return __builtin_bit_cast(bf16x8, fit(load(row)));
+    }
+    __device__ __forceinline__ i32x4 fit(i32x4 v) const
+    {
         if (s & 8)
             v = i32x4{};
         if (s & 4)
@@ -60,7 +64,7 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 v[i] = (int)((uint32_t)v[i] >> 16 | (i < 3 ? (uint32_t)v[i < 3 ? i + 1 : i] << 16 : 0u));
-        return __builtin_bit_cast(bf16x8, v);
+        return v;
     }
 };
 
@@ -88,10 +92,35 @@ __device__ __forceinline__ void give8(__bf16* p, int n, bf16x8 v)
             p[e] = v[e];
 }
 
+// Value e of eight.  (As vectors of bf16 what is kept between its uses takes twice the registers.)
+__device__ __forceinline__ float value(const i32x4& v, int e)
+{
+    return __builtin_bit_cast(float, e & 1 ? (uint32_t)v[e >> 1] & 0xFFFF0000u : (uint32_t)v[e >> 1] << 16);
+}
+
 __device__ __forceinline__ bf16x8 ones()
 {
     const __bf16 x = (__bf16)1.0f;
     return bf16x8{x, x, x, x, x, x, x, x};
+}
+
+// x summed over N = 16, 32 or 64 neighbouring lanes: within 16 by the arithmetic's own lane exchange (the neighbour, the other
+// pair, the other four and the other eight mirrored), which needs no LDS.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float x)
+{
+    auto with = [&](auto ctrl) {
+        x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    with(std::integral_constant<int, 0xB1>());       // quad_perm [1, 0, 3, 2]
+    with(std::integral_constant<int, 0x4E>());       // quad_perm [2, 3, 0, 1]
+    with(std::integral_constant<int, 0x141>());      // row_half_mirror
+    with(std::integral_constant<int, 0x140>());      // row_mirror
+    if (N > 16)
+        x += __shfl_xor(x, 16);
+    if (N > 32)
+        x += __shfl_xor(x, 32);
+    return x;
 }
 
 // (a, b) summed over the TPR threads of a row; every one of them gets the sums.  `turn` counts the sums taken: two
@@ -99,11 +128,8 @@ __device__ __forceinline__ bf16x8 ones()
 template <int TPR>
 __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*s_sum)[16], int& turn)
 {
-#pragma unroll
-    for (int s = 1; s < (TPR < 64 ? TPR : 64); s <<= 1) {
-        a += __shfl_xor(a, s);
-        b += __shfl_xor(b, s);
-    }
+    a = lanes_sum<TPR < 64 ? TPR : 64>(a);
+    b = lanes_sum<TPR < 64 ? TPR : 64>(b);
     if constexpr (TPR > 64) {
         float2* const buf = s_sum[turn++ & 1];
         if ((threadIdx.x & 63) == 0)
@@ -129,7 +155,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a)
     constexpr int RPW = kThreads<TPR> / TPR;            // rows of a workgroup at a time
     __shared__ float2 s_sum[2][16];
     int turn = 0;
-    const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
+    const int t = RPW == 1 ? threadIdx.x : threadIdx.x % TPR, rl = RPW == 1 ? 0 : threadIdx.x / TPR;
     bf16x8 w[C], b[C];
     auto piece = [&](int c) { return Piece((c * TPR + t) * 8, a.width); };
 #pragma unroll
@@ -264,64 +290,112 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a)
 
 // ----------------------------------------------------------------------------------------- gradients
 // A workgroup's rows, and its share of the column sums in registers; `part` gets one row of them for each workgroup.
-template <int TPR, int C>
+template <int TPR, int C, bool DH>
 __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
 {
     constexpr int NTH = kThreads<TPR>, RPW = NTH / TPR;
     __shared__ float2 s_sum[2][16];
     int turn = 0;
-    const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
-    bf16x8 w[C];
+    const int t = RPW == 1 ? threadIdx.x : threadIdx.x % TPR, rl = RPW == 1 ? 0 : threadIdx.x / TPR;
+    i32x4 w[C];
     float dw[C][8], db[C][8];
     auto piece = [&](int c) { return Piece((c * TPR + t) * 8, a.width); };
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        w[c] = a.w ? piece(c).take(a.w) : ones();
+        w[c] = a.w ? piece(c).fit(piece(c).load(a.w)) : __builtin_bit_cast(i32x4, ones());
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             dw[c][e] = db[c][e] = 0.0f;
     }
-    const float count = (float)a.width;
-    for (int64_t row = blockIdx.x * (int64_t)RPW + rl; row < a.rows; row += gridDim.x * (int64_t)RPW) {
+    const float inv = 1.0f / (float)a.width;
+    // A row's loads go out while the one before it is computed (dh's with the row's own computation: its use comes last).
+    // Two rows in turn, and loads without a condition (past the last row that one again): a copy of a row, or a branch
+    // around its loads, would wait for them.
+    struct Row {
+        i32x4 dy[C], h[C];
+        float mean, rstd;
+    };
+    auto fetch = [&](Row& r, int64_t row) {
+        row = min(row, a.rows - 1);
         const int64_t at = row * a.width;
-        bf16x8 dy[C], h[C], dh[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            dy[c] = piece(c).take(a.dy + at);
+            r.dy[c] = piece(c).load(a.dy + at);
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            h[c] = piece(c).take(a.h + at);
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        if (a.dx && a.dh) {
+            r.h[c] = piece(c).load(a.h + at);
+        r.mean = a.mean[row];
+        r.rstd = a.rstd[row];
+    };
+    const int64_t step = gridDim.x * (int64_t)RPW;
+    constexpr bool AHEAD = TPR < 1024;                 // those have no registers for a second row
+    auto compute = [&](Row& r, Row& next, int64_t row) {
+        if constexpr (!AHEAD)
+            fetch(r, row);
+        i32x4 more[DH ? C : 1];
+        auto fetch_more = [&] {
+            if constexpr (DH) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                dh[c] = piece(c).take(a.dh + at);
-        }
+                for (int c = 0; c < C; ++c)
+                    more[c] = piece(c).load(a.dh + row * a.width);
+            }
+        };
+        if constexpr (AHEAD)
+            fetch_more();
+        if constexpr (AHEAD)
+            fetch(next, row + step);
+        __builtin_amdgcn_sched_barrier(0);
+        i32x4 dy[C], h[C];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            asm volatile("" : "+v"(w[c]));            // not eight floats from one row to the next
+            dy[c] = piece(c).fit(r.dy[c]);
+            h[c] = piece(c).fit(r.h[c]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = ((float)h[c][e] - mean) * rstd, d = (float)dy[c][e];
-                const float g = d * (float)w[c][e];
+                const float xh = (value(h[c], e) - r.mean) * r.rstd, d = value(dy[c], e);
+                const float g = d * value(w[c], e);
                 s1 += g;
                 s2 = fmaf(g, xh, s2);
                 dw[c][e] = fmaf(d, xh, dw[c][e]);
                 db[c][e] += d;
+                asm volatile("" : "+v"(dw[c][e]), "+v"(db[c][e]));       // added now, not behind the sums over the row
             }
-        if (!a.dx)
-            continue;
+            __builtin_amdgcn_sched_barrier(0);         // one piece's temporaries at a time
+        }
+        if constexpr (!AHEAD)
+            fetch_more();
         const float2 s = row_sum<TPR>(s1, s2, s_sum, turn);
-        const float m1 = s.x / count, m2 = s.y / count;
+        const float m1 = s.x * inv, m2 = s.y * inv;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+            // g and xh again from what is packed: kept, they are sixteen registers for each piece
+            asm volatile("" : "+v"(dy[c]), "+v"(h[c]), "+v"(w[c]));
+            const i32x4 d = DH ? piece(c).fit(more[DH ? c : 0]) : i32x4{};
             bf16x8 o;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = ((float)h[c][e] - mean) * rstd, g = (float)dy[c][e] * (float)w[c][e];
-                o[e] = (__bf16)fmaf(rstd, g - m1 - xh * m2, a.dh ? (float)dh[c][e] : 0.0f);
+                const float xh = (value(h[c], e) - r.mean) * r.rstd, g = value(dy[c], e) * value(w[c], e);
+                o[e] = (__bf16)fmaf(r.rstd, g - m1 - xh * m2, value(d, e));
             }
-            give8(a.dx + at + (c * TPR + t) * 8, piece(c).n(), o);
+            if (a.dx)
+                give8(a.dx + row * a.width + (c * TPR + t) * 8, piece(c).n(), o);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int64_t row = blockIdx.x * (int64_t)RPW + rl;
+    Row r0, r1;
+    if constexpr (AHEAD)
+        fetch(r0, row);
+    while (row < a.rows) {
+        compute(r0, r1, row);
+        row += step;
+        if constexpr (AHEAD) {
+            if (row >= a.rows)
+                break;
+            compute(r1, r0, row);
+            row += step;
         }
     }
     if (!a.part)
@@ -511,8 +585,8 @@ auto by_width(int64_t width, F f)
     if (width <= 4096)
         AG_NORM(256, 2);
     if (width <= 8192)
-        AG_NORM(256, 4);
-    AG_NORM(512, 4);
+        AG_NORM(512, 2);
+    AG_NORM(1024, 2);
 #undef AG_NORM
 }
 
@@ -615,7 +689,11 @@ extern "C" int layer_norm_bwd(const void* dy, const void* h, const float* mean, 
     } else if (rows > 0) {
         by_width(width, [&](auto tpr, auto c) {
             constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
-            norm_bwd_kernel<T, C><<<dim3((unsigned)parts), dim3(kThreads<T>), 0, s>>>(a);
+            const dim3 grid((unsigned)parts), block(kThreads<T>);
+            if (dx && dh)
+                norm_bwd_kernel<T, C, true><<<grid, block, 0, s>>>(a);
+            else
+                norm_bwd_kernel<T, C, false><<<grid, block, 0, s>>>(a);
         });
     }
     NORM_HIP("launch layer_norm_bwd");

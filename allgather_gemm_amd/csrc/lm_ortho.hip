@@ -1,15 +1,15 @@
 // lm_ortho.hip -- Newton-Schulz orthogonalisation of a matrix or a stack of them: kernels and entry points.
 //
-//   X = G / (|G| + eps), turned so that it is m x n with m <= n; for each (a, b, c):  A = X X^T,  B = b A + c A A,
-//   X = a X + B X.
+//   X = G / (|G| + eps), turned so that it is m x n with m <= n; for each (a, b, c):  A = X X^T,  B = a I + b A + c A A,
+//   X = B X.
 //
 // Products by fp16 matrix instructions with fp32 sums: the iterates' singular values stay below a bound that the
 // coefficients give (checked by the entry point), so fp16 with a fixed scale holds them, with three bits more than bf16.
 // What a rounding of X does is not the same everywhere: an error e among X's small left and right singular directions comes
-// out multiplied by the remaining steps' a's (3.4445^4 after the first of five), any other by about one.  Through the products
-// a rounding reaches those directions only as B e or (e X^T) X, both small there; directly it does as a X.  So the
-// iterates are kept as two fp16, value and remainder, as long as the remaining gain is large, the addend a X takes both and the
-// products the value alone.  (Error of 1024 x 1024 with singular values i^-1.5, of the result's norm: with one fp16 1.2e-2,
+// out multiplied by the remaining steps' a's (3.4445^4 after the first of five), any other by about one.  Through A, and
+// through B's own rounding, what is off reaches those directions only times X, which is small there; a rounding of X is in
+// them as it is.  So the iterates are kept as two fp16, value and remainder, as long as the remaining gain is large: the
+// products take the value alone, and a times the remainder is added to B X (B times it, but for what does not grow).  (Error of 1024 x 1024 with singular values i^-1.5, of the result's norm: with one fp16 1.2e-2,
 // with bf16 9e-2, so 2.0e-3, of which 1.66e-3 is the result's own rounding to bf16.)
 //
 // A and A A are symmetric: their tiles at and below the diagonal are computed, and each is stored on both sides of it.  All
@@ -25,9 +25,10 @@ namespace ag {
 namespace lm {
 
 struct OrthoArgs : TileArgs {
-    float alpha, beta;       // out = alpha sums + beta addend, of which
+    float alpha, beta;       // out = alpha sums + beta addend, plus `unit` on the diagonal (kEpiSquare)
+    float unit;
     const float* scale;      // the first step's rest of the norm, a factor for each matrix: squared in A, once in X (null: 1)
-    const _Float16 *add, *add_lo;      // addend and its remainder, or null
+    const _Float16* add;     // addend: A (kEpiSquare); X's remainder, or null (kEpiUpdate)
     _Float16 *hi, *lo;       // the result and (unless null) its remainder
     int64_t ldo, stride;     // of addend and result: rows, matrices
     // the last step's result, m x n unpadded (null: hi), or its transpose
@@ -35,6 +36,7 @@ struct OrthoArgs : TileArgs {
     int64_t m, n;
     bool turned;
     int tiles_m;
+    int cut;                 // of the tiles, those that go in quarters
 };
 
 namespace {
@@ -42,32 +44,74 @@ namespace {
 constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;   // stored = true x this
 constexpr int PAD = 128;
 
-// 32 rows x 32 FN columns of 16 bits from memory into a wave's slab, as half_slab_at() has them
+// A wave's block of 32 rows and FN * 32 columns of 16 bits in its LDS slab, laid out as half_slab_at() has it; three blocks
+// side by side take rows of four, of which `units` 16-byte units are there.
 template <int FN>
-__device__ __forceinline__ void half_slab_in(char* slab, const _Float16* p, int64_t ld, int lane)
-{
-    constexpr uint32_t RB = FN * 64, UN = RB / 16;
-    constexpr int RPI = 64 / UN;
-    const uint32_t u = lane % UN, r0 = lane / UN;
-    p += r0 * ld + u * 8;
-    i32x4 x[32 / RPI];
-#pragma unroll
-    for (int it = 0; it < 32 / RPI; ++it)
-        x[it] = *reinterpret_cast<const i32x4*>(p + it * RPI * ld);
-#pragma unroll
-    for (int it = 0; it < 32 / RPI; ++it) {
+struct Slab {
+    static constexpr int L = FN == 3 ? 4 : FN;
+    static constexpr uint32_t RB = L * 64, UN = RB / 16;           // bytes and 16-byte units of a row
+    static constexpr int RPI = 64 / UN, ITS = 32 / RPI;            // rows at a time, times
+    static constexpr int BYTES = 32 * RB;
+
+    // 16-byte unit u of row it * RPI + r0, the halves of the lower rows' units the other way round
+    static __device__ __forceinline__ i32x4* unit(char* slab, int it, uint32_t r0, uint32_t u)
+    {
         const uint32_t r = it * RPI + r0;
-        const i32x4 y = it * RPI >= 16 ? i32x4{x[it][2], x[it][3], x[it][0], x[it][1]} : x[it];
-        *reinterpret_cast<i32x4*>(slab + r * RB + ((u ^ (r & (UN - 1))) * 16)) = y;
+        return reinterpret_cast<i32x4*>(slab + r * RB + ((u ^ (r & (UN - 1))) * 16));
     }
-}
+    static __device__ __forceinline__ i32x4 halves(int it, i32x4 x)
+    {
+        return it * RPI >= 16 ? i32x4{x[2], x[3], x[0], x[1]} : x;
+    }
+
+    // a block on its way from memory
+    struct Ahead {
+        i32x4 x[ITS];
+    };
+    static __device__ __forceinline__ void fetch(Ahead& p, const _Float16* from, int64_t ld, uint32_t units, int lane)
+    {
+        const uint32_t u = lane % UN, r0 = lane / UN;
+        if (FN != 3 || u < units) {
+            from += r0 * ld + u * 8;
+#pragma unroll
+            for (int it = 0; it < ITS; ++it)
+                p.x[it] = *reinterpret_cast<const i32x4*>(from + it * RPI * ld);
+        }
+    }
+    static __device__ __forceinline__ void put(char* slab, const Ahead& p, int lane)
+    {
+        const uint32_t u = lane % UN, r0 = lane / UN;
+#pragma unroll
+        for (int it = 0; it < ITS; ++it)
+            *unit(slab, it, r0, u) = halves(it, p.x[it]);
+    }
+    static __device__ __forceinline__ void out(char* slab, _Float16* to, int64_t ld, uint32_t units, int lane)
+    {
+        const uint32_t u = lane % UN, r0 = lane / UN;
+        settle();
+        to += r0 * ld + u * 8;
+#pragma unroll
+        for (int it = 0; it < ITS; ++it) {
+            const i32x4 y = halves(it, *unit(slab, it, r0, u));
+            if (FN != 3 || u < units)
+                *reinterpret_cast<i32x4*>(to + it * RPI * ld) = y;
+        }
+        settle();
+    }
+    // this wave's LDS reads and writes are done
+    static __device__ __forceinline__ void settle()
+    {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_wave_barrier();
+    }
+};
 
 // The slab's transpose to memory: the transposing LDS reads give a lane eight rows of its column.  p: where the block's first
 // element goes, cols: valid columns of the block (rows there), rows: valid rows.
 template <int FN>
 __device__ __forceinline__ void half_slab_turned(const char* slab, __bf16* p, int64_t ld, int64_t rows, int64_t cols, int lane)
 {
-    constexpr uint32_t RB = FN * 64, UN = RB / 16;
+    constexpr uint32_t RB = Slab<FN>::RB, UN = Slab<FN>::UN;
     const uint32_t g = lane >> 4, i = lane & 15;
     const int n = (int)min((int64_t)8, rows - (int64_t)g * 8);
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slab is written
@@ -104,49 +148,53 @@ template <int EPI, int FM, int FN, int WM, typename Acc>
 __device__ __forceinline__ void after_sums(const OrthoArgs& a, const Where& w, Acc acc, char* slab, int64_t row0, int64_t col0,
                                            int lane)
 {
-    constexpr int SLAB = 32 * FN * 64;                 // bytes of a slab of 16 bits
+    typedef Slab<FN> S;
     const uint32_t fr = lane & 31, fh = lane >> 5;
     const float r = a.scale ? a.scale[w.g] : 1.0f;
     const float alpha = a.alpha * (EPI == kEpiGram ? r * r : EPI == kEpiUpdate ? r : 1.0f);
     const float beta = a.beta * (EPI == kEpiUpdate ? r : 1.0f);
-    const bool keep = EPI == kEpiUpdate && a.lo, two = EPI == kEpiUpdate && a.add_lo;
+    const bool keep = EPI == kEpiUpdate && a.lo, add = EPI == kEpiSquare || (EPI == kEpiUpdate && a.add);
     if (col0 >= a.N)
         return;
+    // extents are multiples of 128, a wave's columns of a 192 x 192 tile are not
+    const uint32_t units = (uint32_t)min((int64_t)FN * 4, (a.N - col0) / 8);
+    const int64_t first = w.g * a.stride + row0 * a.ldo + col0;
+    typename S::Ahead ahead;
+    if (add && row0 < w.M)
+        S::fetch(ahead, a.add + first, a.ldo, units, lane);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const f32x16* const x = acc(i);
         const int64_t row = row0 + i * WM * 32;
         if (row >= w.M)
             break;
-        const int64_t at = w.g * a.stride + row * a.ldo + col0;
-        if constexpr (EPI != kEpiGram) {
-            half_slab_in<FN>(slab, a.add + at, a.ldo, lane);
-            if (two)
-                half_slab_in<FN>(slab + SLAB, a.add_lo + at, a.ldo, lane);
-            __builtin_amdgcn_s_waitcnt(0xC07F);
-            __builtin_amdgcn_wave_barrier();
+        const int64_t at = first + i * WM * 32 * a.ldo;
+        if (add) {
+            S::put(slab, ahead, lane);
+            if (i + 1 < FM && row + WM * 32 < w.M)
+                S::fetch(ahead, a.add + at + WM * 32 * a.ldo, a.ldo, units, lane);
+            S::settle();
         }
+        const int diagonal = (int)(row - col0) + (int)fr - (int)fh * 4;      // the lane's columns count from fh * 4
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                f16x4* const p = reinterpret_cast<f16x4*>(half_slab_at<FN>(slab, j, q, fr, fh));
-                f16x4* const p2 = reinterpret_cast<f16x4*>(half_slab_at<FN>(slab + SLAB, j, q, fr, fh));
+                f16x4* const p = reinterpret_cast<f16x4*>(half_slab_at<S::L>(slab, j, q, fr, fh));
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v[e] = alpha * x[j][q * 4 + e];
-                if constexpr (EPI != kEpiGram) {
+                if (add) {
                     const f16x4 y = *p;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v[e] = fmaf(beta, (float)y[e], v[e]);
-                    if (two) {
-                        const f16x4 z = *p2;
+                }
+                if constexpr (EPI == kEpiSquare) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = fmaf(beta, (float)z[e], v[e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[e] += diagonal == j * 32 + q * 8 + e ? a.unit : 0.0f;
                 }
                 if (EPI == kEpiUpdate && a.last) {
                     *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
@@ -155,22 +203,25 @@ __device__ __forceinline__ void after_sums(const OrthoArgs& a, const Where& w, A
                 const f16x4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
                 *p = h;
                 if (keep)
-                    *p2 = f16x4{(_Float16)(v[0] - (float)h[0]), (_Float16)(v[1] - (float)h[1]), (_Float16)(v[2] - (float)h[2]),
-                                (_Float16)(v[3] - (float)h[3])};
+                    *reinterpret_cast<f16x4*>(half_slab_at<S::L>(slab + S::BYTES, j, q, fr, fh)) =
+                        f16x4{(_Float16)(v[0] - (float)h[0]), (_Float16)(v[1] - (float)h[1]), (_Float16)(v[2] - (float)h[2]),
+                              (_Float16)(v[3] - (float)h[3])};
             }
-        if (EPI == kEpiUpdate && a.last) {
-            __bf16* const out = a.last + w.g * a.m * a.n;
-            if (a.turned)
-                half_slab_turned<FN>(slab, out + col0 * a.m + row, a.m, a.m - row, a.n - col0, lane);
-            else
-                half_slab_out<FN, true>(slab, out + row * a.n + col0, a.n, a.m - row, a.n - col0, lane);
-            continue;
+        if constexpr (EPI == kEpiUpdate) {
+            if (a.last) {
+                __bf16* const out = a.last + w.g * a.m * a.n;
+                if (a.turned)
+                    half_slab_turned<FN>(slab, out + col0 * a.m + row, a.m, a.m - row, a.n - col0, lane);
+                else
+                    half_slab_out<FN, true>(slab, out + row * a.n + col0, a.n, a.m - row, a.n - col0, lane);
+                continue;
+            }
         }
-        half_slab_out<FN, false>(slab, reinterpret_cast<__bf16*>(a.hi + at), a.ldo, 32, FN * 32, lane);
+        S::out(slab, a.hi + at, a.ldo, units, lane);
         if (keep)
-            half_slab_out<FN, false>(slab + SLAB, reinterpret_cast<__bf16*>(a.lo + at), a.ldo, 32, FN * 32, lane);
+            S::out(slab + S::BYTES, a.lo + at, a.ldo, units, lane);
         if (EPI != kEpiUpdate && w.m0 > w.n0)  // a tile below the diagonal
-            half_slab_turned<FN>(slab, reinterpret_cast<__bf16*>(a.hi + w.g * a.stride + col0 * a.ldo + row), a.ldo, 32, FN * 32,
+            half_slab_turned<FN>(slab, reinterpret_cast<__bf16*>(a.hi + w.g * a.stride + col0 * a.ldo + row), a.ldo, 32, units * 8,
                                  lane);
     }
 }
@@ -203,58 +254,108 @@ __device__ __forceinline__ void lower_tile(int t, int rows, int& m, int& n)
     }
 }
 
-template <int BM, int S, bool TB, int EPI>
+// A launch's tiles: BM x BM ones, then (256 and 128) the last `cut` of them in quarters.
+template <int BM, int S, int EPI>
 __device__ __forceinline__ void ortho_body(const OrthoArgs& a)
 {
-    constexpr int BYTES = BM * BK * 2, SLAB = 32 * (BM / 2) * 4;
-    __shared__ __attribute__((aligned(1024))) char sA0[BYTES];
+    constexpr bool TB = EPI == kEpiUpdate, LARGE = BM == 256, QUARTERS = LARGE || BM == 128;
+    constexpr int BYTES = BM * BK * 2;
+    static_assert(S == 2 ? LARGE : S == 3 || S == 4, "stages");
+    __shared__ __attribute__((aligned(1024))) char sA0[LARGE ? BYTES / 2 : BYTES], sU0[LARGE ? BYTES / 2 : 16];
     __shared__ __attribute__((aligned(1024))) char sB0[BYTES];
     __shared__ __attribute__((aligned(1024))) char sA1[BYTES];
     __shared__ __attribute__((aligned(1024))) char sB1[BYTES];
     __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? BYTES : 16];
     __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sA3[S > 2 ? BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sB3[S > 2 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sA3[S > 3 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sB3[S > 3 ? BYTES : 16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Stages<S> l;
-    l.a[0] = {sA0, sA0 + BYTES / 2};
+    l.a[0] = {sA0, LARGE ? sU0 : sA0};
     l.b[0] = {sB0, sB0 + BYTES / 2};
     l.a[1] = {sA1, sA1 + BYTES / 2};
     l.b[1] = {sB1, sB1 + BYTES / 2};
-    if constexpr (S == 4) {
-        l.a[2] = {sA2, sA2 + BYTES / 2};
-        l.b[2] = {sB2, sB2 + BYTES / 2};
-        l.a[3] = {sA3, sA3 + BYTES / 2};
-        l.b[3] = {sB3, sB3 + BYTES / 2};
+    if constexpr (S > 2) {
+        l.a[2].lo = sA2;
+        l.b[2].lo = sB2;
     }
-    static_assert(2 * SLAB <= BYTES, "two slabs in a stage of one operand");
-    l.slab = (wave < 2 ? sA0 : sB0) + (wave & 1) * SLAB;
+    if constexpr (S > 3) {
+        l.a[3].lo = sA3;
+        l.b[3].lo = sB3;
+    }
+    // two slabs a wave where a remainder is kept beside the result
+    constexpr int SLABS = (EPI == kEpiUpdate ? 2 : 1) * Slab<BM / 64>::BYTES;
+    if constexpr (LARGE)
+        l.slab = (wave == 0 ? sA0 : wave == 1 ? sU0 : sB0 + (wave - 2) * SLABS);
+    else
+        l.slab = (wave < 2 ? sA0 : sB0) + (wave & 1) * SLABS;
+    static_assert((LARGE ? 1 : 2) * SLABS <= (int)sizeof(sA0) && 2 * SLABS <= BYTES, "slabs in the first stage");
+    Stages<4> lq;
+    if constexpr (BM == 128) {
+        lq = l;
+    } else if constexpr (LARGE) {
+        lq.a[0].lo = sA0;
+        lq.b[0].lo = sU0;
+        lq.a[1].lo = sB0;
+        lq.b[1].lo = sB0 + 16384;
+        lq.a[2].lo = sA1;
+        lq.b[2].lo = sA1 + 16384;
+        lq.a[3].lo = sB1;
+        lq.b[3].lo = sB1 + 16384;
+        lq.slab = l.slab;
+    }
     const int G = gridDim.x, rows = a.tiles_m, cols = (int)a.tiles_n;
     // workgroups are dispatched round-robin over the 8 XCDs: each XCD takes a contiguous run of tiles
     const int vid = (G % 8 == 0) ? (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
-    const int per = EPI == kEpiUpdate ? rows * cols : rows * (rows + 1) / 2, all = per * a.E;
-    for (int t = vid; t < all; t += G) {
-        const int e = t / per;
-        int tm, tn;
+    const int per = EPI == kEpiUpdate ? rows * cols : rows * (rows + 1) / 2, all = per * a.E, whole = all - a.cut;
+    auto tile = [&](int t, int& e, int& tm, int& tn) {
+        e = t / per;
         if (EPI == kEpiUpdate)
             tile_of(t - e * per, rows, cols, tm, tn);
         else
             lower_tile(t - e * per, rows, tm, tn);
+    };
+    for (int t = vid; t < whole; t += G) {
+        int e, tm, tn;
+        tile(t, e, tm, tn);
         const Where w = {(int64_t)tm * BM, (int64_t)tn * BM, a.M, a.K, 0, e * a.M, tn, e, 0, false};
         product_tile<BM, BM, 2, 2, S, false, TB, EPI>(a, l, w);
+    }
+    if constexpr (QUARTERS) {
+        for (int t = vid; t < 4 * a.cut; t += G) {
+            int e, tm, tn;
+            tile(whole + t / 4, e, tm, tn);
+            const int64_t m0 = (int64_t)tm * BM + (t >> 1 & 1) * (BM / 2), n0 = (int64_t)tn * BM + (t & 1) * (BM / 2);
+            if (m0 >= a.M || n0 >= a.N || (EPI != kEpiUpdate && n0 > m0))
+                continue;
+            const Where w = {m0, n0, a.M, a.K, 0, e * a.M, tn, e, 0, false};
+            product_tile<BM / 2, BM / 2, 2, 2, 4, false, TB, EPI>(a, lq, w);
+        }
     }
 }
 
 template <int EPI>
 __global__ __launch_bounds__(NT, 1) void ortho256_kernel(OrthoArgs a)
 {
-    ortho_body<256, 2, EPI == kEpiUpdate, EPI>(a);
+    ortho_body<256, 2, EPI>(a);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 1) void ortho192_kernel(OrthoArgs a)
+{
+    ortho_body<192, 3, EPI>(a);
 }
 
 template <int EPI>
 __global__ __launch_bounds__(NT, 1) void ortho128_kernel(OrthoArgs a)
 {
-    ortho_body<128, 4, EPI == kEpiUpdate, EPI>(a);
+    ortho_body<128, 4, EPI>(a);
+}
+
+template <int EPI>
+__global__ __launch_bounds__(NT, 2) void ortho64_kernel(OrthoArgs a)
+{
+    ortho_body<64, 4, EPI>(a);
 }
 
 // ------------------------------------------------------------------------------------------- what comes first
@@ -388,7 +489,7 @@ Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
     o.n = std::max(R, C);
     o.mp = up(o.m, PAD);
     o.np = up(o.n, PAD);
-    o.parts = (int)std::max<int64_t>(1, std::min<int64_t>(256, R * C / 8192));
+    o.parts = (int)std::max<int64_t>(1, std::min<int64_t>(1024, R * C / 8192));
     int64_t at = 0;
     auto region = [&](int64_t bytes) {
         const int64_t here = at;
@@ -412,7 +513,7 @@ bool ortho_too_large(int64_t E, int64_t R, int64_t C)
     return n > 1 << 20 || E > 65535 || m * n > (int64_t)1 << 36 || E * ((m + 127) / 128) * ((n + 127) / 128) > 1 << 26;
 }
 
-// The largest |s (a + b t + c t^2)| (in: t = s^2 in [0, top^2]) and |b t + c t^2| there, in doubles.
+// The largest |s (a + b t + c t^2)| and |a + b t + c t^2| for t = s^2, s in [0, top].
 void bounds(const float* q, double top, double* x, double* b)
 {
     const double A = q[0], B = q[1], C = q[2], T = top * top;
@@ -429,30 +530,81 @@ void bounds(const float* q, double top, double* x, double* b)
     for (int i = 0; i < n; ++i)
         if (t[i] >= 0 && t[i] <= T)
             *x = std::max(*x, std::fabs(std::sqrt(t[i]) * (A + B * t[i] + C * t[i] * t[i])));
-    *b = std::fabs(B * T + C * T * T);
+    *b = std::max(std::fabs(A), std::fabs(A + B * T + C * T * T));
     if (C != 0 && -B / (2 * C) > 0 && -B / (2 * C) < T)
-        *b = std::max(*b, B * B / std::fabs(4 * C));
+        *b = std::max(*b, std::fabs(A - B * B / (4 * C)));
 }
 
-// kGram, kSquare: at and below the diagonal; kUpdate: all tiles.
+// A launch: its tiles, and how many of the last ones go in quarters.
+struct OrthoTiles {
+    int size;
+    int64_t rows, cols, all, cut;
+};
+
+OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
+{
+    int cus = 0;
+    if (device_cus(&cus) != hipSuccess || cus <= 0)
+        cus = 256;
+    const double steps = (double)(K / 64);
+    OrthoTiles best = {};
+    double least = 1e30;
+    auto tile_us = [&](int size, double fill) {
+        switch (size) {
+        case 64: return (fill > 1 ? 0.38 : 0.25) * steps + 4;
+        case 128: return 0.44 * steps + 5;
+        case 192: return (0.7 + 0.35 * fill) * steps + 7;
+        default: return (1.0 + 0.7 * fill) * steps + 12;
+        }
+    };
+    auto rounds = [&](int size, int64_t tiles) {
+        const int64_t room = size == 64 ? 2 * cus : cus, full = tiles / room, rest = tiles % room;
+        return full * tile_us(size, size == 64 ? 2 : 1) + (rest ? tile_us(size, full ? 1 : (double)rest / cus) : 0);
+    };
+    for (const int size : {64, 128, 192, 256}) {
+        if (size == 192 && !lower)
+            continue;
+        OrthoTiles t = {size, (M + size - 1) / size, (N + size - 1) / size, 0, 0};
+        t.all = E * (lower ? t.rows * (t.rows + 1) / 2 : t.rows * t.cols);
+        double us = rounds(size, t.all);
+        const int64_t rest = t.all % cus;
+        if ((size == 128 || size == 256) && t.all > cus && rest) {
+            const double cut = rounds(size, t.all - rest) + rounds(size / 2, 4 * rest);
+            if (cut < us) {
+                us = cut;
+                t.cut = rest;
+            }
+        }
+        if (us < least) {
+            least = us;
+            best = t;
+        }
+    }
+    return best;
+}
+
+// kEpiGram, kEpiSquare: tiles at and below the diagonal; kEpiUpdate: all of them.
 template <int EPI>
 hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
 {
     int cus = 0;
-    hipError_t e = device_cus(&cus);
+    const hipError_t e = device_cus(&cus);
     if (e != hipSuccess)
         return e;
-    const int64_t t256 = EPI == kEpiUpdate ? up(a.M, 256) / 256 * (up(a.N, 256) / 256) : up(a.M, 256) / 256 * (up(a.M, 256) / 256 + 1) / 2;
-    const bool large = t256 * a.E >= cus;
-    const int bm = large ? 256 : 128;
-    a.tiles_m = (int)((a.M + bm - 1) / bm);
-    a.tiles_n = (a.N + bm - 1) / bm;
-    const int64_t tiles = a.E * (EPI == kEpiUpdate ? a.tiles_m * a.tiles_n : (int64_t)a.tiles_m * (a.tiles_m + 1) / 2);
-    const dim3 grid((unsigned)std::min<int64_t>(tiles, cus));
-    if (large)
-        ortho256_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
-    else
-        ortho128_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
+    const OrthoTiles t = plan_tiles(EPI != kEpiUpdate, a.E, a.M, a.N, a.K);
+    a.tiles_m = (int)t.rows;
+    a.tiles_n = t.cols;
+    a.cut = (int)t.cut;
+    const dim3 grid((unsigned)std::min(t.all - t.cut + 4 * t.cut, (int64_t)cus * (t.size == 64 ? 2 : 1)));
+    switch (t.size) {
+    case 64: ortho64_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a); break;
+    case 128: ortho128_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a); break;
+    case 192:
+        if constexpr (EPI != kEpiUpdate)
+            ortho192_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
+        break;
+    default: ortho256_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -565,6 +717,7 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p = product(o.a, o.mp, o.a, o.mp, o.mp, o.mp, o.mp, as);
         p.alpha = c * (kScaleB / (kScaleA * kScaleA));
         p.beta = b * (kScaleB / kScaleA);
+        p.unit = a * kScaleB;
         p.add = half(o.a);
         p.hi = half(o.b);
         ORTHO_HIP(launch_ortho<kEpiSquare>(p, s), "launch newton_schulz A A");
@@ -572,8 +725,7 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.alpha = 1.0f / kScaleB;
         p.beta = a;
         p.scale = i == 0 ? scale : nullptr;
-        p.add = half(cur);
-        p.add_lo = kept ? half(o.lo) : nullptr;
+        p.add = kept ? half(o.lo) : nullptr;
         p.hi = half(next);
         p.lo = keep ? half(o.lo) : nullptr;
         if (i + 1 == steps) {
