@@ -533,15 +533,18 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
             return layer_norm(x, weight, bias, eps, residual, y, h, mean, rstd)
     if h is not None and residual is None:
         raise ValueError("h receives x + residual: without a residual there is nothing to keep")
-    xp, rp = _need(x, "x", (rows, width)), _need(residual, "residual", (rows, width), device=dev)
-    wp, bp = _need(weight, "weight", (width,), device=dev), _need(bias, "bias", (width,), device=dev)
-    hp = _need(h, "h", (rows, width), device=dev)
-    mp, sp = _need(mean, "mean", (rows,), torch.float32, dev), _need(rstd, "rstd", (rows,), torch.float32, dev)
-    out = x.new_empty((rows, width)) if y is None else y
-    yp = _need(out, "y", (rows, width), device=dev)
+    shape, col, row = x.shape, (width,), (rows,)
+    xp, rp = _need(x, "x", shape), _need(residual, "residual", shape, device=dev)
+    wp, bp = _need(weight, "weight", col, device=dev), _need(bias, "bias", col, device=dev)
+    hp = None if h is None else _need(h, "h", shape, device=dev)
+    mp = None if mean is None else _need(mean, "mean", row, torch.float32, dev)
+    sp = None if rstd is None else _need(rstd, "rstd", row, torch.float32, dev)
+    out = torch.empty_like(x) if y is None else y
+    yp = out.data_ptr() if y is None else _need(y, "y", shape, device=dev)
     _done(lib().layer_norm(xp, rp, wp, bp, rows, width, eps, yp, hp, mp, sp, _stream_of(dev)), "layer_norm")
     for t in (y, h, mean, rstd):
-        _written(t)
+        if t is not None:
+            _written(t)
     return out
 
 

@@ -289,9 +289,56 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a)
 }
 
 // ----------------------------------------------------------------------------------------- gradients
+// Sums of 256 columns (32 lanes of eight) over rows [r0, r1), a row for each 32 of the N threads at a time, U of them ahead:
+// into row `y` of the partial sums, or, without those, as dw and db.  `load`: eight columns of a row.
+template <int N, int U, typename Load>
+__device__ __forceinline__ void column_sums(const NormBwdArgs& a, int64_t r0, int64_t r1, int x, int y, Load load)
+{
+    constexpr int R = N / 32;
+    __shared__ float s_sum[R][256 + 8];
+    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int col = x * 256 + cl * 8;
+    float dw[8] = {}, db[8] = {};
+    if (col < a.width) {
+#pragma unroll U
+        for (int64_t row = r0 + rl; row < r1; row += R) {
+            float d[8], h[8];
+            load(a.dy + row * a.width, col, d);
+            load(a.h + row * a.width, col, h);
+            const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[e] = fmaf(d[e], (h[e] - mean) * rstd, dw[e]);
+                db[e] += d[e];
+            }
+        }
+    }
+    const int mine = x * 256 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s_sum[rl][cl * 8 + e] = k ? db[e] : dw[e];
+        barrier_after_lds_write();
+        if (threadIdx.x < 256 && mine < a.width) {
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                s += s_sum[r][threadIdx.x];
+            __bf16* const out = k ? a.db : a.dw;
+            if (a.part)
+                a.part[(k * a.parts + y) * a.width + mine] = s;
+            else if (out)
+                out[mine] = (__bf16)s;
+        }
+        barrier_after_lds_write();
+    }
+}
+
 // A workgroup's rows, and its share of the column sums in registers; `part` gets one row of them for each workgroup.
-template <int TPR, int C, bool DH>
-__global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
+// SUMS: false leaves the columns out.
+template <int TPR, int C, bool DH, bool SUMS>
+__device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int64_t first, int64_t workgroups)
 {
     constexpr int NTH = kThreads<TPR>, RPW = NTH / TPR;
     __shared__ float2 s_sum[2][16];
@@ -327,7 +374,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
         r.mean = a.mean[row];
         r.rstd = a.rstd[row];
     };
-    const int64_t step = gridDim.x * (int64_t)RPW;
+    const int64_t step = workgroups * RPW;
     constexpr bool AHEAD = TPR < 1024;                 // those have no registers for a second row
     auto compute = [&](Row& r, Row& next, int64_t row) {
         if constexpr (!AHEAD)
@@ -358,9 +405,11 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
                 const float g = d * value(w[c], e);
                 s1 += g;
                 s2 = fmaf(g, xh, s2);
-                dw[c][e] = fmaf(d, xh, dw[c][e]);
-                db[c][e] += d;
-                asm volatile("" : "+v"(dw[c][e]), "+v"(db[c][e]));       // added now, not behind the sums over the row
+                if constexpr (SUMS) {
+                    dw[c][e] = fmaf(d, xh, dw[c][e]);
+                    db[c][e] += d;
+                    asm volatile("" : "+v"(dw[c][e]), "+v"(db[c][e]));   // added now, not behind the sums over the row
+                }
             }
             __builtin_amdgcn_sched_barrier(0);         // one piece's temporaries at a time
         }
@@ -384,7 +433,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    int64_t row = blockIdx.x * (int64_t)RPW + rl;
+    int64_t row = first * RPW + rl;
     Row r0, r1;
     if constexpr (AHEAD)
         fetch(r0, row);
@@ -398,9 +447,9 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
             row += step;
         }
     }
-    if (!a.part)
+    if (!SUMS || !a.part)
         return;
-    float* const out = a.part + blockIdx.x * (int64_t)a.width;
+    float* const out = a.part + first * a.width;
     const int64_t second = a.parts * a.width;              // from dw's sums to db's
     if constexpr (TPR >= 256) {
 #pragma unroll
@@ -435,6 +484,37 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
             barrier_after_lds_write();
         }
     }
+}
+
+template <int TPR, int C, bool DH>
+__global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_kernel(NormBwdArgs a)
+{
+    norm_bwd_rows<TPR, C, DH, true>(a, blockIdx.x, gridDim.x);
+}
+
+// Few rows: workgroups for the rows and, after them, for the columns, which read the same again and leave no partial sums to
+// be joined by another launch.
+template <int TPR, int C, bool DH>
+__global__ __launch_bounds__(kThreads<TPR>) void norm_bwd_few_kernel(NormBwdArgs a, int row_workgroups)
+{
+    if ((int)blockIdx.x < row_workgroups) {
+        norm_bwd_rows<TPR, C, DH, false>(a, blockIdx.x, row_workgroups);
+    } else {
+        column_sums<kThreads<TPR>, 4>(a, 0, a.rows, blockIdx.x - row_workgroups, 0, [&](const __bf16* row, int col, float* x) {
+            const i32x4 v = Piece(col, a.width).fit(Piece(col, a.width).load(row));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = value(v, e);
+        });
+    }
+}
+
+// Column sums of rows wider than kNormWidest, a chunk of them
+__global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a, int64_t chunk)
+{
+    const int64_t r0 = blockIdx.y * chunk;
+    column_sums<256, 1>(a, r0, min(a.rows, r0 + chunk), blockIdx.x, blockIdx.y,
+                [&](const __bf16* row, int col, float* x) { load8(row + col, min(a.width - col, 8), x); });
 }
 
 // dx of rows wider than kNormWidest
@@ -486,46 +566,6 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdArgs a)
                 o[e] = (__bf16)fmaf(rstd, g[e] - m1 - xh[e] * m2, dh[e]);
             give8(a.dx + at + col, n, o);
         }
-    }
-}
-
-// Column sums of rows wider than kNormWidest: 256 columns a workgroup (32 lanes of eight), eight rows at a time out of a
-// chunk of them.
-__global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a, int64_t chunk)
-{
-    __shared__ float s_sum[8][256 + 8];
-    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int col = blockIdx.x * 256 + cl * 8;
-    const int n = min(max(a.width - col, 0), 8);
-    const int64_t r0 = blockIdx.y * chunk, r1 = min(a.rows, r0 + chunk);
-    float dw[8] = {}, db[8] = {};
-    if (n > 0)
-        for (int64_t row = r0 + rl; row < r1; row += 8) {
-            float d[8], h[8];
-            load8(a.dy + row * a.width + col, n, d);
-            load8(a.h + row * a.width + col, n, h);
-            const float mean = a.mean[row], rstd = a.rstd[row];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dw[e] = fmaf(d[e], (h[e] - mean) * rstd, dw[e]);
-                db[e] += d[e];
-            }
-        }
-    const int mine = blockIdx.x * 256 + threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s_sum[rl][cl * 8 + e] = k ? db[e] : dw[e];
-        barrier_after_lds_write();
-        if (mine < a.width) {
-            float s = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                s += s_sum[r][threadIdx.x];
-            a.part[(k * a.parts + blockIdx.y) * a.width + mine] = s;
-        }
-        barrier_after_lds_write();
     }
 }
 
@@ -590,16 +630,25 @@ auto by_width(int64_t width, F f)
 #undef AG_NORM
 }
 
+// workgroups for the rows of a backward pass
+int64_t row_parts(int64_t rows, int tpr)
+{
+    const int rpw = std::max(1, 256 / tpr);
+    return std::min((rows + rpw - 1) / rpw, cus() * (tpr > 256 ? 1 : 2));
+}
+
+bool few_rows(int64_t rows, int64_t width) { return in_registers(width) && width <= 8192 && rows <= 256; }
+
+// rows of partial sums
 int64_t bwd_parts(int64_t rows, int64_t width)
 {
     if (rows <= 0 || width <= 0)
         return 0;
     if (!in_registers(width))
         return std::min<int64_t>((rows + 31) / 32, 32);
-    return by_width(width, [&](auto tpr, auto) {
-        constexpr int T = decltype(tpr)::value, rpw = kThreads<T> / T;
-        return std::min((rows + rpw - 1) / rpw, cus() * (T > 256 ? 1 : 2));
-    });
+    if (few_rows(rows, width))
+        return 0;
+    return by_width(width, [&](auto tpr, auto) { return row_parts(rows, decltype(tpr)::value); });
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -679,17 +728,31 @@ extern "C" int layer_norm_bwd(const void* dy, const void* h, const float* mean, 
     const NormBwdArgs a = {static_cast<const __bf16*>(dy), static_cast<const __bf16*>(h), static_cast<const __bf16*>(weight),
                            static_cast<const __bf16*>(dh), mean, rstd, rows, (int)width, static_cast<__bf16*>(dx),
                            static_cast<__bf16*>(dweight), static_cast<__bf16*>(dbias),
-                           sums ? static_cast<float*>(work) : nullptr, parts};
+                           sums && parts > 0 ? static_cast<float*>(work) : nullptr, parts};
     if (rows > 0 && !in_registers(width)) {
         if (dx)
             norm_bwd_wide_kernel<<<dim3((unsigned)std::min(rows, cus() * 2)), dim3(1024), 0, s>>>(a);
         if (sums)
             norm_cols_kernel<<<dim3((unsigned)((width + 255) / 256), (unsigned)parts), dim3(256), 0, s>>>(
                 a, (rows + parts - 1) / parts);
+    } else if (few_rows(rows, width) && sums && rows > 0) {
+        by_width(width, [&](auto tpr, auto c) {
+            constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
+            if constexpr (T < 1024) {
+                const int row_wgs = dx ? (int)((rows * T + kThreads<T> - 1) / kThreads<T>) : 0;
+                const dim3 grid((unsigned)(row_wgs + (width + 255) / 256)), block(kThreads<T>);
+                if (dx && dh)
+                    norm_bwd_few_kernel<T, C, true><<<grid, block, 0, s>>>(a, row_wgs);
+                else
+                    norm_bwd_few_kernel<T, C, false><<<grid, block, 0, s>>>(a, row_wgs);
+            }
+        });
+        NORM_HIP("launch layer_norm_bwd");
+        return AG_OK;
     } else if (rows > 0) {
         by_width(width, [&](auto tpr, auto c) {
             constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
-            const dim3 grid((unsigned)parts), block(kThreads<T>);
+            const dim3 grid((unsigned)row_parts(rows, T)), block(kThreads<T>);
             if (dx && dh)
                 norm_bwd_kernel<T, C, true><<<grid, block, 0, s>>>(a);
             else

@@ -27,6 +27,7 @@ namespace lm {
 struct OrthoArgs : TileArgs {
     float alpha, beta;       // out = alpha sums + beta addend, plus `unit` on the diagonal (kEpiSquare)
     float unit;
+    float square_alpha, square_beta;   // B out of A A and A, where X = B X forms it (ortho_thin_kernel)
     const float* scale;      // the first step's rest of the norm, a factor for each matrix: squared in A, once in X (null: 1)
     const _Float16* add;     // addend: A (kEpiSquare); X's remainder, or null (kEpiUpdate)
     _Float16 *hi, *lo;       // the result and (unless null) its remainder
@@ -262,13 +263,9 @@ __device__ __forceinline__ void ortho_body(const OrthoArgs& a)
     constexpr int BYTES = BM * BK * 2;
     static_assert(S == 2 ? LARGE : S == 3 || S == 4, "stages");
     __shared__ __attribute__((aligned(1024))) char sA0[LARGE ? BYTES / 2 : BYTES], sU0[LARGE ? BYTES / 2 : 16];
-    __shared__ __attribute__((aligned(1024))) char sB0[BYTES];
-    __shared__ __attribute__((aligned(1024))) char sA1[BYTES];
-    __shared__ __attribute__((aligned(1024))) char sB1[BYTES];
-    __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sB2[S > 2 ? BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sA3[S > 3 ? BYTES : 16];
-    __shared__ __attribute__((aligned(1024))) char sB3[S > 3 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sB0[BYTES], sA1[BYTES], sB1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char sA2[S > 2 ? BYTES : 16], sB2[S > 2 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char sA3[S > 3 ? BYTES : 16], sB3[S > 3 ? BYTES : 16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Stages<S> l;
     l.a[0] = {sA0, LARGE ? sU0 : sA0};
@@ -352,10 +349,232 @@ __global__ __launch_bounds__(NT, 1) void ortho128_kernel(OrthoArgs a)
     ortho_body<128, 4, EPI>(a);
 }
 
-template <int EPI>
-__global__ __launch_bounds__(NT, 2) void ortho64_kernel(OrthoArgs a)
+// 64 x 64 tiles, a workgroup for each, of matrices so small that a launch mostly waits: for its code, its first loads, LDS.
+// Everything about where a tile lies is one workgroup index each and 32 bits; a step's fragments are all read while the
+// step before multiplies; four steps are on their way.  H = 2: steps of 128, one workgroup a CU; H = 1: of 64, two.
+template <int EPI, int H>
+__global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a)
 {
-    ortho_body<64, 4, EPI>(a);
+    constexpr bool TB = EPI == kEpiUpdate;
+    constexpr int HALF = H * 8192, OPS = H * 4;        // bytes of a step's A, loads of a step
+    __shared__ __attribute__((aligned(1024))) char s0[2 * HALF], s1[2 * HALF], s2[2 * HALF], s3[2 * HALF];
+    const int tn = blockIdx.x, tm = blockIdx.y, e = blockIdx.z;
+    if (!TB && tn > tm)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+    const uint32_t lda = (uint32_t)a.lda * 2, ldb = (uint32_t)a.ldb * 2, r = tid >> 3, p = tid & 7;
+    const uint32_t va = r * lda + ((p ^ swz(r)) * 16);
+    const uint32_t vb = TB ? r * ldb + (((p >> 2) ^ Side<64, true>::ksw(r)) * 4 + (p & 3)) * 16 : r * ldb + ((p ^ swz(r)) * 16);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A + (e * a.M + tm * 64) * a.lda, 64 * lda);
+    const __amdgpu_buffer_rsrc_t rb = TB ? make_rsrc(a.B + e * a.strideB + tn * 64, (uint32_t)a.K * ldb - tn * 128)
+                                         : make_rsrc(a.B + e * a.strideB + (int64_t)tn * 64 * a.ldb, 64 * ldb);
+    const int steps = (int)a.K / (H * 64);
+    int at = 0;                                        // of the next loads; past the last step that one again
+    auto issue = [&](char* s) {
+        const uint32_t ka = at * H * 128, kb = TB ? at * H * 64 * ldb : ka;
+        at = min(at + 1, steps - 1);
+        char* const to = s + wave * 1024;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(to + h * 8192 + q * 4096), 16, (int)(va + q * 32 * lda),
+                                                         (int)(ka + h * 128), 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(to + HALF + h * 8192 + q * 4096), 16,
+                                                         (int)(vb + q * 32 * ldb), (int)(kb + h * (TB ? 64 * ldb : 128)), 0, 0);
+            }
+    };
+    issue(s0);
+    issue(s1);
+    issue(s2);
+    issue(s3);
+    Frag<64, false, 1, true> fa;
+    Frag<64, TB, 1, false> fb;
+    fa.init(lane, wm);
+    fb.init(lane, wn);
+    bf16x8 af[2][4 * H], bf[2][4 * H];
+    auto read = [&](int set, char* s) {
+#pragma unroll
+        for (int kk = 0; kk < 4 * H; ++kk) {
+            af[set][kk] = fa.read(Part{s + (kk >> 2) * 8192, nullptr}, kk & 3, 0);
+            bf[set][kk] = fb.read(Part{s + HALF + (kk >> 2) * 8192, nullptr}, kk & 3, 0);
+        }
+    };
+    f32x16 acc = {};
+    // the next step's loads are there, everyone has read this one's stage
+    auto step = [&](int set, char* s, char* next) {
+        wait_vmcnt<2 * OPS>();
+        stage_barrier();
+        issue(s);
+        read(set ^ 1, next);
+#pragma unroll
+        for (int kk = 0; kk < 4 * H; ++kk)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, bf[set][kk]), __builtin_bit_cast(f16x8, af[set][kk]),
+                                                         acc, 0, 0, 0);
+    };
+    wait_vmcnt<3 * OPS>();
+    stage_barrier();
+    read(0, s0);
+    int k = 0;
+    for (; k + 4 <= steps; k += 4) {
+        step(0, s0, s1);
+        step(1, s1, s2);
+        step(0, s2, s3);
+        step(1, s3, s0);
+    }
+    if (k < steps) {
+        step(0, s0, s1);
+        if (k + 1 < steps) {
+            step(1, s1, s2);
+            if (k + 2 < steps)
+                step(0, s2, s3);
+        }
+    }
+    wait_vmcnt0();
+    stage_barrier();
+    const Where w = {tm * 64, tn * 64, a.M, a.K, 0, 0, tn, e, 0, false};
+    after_sums<EPI, 1, 1, 2>(a, w, [&](int) { return &acc; }, s0 + wave * 2 * Slab<1>::BYTES, tm * 64 + wm * 32, tn * 64 + wn * 32, lane);
+}
+
+// ------------------------------------------------------------------------------------------- few rows
+// X = B X with B = a I + b A + c A A formed on the way, for MP = 128 or 256 rows (padded), whose products take less than a
+// launch: a workgroup holds all of A in LDS, makes 64 rows of B out of it and multiplies them with blocks of 64 columns of X,
+// the next block on its way meanwhile.  What every workgroup of the same 64 rows does again is 64 MP MP products.
+template <int MP>
+__global__ __launch_bounds__(NT, MP == 256 ? 1 : 2) void ortho_thin_kernel(OrthoArgs a)
+{
+    constexpr int KS = MP / 64, F = MP / 128, XOPS = 2 * KS;      // steps of 64; a wave's blocks of 32 columns of B
+    // A by steps of 64 columns, MP rows of 128 bytes each; then B's rows, the slabs and a second block of X
+    __shared__ __attribute__((aligned(1024))) char sT0[MP * 128];
+    __shared__ __attribute__((aligned(1024))) char sT1[MP * 128];
+    __shared__ __attribute__((aligned(1024))) char sT2[MP * 128];
+    __shared__ __attribute__((aligned(1024))) char sT3[KS > 2 ? MP * 128 : 16];
+    __shared__ __attribute__((aligned(1024))) char sX[MP * 128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const uint32_t fr = lane & 31, fh = lane >> 5, wave_off = wave * 1024;
+    const int blocks = (int)(a.N / 64), sharers = (int)(gridDim.x / (a.E * KS));      // workgroups of the same rows
+    const int first = (int)blockIdx.x % sharers, rb = (int)blockIdx.x / sharers % KS, e = (int)blockIdx.x / sharers / KS;
+    char* const stage[4] = {sT0, sT1, KS > 2 ? sT2 : sT0, KS > 2 ? sT3 : sT1};
+
+    Side<MP, false> sa;
+    sa.init(tid, a.lda);
+    sa.start(a.A + (int64_t)e * MP * MP, MP, MP, 0, 0, MP);
+    each<KS>([&](auto kb) {
+        const __amdgpu_buffer_rsrc_t r = sa.rsrc();
+        const Part p = {stage[kb], stage[kb] + 16384};
+#pragma unroll
+        for (int q = 0; q < MP / 32; ++q)
+            sa.load(r, p, wave_off, sa.offset(), sa.op_stride, q);
+        sa.advance();
+    });
+    Side<64, true> sx;
+    sx.init(tid, a.ldb);
+    auto fetch_x = [&](char* to, int block) {
+        sx.start(a.B + e * a.strideB + block * 64, 64, MP, block * 64, 0, MP);
+#pragma unroll
+        for (int kb = 0; kb < KS; ++kb) {
+            const __amdgpu_buffer_rsrc_t r = sx.rsrc();
+            const Part p = {to + kb * 8192, nullptr};
+            sx.load(r, p, wave_off, sx.offset(), sx.op_stride, 0);
+            sx.load(r, p, wave_off, sx.offset(), sx.op_stride, 1);
+            sx.advance();
+        }
+    };
+    fetch_x(sX, first);
+
+    // 64 rows of A A: a wave's MP / 4 columns
+    {
+        Frag<64, false, 2, false> fa;
+        Frag<64, false, F, false> fb;
+        fa.init(lane, 0);
+        fb.init(lane, 0);
+        f32x16 acc[2][F] = {};
+        each<KS>([&](auto kb) {
+            wait_vmcnt<(KS - 1 - decltype(kb)::value) * (MP / 32) + XOPS>();
+            stage_barrier();
+            const Part pa = {stage[kb] + rb * 8192, nullptr}, pb = {stage[kb] + wave * F * 4096, nullptr};
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                bf16x8 af[2], bf[F];
+#pragma unroll
+                for (int j = 0; j < F; ++j)
+                    bf[j] = fb.read(pb, kk, j);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    af[i] = fa.read(pa, kk, i);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < F; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, bf[j]),
+                                                                           __builtin_bit_cast(f16x8, af[i]), acc[i][j], 0, 0, 0);
+            }
+        });
+        const int kb = wave * F / 2;                   // the step in which the wave's columns are
+        const char* const from = KS == 2 ? (kb ? sT1 : sT0) : kb < 2 ? (kb ? sT1 : sT0) : (kb == 2 ? sT2 : sT3);
+        const uint32_t sw = swz(fr & 15);
+        auto place = [&](int i, int j, int q) {        // of four columns in a step's row
+            const uint32_t chunk = ((wave * F + j) & 1) * 4 + q;
+            return (uint32_t)(i * 32 + fr) * 128 + ((chunk ^ sw) * 16) + fh * 8;
+        };
+        f16x4 h[2][F][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) {
+                const int diagonal = rb * 64 + i * 32 + (int)fr - ((wave * F + j) * 32 + (int)fh * 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f16x4 y = *reinterpret_cast<const f16x4*>(from + rb * 8192 + place(i, j, q));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        h[i][j][q][c] = (_Float16)(fmaf(a.square_beta, (float)y[c], a.square_alpha * acc[i][j][q * 4 + c]) +
+                                                   (diagonal == q * 8 + c ? a.unit : 0.0f));
+                }
+            }
+        stage_barrier();                               // A is read
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f16x4*>(sT0 + kb * 8192 + place(i, j, q)) = h[i][j][q];
+    }
+
+    Frag<64, false, 1, true> fa;
+    Frag<64, true, 1, false> fb;
+    fa.init(lane, wm);
+    fb.init(lane, wn);
+    char* const slab = sT1 + wave * 2 * Slab<1>::BYTES;
+    auto block = [&](const char* x, char* other, int b) {
+        const int next = b + sharers;
+        if (next < blocks)
+            fetch_x(other, next);
+        if (next < blocks)
+            wait_vmcnt<XOPS>();
+        else
+            wait_vmcnt0();
+        stage_barrier();                               // B's rows are written, this block of X is there
+        f32x16 acc = {};
+#pragma unroll
+        for (int kb = 0; kb < KS; ++kb)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const bf16x8 bf = fb.read(Part{const_cast<char*>(x) + kb * 8192, nullptr}, kk, 0);
+                const bf16x8 af = fa.read(Part{sT0 + kb * 8192, nullptr}, kk, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, bf), __builtin_bit_cast(f16x8, af), acc, 0, 0, 0);
+            }
+        stage_barrier();                               // read: the block after the next may come there
+        const Where w = {rb * 64, b * 64, a.M, a.K, 0, 0, 0, e, 0, false};
+        after_sums<kEpiUpdate, 1, 1, 2>(a, w, [&](int) { return &acc; }, slab, rb * 64 + wm * 32, (int64_t)b * 64 + wn * 32, lane);
+    };
+    for (int b = first; b < blocks; b += 2 * sharers) {
+        block(sX, sT2, b);
+        if (b + sharers < blocks)
+            block(sT2, sX, b + sharers);
+    }
 }
 
 // ------------------------------------------------------------------------------------------- what comes first
@@ -482,31 +701,6 @@ struct Ortho {
     int64_t part, scale, x0, x1, lo, a, b, bytes;      // offsets in the workspace
 };
 
-Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
-{
-    Ortho o;
-    o.m = std::min(R, C);
-    o.n = std::max(R, C);
-    o.mp = up(o.m, PAD);
-    o.np = up(o.n, PAD);
-    o.parts = (int)std::max<int64_t>(1, std::min<int64_t>(1024, R * C / 8192));
-    int64_t at = 0;
-    auto region = [&](int64_t bytes) {
-        const int64_t here = at;
-        at += up(bytes, 256);
-        return here;
-    };
-    o.part = region(E * o.parts * 8);
-    o.scale = region(E * 4);
-    o.x0 = region(E * o.mp * o.np * 2);
-    o.x1 = region(E * o.mp * o.np * 2);
-    o.lo = region(E * o.mp * o.np * 2);
-    o.a = region(E * o.mp * o.mp * 2);
-    o.b = region(E * o.mp * o.mp * 2);
-    o.bytes = at;
-    return o;
-}
-
 bool ortho_too_large(int64_t E, int64_t R, int64_t C)
 {
     const int64_t m = std::min(R, C), n = std::max(R, C);
@@ -551,8 +745,8 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
     double least = 1e30;
     auto tile_us = [&](int size, double fill) {
         switch (size) {
-        case 64: return (fill > 1 ? 0.38 : 0.25) * steps + 4;
-        case 128: return 0.44 * steps + 5;
+        case 64: return (fill > 1 ? 0.36 : 0.16) * steps + (fill > 1 ? 4 : 5.5);
+        case 128: return 0.44 * steps + 8;
         case 192: return (0.7 + 0.35 * fill) * steps + 7;
         default: return (1.0 + 0.7 * fill) * steps + 12;
         }
@@ -566,6 +760,8 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
             continue;
         OrthoTiles t = {size, (M + size - 1) / size, (N + size - 1) / size, 0, 0};
         t.all = E * (lower ? t.rows * (t.rows + 1) / 2 : t.rows * t.cols);
+        if (size == 64 && t.all > 8 * cus)             // (offsets of 32 bits)
+            continue;
         double us = rounds(size, t.all);
         const int64_t rest = t.all % cus;
         if ((size == 128 || size == 256) && t.all > cus && rest) {
@@ -583,6 +779,31 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
     return best;
 }
 
+Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
+{
+    Ortho o;
+    o.m = std::min(R, C);
+    o.n = std::max(R, C);
+    o.mp = up(o.m, PAD);
+    o.np = up(o.n, PAD);
+    o.parts = (int)std::max<int64_t>(1, std::min<int64_t>(1024, R * C / 8192));
+    int64_t at = 0;
+    auto region = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    o.part = region(E * o.parts * 8);
+    o.scale = region(E * 4);
+    o.x0 = region(E * o.mp * o.np * 2);
+    o.x1 = region(E * o.mp * o.np * 2);
+    o.lo = region(E * o.mp * o.np * 2);
+    o.a = region(E * o.mp * o.mp * 2);
+    o.b = region(E * o.mp * o.mp * 2);
+    o.bytes = at;
+    return o;
+}
+
 // kEpiGram, kEpiSquare: tiles at and below the diagonal; kEpiUpdate: all of them.
 template <int EPI>
 hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
@@ -595,9 +816,16 @@ hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
     a.tiles_m = (int)t.rows;
     a.tiles_n = t.cols;
     a.cut = (int)t.cut;
-    const dim3 grid((unsigned)std::min(t.all - t.cut + 4 * t.cut, (int64_t)cus * (t.size == 64 ? 2 : 1)));
+    if (t.size == 64) {
+        const dim3 tiles((unsigned)t.cols, (unsigned)t.rows, (unsigned)a.E);
+        if (t.all <= cus)
+            ortho64_kernel<EPI, 2><<<tiles, dim3(NT), 0, s>>>(a);
+        else
+            ortho64_kernel<EPI, 1><<<tiles, dim3(NT), 0, s>>>(a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)std::min(t.all - t.cut + 4 * t.cut, (int64_t)cus));
     switch (t.size) {
-    case 64: ortho64_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a); break;
     case 128: ortho128_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a); break;
     case 192:
         if constexpr (EPI != kEpiUpdate)
@@ -605,6 +833,21 @@ hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
         break;
     default: ortho256_kernel<EPI><<<grid, dim3(NT), 0, s>>>(a);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_thin(const OrthoArgs& a, hipStream_t s)
+{
+    int cus = 0;
+    const hipError_t e = device_cus(&cus);
+    if (e != hipSuccess)
+        return e;
+    const int64_t rows = a.E * (a.M / 64), sharers = std::max<int64_t>(1, std::min(a.N / 64, (a.M == 128 ? 2 : 1) * cus / rows));
+    const dim3 grid((unsigned)(rows * sharers));
+    if (a.M == 128)
+        ortho_thin_kernel<128><<<grid, dim3(NT), 0, s>>>(a);
+    else
+        ortho_thin_kernel<256><<<grid, dim3(NT), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -714,14 +957,21 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.scale = i == 0 ? scale : nullptr;
         p.hi = half(o.a);
         ORTHO_HIP(launch_ortho<kEpiGram>(p, s), "launch newton_schulz X X^T");
-        p = product(o.a, o.mp, o.a, o.mp, o.mp, o.mp, o.mp, as);
-        p.alpha = c * (kScaleB / (kScaleA * kScaleA));
-        p.beta = b * (kScaleB / kScaleA);
+        const float square_alpha = c * (kScaleB / (kScaleA * kScaleA)), square_beta = b * (kScaleB / kScaleA);
+        const bool thin = o.mp <= 256;
+        if (!thin) {
+            p = product(o.a, o.mp, o.a, o.mp, o.mp, o.mp, o.mp, as);
+            p.alpha = square_alpha;
+            p.beta = square_beta;
+            p.unit = a * kScaleB;
+            p.add = half(o.a);
+            p.hi = half(o.b);
+            ORTHO_HIP(launch_ortho<kEpiSquare>(p, s), "launch newton_schulz A A");
+        }
+        p = product(thin ? o.a : o.b, o.mp, cur, o.np, o.mp, o.np, o.mp, xs);
+        p.square_alpha = square_alpha;
+        p.square_beta = square_beta;
         p.unit = a * kScaleB;
-        p.add = half(o.a);
-        p.hi = half(o.b);
-        ORTHO_HIP(launch_ortho<kEpiSquare>(p, s), "launch newton_schulz A A");
-        p = product(o.b, o.mp, cur, o.np, o.mp, o.np, o.mp, xs);
         p.alpha = 1.0f / kScaleB;
         p.beta = a;
         p.scale = i == 0 ? scale : nullptr;
@@ -736,7 +986,7 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
             p.n = o.n;
             p.turned = R > C;
         }
-        ORTHO_HIP(launch_ortho<kEpiUpdate>(p, s), "launch newton_schulz B X");
+        ORTHO_HIP(thin ? launch_thin(p, s) : launch_ortho<kEpiUpdate>(p, s), "launch newton_schulz B X");
         kept = keep;
         std::swap(cur, next);
     }

@@ -42,11 +42,11 @@ def test_norm_refusals():
 
 
 def test_norm_bwd_refusals():
-    need = ag.lib().layer_norm_bwd_workspace(64, 64)
+    need = ag.lib().layer_norm_bwd_workspace(640, 64)
     assert need > 0
 
     def call(**kw):
-        a = dict(dy=P[0], h=P[1], mean=P[2], rstd=P[3], w=P[4], dh=P[5], rows=64, width=64, dx=P[6], dw=P[7], db=P[8], work=P[9], n=need)
+        a = dict(dy=P[0], h=P[1], mean=P[2], rstd=P[3], w=P[4], dh=P[5], rows=640, width=64, dx=P[6], dw=P[7], db=P[8], work=P[9], n=need)
         a.update(kw)
         return ag.lib().layer_norm_bwd(a["dy"], a["h"], a["mean"], a["rstd"], a["w"], a["dh"], a["rows"], a["width"], a["dx"],
                                        a["dw"], a["db"], a["work"], a["n"], None)
