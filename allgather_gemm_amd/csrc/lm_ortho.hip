@@ -38,6 +38,10 @@ struct OrthoArgs : TileArgs {
     bool turned;
     int tiles_m;
     int cut;                 // of the tiles, those that go in quarters
+    // X X^T of a long reduction over few tiles: `splits` workgroups for each, whose fp32 sums go here, 4096 for each, and a
+    // count for each tile of those that are done, zero before and after
+    float* sums;
+    uint32_t* done;
 };
 
 namespace {
@@ -349,16 +353,66 @@ __global__ __launch_bounds__(NT, 1) void ortho128_kernel(OrthoArgs a)
     ortho_body<128, 4, EPI>(a);
 }
 
+// The parts of a 64 x 64 tile's reduction: each workgroup leaves its sums in memory and counts itself; the last one adds
+// them all up, in the parts' order whoever came last, and has the tile from there on (true).  Nobody waits.  The sums are
+// stored through the caches and counted when they have arrived, so no cache has to be written back (a release fence
+// does that with the whole L2: 25 us for 512 x 4096 in six parts, which takes 16 in one and 10 so).  The reader's
+// caches hold nothing of them: no one has read them in this launch.
+__device__ __forceinline__ bool join_parts(const OrthoArgs& a, int64_t tile, int part, f32x16& x)
+{
+    constexpr int kWriteThrough = 1 | 16;              // cache policy bits sc0 | sc1
+    __shared__ uint32_t s_before;
+    f32x4* const sums = reinterpret_cast<f32x4*>(a.sums) + tile * a.splits * 1024;
+    const __amdgpu_buffer_rsrc_t to = make_rsrc(sums + part * 1024, 16384);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(i32x4, f32x4{x[q * 4], x[q * 4 + 1], x[q * 4 + 2], x[q * 4 + 3]}), to,
+            (q * 256 + threadIdx.x) * 16, 0, kWriteThrough);
+    wait_vmcnt0();
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const uint32_t before = wave_fetch_add(a.done + tile, 1);
+        if (is_lane0())
+            s_before = before;
+    }
+    barrier_after_lds_write();
+    if ((int)__builtin_amdgcn_readfirstlane(s_before) != a.splits - 1)
+        return false;
+    acquire_agent();
+    if (threadIdx.x < 64)
+        wave_exchange(a.done + tile, 0);
+    x = f32x16{};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 y = sums[s * 1024 + q * 256 + threadIdx.x];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[q * 4 + e] += y[e];
+        }
+    }
+    return true;
+}
+
 // 64 x 64 tiles, a workgroup for each, of matrices so small that a launch mostly waits: for its code, its first loads, LDS.
 // Everything about where a tile lies is one workgroup index each and 32 bits; a step's fragments are all read while the
 // step before multiplies; four steps are on their way.  H = 2: steps of 128, one workgroup a CU; H = 1: of 64, two.
-template <int EPI, int H>
+// PARTS: of a tile's reduction.
+template <int EPI, int H, bool PARTS>
 __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a)
 {
     constexpr bool TB = EPI == kEpiUpdate;
     constexpr int HALF = H * 8192, OPS = H * 4;        // bytes of a step's A, loads of a step
     __shared__ __attribute__((aligned(1024))) char s0[2 * HALF], s1[2 * HALF], s2[2 * HALF], s3[2 * HALF];
-    const int tn = blockIdx.x, tm = blockIdx.y, e = blockIdx.z;
+    int tn = blockIdx.x, tm = blockIdx.y, part = 0;
+    const int e = blockIdx.z;
+    if constexpr (PARTS) {         // parts come first: a multiple of 8, so each XCD has its own columns of X in its cache
+        part = blockIdx.x;
+        tm = blockIdx.y / (uint32_t)a.tiles_n;
+        tn = blockIdx.y - tm * (int)a.tiles_n;
+    }
     if (!TB && tn > tm)
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
@@ -368,11 +422,12 @@ __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A + (e * a.M + tm * 64) * a.lda, 64 * lda);
     const __amdgpu_buffer_rsrc_t rb = TB ? make_rsrc(a.B + e * a.strideB + tn * 64, (uint32_t)a.K * ldb - tn * 128)
                                          : make_rsrc(a.B + e * a.strideB + (int64_t)tn * 64 * a.ldb, 64 * ldb);
-    const int steps = (int)a.K / (H * 64);
-    int at = 0;                                        // of the next loads; past the last step that one again
+    const int all = (int)a.K / (H * 64), begin = PARTS ? min(part * (int)a.split_steps, all) : 0;
+    const int end = PARTS ? min(begin + (int)a.split_steps, all) : all, steps = end - begin, last = max(end - 1, 0);
+    int at = min(begin, last);                         // of the next loads; past the last step that one again
     auto issue = [&](char* s) {
         const uint32_t ka = at * H * 128, kb = TB ? at * H * 64 * ldb : ka;
-        at = min(at + 1, steps - 1);
+        at = min(at + 1, last);
         char* const to = s + wave * 1024;
 #pragma unroll
         for (int h = 0; h < H; ++h)
@@ -432,6 +487,9 @@ __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a
     }
     wait_vmcnt0();
     stage_barrier();
+    if constexpr (PARTS)
+        if (!join_parts(a, ((int64_t)e * a.tiles_m + tm) * a.tiles_n + tn, part, acc))
+            return;
     const Where w = {tm * 64, tn * 64, a.M, a.K, 0, 0, tn, e, 0, false};
     after_sums<EPI, 1, 1, 2>(a, w, [&](int) { return &acc; }, s0 + wave * 2 * Slab<1>::BYTES, tm * 64 + wm * 32, tn * 64 + wn * 32, lane);
 }
@@ -616,6 +674,8 @@ struct StartArgs {
     float eps;
     const double* part;
     float* scale;
+    uint32_t* done;          // counts to be zero
+    int64_t counts;
     _Float16 *hi, *lo;       // lo may be null
 };
 
@@ -644,6 +704,9 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs 
     const int64_t i0 = blockIdx.x / tiles * 64, j0 = (int64_t)(blockIdx.x % tiles) * 64;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         a.scale[e] = (float)(1.0 / part);
+    if (blockIdx.x == 0 && e == 0)
+        for (int64_t i = threadIdx.x; i < a.counts; i += 256)
+            a.done[i] = 0;
     const int64_t g0 = TURN ? j0 : i0, h0 = TURN ? i0 : j0;             // the tile's first row and column in G
     const T* p = G + e * a.R * a.C;
     const int rl = threadIdx.x >> 2, cl = (threadIdx.x & 3) * 16;
@@ -698,7 +761,8 @@ int64_t up(int64_t x, int64_t n) { return (x + n - 1) / n * n; }
 struct Ortho {
     int64_t m, n, mp, np;
     int parts;
-    int64_t part, scale, x0, x1, lo, a, b, bytes;      // offsets in the workspace
+    int64_t part, scale, sums, done, x0, x1, lo, a, b, bytes;      // offsets in the workspace
+    int64_t counts;          // of tiles in parts
 };
 
 bool ortho_too_large(int64_t E, int64_t R, int64_t C)
@@ -733,10 +797,12 @@ void bounds(const float* q, double top, double* x, double* b)
 struct OrthoTiles {
     int size;
     int64_t rows, cols, all, cut;
+    int splits, split_steps;         // workgroups of a tile, steps of 128 that each takes
 };
 
-OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
+OrthoTiles plan_tiles(int epi, int64_t E, int64_t M, int64_t N, int64_t K)
 {
+    const bool lower = epi != kEpiUpdate;
     int cus = 0;
     if (device_cus(&cus) != hipSuccess || cus <= 0)
         cus = 256;
@@ -746,9 +812,9 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
     auto tile_us = [&](int size, double fill) {
         switch (size) {
         case 64: return (fill > 1 ? 0.36 : 0.16) * steps + (fill > 1 ? 4 : 5.5);
-        case 128: return 0.44 * steps + 8;
+        case 128: return 0.44 * steps + 5.5;
         case 192: return (0.7 + 0.35 * fill) * steps + 7;
-        default: return (1.0 + 0.7 * fill) * steps + 12;
+        default: return (1.0 + 0.7 * fill) * steps + 14;
         }
     };
     auto rounds = [&](int size, int64_t tiles) {
@@ -758,14 +824,16 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
     for (const int size : {64, 128, 192, 256}) {
         if (size == 192 && !lower)
             continue;
-        OrthoTiles t = {size, (M + size - 1) / size, (N + size - 1) / size, 0, 0};
+        OrthoTiles t = {size, (M + size - 1) / size, (N + size - 1) / size, 0, 0, 1, 0};
         t.all = E * (lower ? t.rows * (t.rows + 1) / 2 : t.rows * t.cols);
         if (size == 64 && t.all > 8 * cus)             // (offsets of 32 bits)
             continue;
-        double us = rounds(size, t.all);
+        double us = rounds(size, t.all) + (size == 128 ? 2.5 : 0);
+        if (size == 64 && epi == kEpiGram)             // what the tiles read between them
+            us = std::max(us, 5.5 + 256.0 * t.all * K / 11e6);
         const int64_t rest = t.all % cus;
         if ((size == 128 || size == 256) && t.all > cus && rest) {
-            const double cut = rounds(size, t.all - rest) + rounds(size / 2, 4 * rest);
+            const double cut = rounds(size, t.all - rest) + rounds(size / 2, 4 * rest) + (size == 128 ? 2.5 : 0);
             if (cut < us) {
                 us = cut;
                 t.cut = rest;
@@ -774,6 +842,17 @@ OrthoTiles plan_tiles(bool lower, int64_t E, int64_t M, int64_t N, int64_t K)
         if (us < least) {
             least = us;
             best = t;
+        }
+        // parts of a long reduction
+        for (int64_t parts = 8; epi == kEpiGram && size == 64 && parts <= 32 && parts * t.all <= 2 * cus; parts += 8) {
+            const int64_t each = (K / 128 + parts - 1) / parts;
+            us = (parts * t.all > cus ? 0.72 : 0.33) * each + 8.5 + 0.018 * parts * t.all;
+            if (us < least) {
+                least = us;
+                best = t;
+                best.splits = (int)parts;
+                best.split_steps = (int)each;
+            }
         }
     }
     return best;
@@ -795,6 +874,10 @@ Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
     };
     o.part = region(E * o.parts * 8);
     o.scale = region(E * 4);
+    const OrthoTiles gram = plan_tiles(kEpiGram, E, o.mp, o.mp, o.np);
+    o.counts = gram.splits > 1 ? E * gram.rows * gram.cols : 0;
+    o.sums = region(o.counts * gram.splits * 16384);
+    o.done = region(o.counts * 4);
     o.x0 = region(E * o.mp * o.np * 2);
     o.x1 = region(E * o.mp * o.np * 2);
     o.lo = region(E * o.mp * o.np * 2);
@@ -812,16 +895,30 @@ hipError_t launch_ortho(OrthoArgs a, hipStream_t s)
     const hipError_t e = device_cus(&cus);
     if (e != hipSuccess)
         return e;
-    const OrthoTiles t = plan_tiles(EPI != kEpiUpdate, a.E, a.M, a.N, a.K);
+    const OrthoTiles t = plan_tiles(EPI, a.E, a.M, a.N, a.K);
+    a.splits = t.splits;
+    a.split_steps = t.split_steps;
     a.tiles_m = (int)t.rows;
     a.tiles_n = t.cols;
     a.cut = (int)t.cut;
     if (t.size == 64) {
         const dim3 tiles((unsigned)t.cols, (unsigned)t.rows, (unsigned)a.E);
+        if constexpr (EPI == kEpiGram) {
+            if (t.splits > 1) {
+                const dim3 parts((unsigned)t.splits, tiles.x * tiles.y, tiles.z);
+                if (t.all * t.splits > cus) {
+                    a.split_steps *= 2;                // of 64
+                    ortho64_kernel<EPI, 1, true><<<parts, dim3(NT), 0, s>>>(a);
+                } else {
+                    ortho64_kernel<EPI, 2, true><<<parts, dim3(NT), 0, s>>>(a);
+                }
+                return hipGetLastError();
+            }
+        }
         if (t.all <= cus)
-            ortho64_kernel<EPI, 2><<<tiles, dim3(NT), 0, s>>>(a);
+            ortho64_kernel<EPI, 2, false><<<tiles, dim3(NT), 0, s>>>(a);
         else
-            ortho64_kernel<EPI, 1><<<tiles, dim3(NT), 0, s>>>(a);
+            ortho64_kernel<EPI, 1, false><<<tiles, dim3(NT), 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)std::min(t.all - t.cut + 4 * t.cut, (int64_t)cus));
@@ -924,7 +1021,8 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
     };
     bool kept = g_type == AG_TYPE_F32 && keeps(-1);
     float* const scale = reinterpret_cast<float*>(ws + o.scale);
-    const StartArgs st = {R, C, o.mp, o.np, o.parts, eps, reinterpret_cast<double*>(ws + o.part), scale, half(o.x0),
+    const StartArgs st = {R, C, o.mp, o.np, o.parts, eps, reinterpret_cast<double*>(ws + o.part), scale,
+                          reinterpret_cast<uint32_t*>(ws + o.done), o.counts, half(o.x0),
                           kept ? half(o.lo) : nullptr};
     if (g_type == AG_TYPE_F32)
         launch_start<float>(G, o, st, E, s);
@@ -956,6 +1054,8 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.alpha = kScaleA / (kScaleX * kScaleX);
         p.scale = i == 0 ? scale : nullptr;
         p.hi = half(o.a);
+        p.sums = reinterpret_cast<float*>(ws + o.sums);
+        p.done = reinterpret_cast<uint32_t*>(ws + o.done);
         ORTHO_HIP(launch_ortho<kEpiGram>(p, s), "launch newton_schulz X X^T");
         const float square_alpha = c * (kScaleB / (kScaleA * kScaleA)), square_beta = b * (kScaleB / kScaleA);
         const bool thin = o.mp <= 256;
