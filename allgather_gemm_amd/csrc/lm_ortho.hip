@@ -765,16 +765,18 @@ struct Ortho {
     int64_t counts;          // of tiles in parts
 };
 
+// Workgroups of a launch: 64 x 64 elements each at the start, tiles of 128 x 128 and their quarters in 32 bits.
 bool ortho_too_large(int64_t E, int64_t R, int64_t C)
 {
-    const int64_t m = std::min(R, C), n = std::max(R, C);
-    return n > 1 << 20 || E > 65535 || m * n > (int64_t)1 << 36 || E * ((m + 127) / 128) * ((n + 127) / 128) > 1 << 26;
+    const int64_t n = std::max(R, C), tiles = ((R + 127) / 128) * ((C + 127) / 128);
+    return n > 1 << 20 || E > 65535 || tiles > 1 << 21 || E * tiles > 1 << 26;
 }
 
-// The largest |s (a + b t + c t^2)| and |a + b t + c t^2| for t = s^2, s in [0, top].
+// The largest |s (a + b t + c t^2)| and |a + b t + c t^2| for t = s^2, s in [0, top] and a hundredth beyond, which covers
+// what the roundings add to a singular value.
 void bounds(const float* q, double top, double* x, double* b)
 {
-    const double A = q[0], B = q[1], C = q[2], T = top * top;
+    const double A = q[0], B = q[1], C = q[2], T = 1.01 * top * (1.01 * top);
     double t[4] = {0.0, T, T, T};
     int n = 2;
     const double disc = 9 * B * B - 20 * A * C;                          // a + 3 b t + 5 c t^2 = 0

@@ -314,7 +314,7 @@ int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float
  * Every singular value s of X becomes s (a + b s^2 + c s^4), step by step.  The products take fp16 of X, A and
  * a I + b A + c A A, with fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.  Coefficients whose X could
  * have a singular value above 3.5 on the way, or whose |a + b t + c t^2| could exceed 28 (t: the squares), return
- * AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, more than 2^36 elements of a matrix or 2^26 tiles of 128 x 128.  A matrix
+ * AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  A matrix
  * with an infinity or NaN gives NaN throughout.
  */
 #define AG_TYPE_BF16  0

@@ -115,8 +115,10 @@ def test_forward_and_backward(i, width):
 
 
 # more rows than a launch has workgroups for, and enough for many partial sums
-@pytest.mark.parametrize("rows,width", [(20001, 72), (9000, 200), (5003, 1000), (5000, 1504), (4100, 4096), (2100, 6000), (1500, 9001),
-                                        (700, 17000)])
+MANY = [(20001, 72), (9000, 200), (5003, 500), (5003, 1000), (5000, 1504), (4100, 4096), (2100, 6000), (1500, 9001), (700, 17000)]
+
+
+@pytest.mark.parametrize("rows,width", MANY)
 def test_many_rows(rows, width):
     g = gen(rows)
     print("norm", rows, width, flush=True)
@@ -128,9 +130,10 @@ def test_many_rows(rows, width):
     assert torch.equal(h, s)
     for name, got, (want, off) in zip(("y", "mean", "rstd"), (y, mean, rstd), forward(s, w, b, EPS)):
         near(got, want, off, name)
-    first = ag.layer_norm_bwd(dy, h, mean, rstd, weight=w, dh=dh)
-    for name, t, (want, off) in zip(("dx", "dw", "db"), first, backward(dy, h, mean, rstd, w, dh)):
-        near(t, want, off, name)
+    for more in (None, dh):
+        first = ag.layer_norm_bwd(dy, h, mean, rstd, weight=w, dh=more)
+        for name, t, (want, off) in zip(("dx", "dw", "db"), first, backward(dy, h, mean, rstd, w, more)):
+            near(t, want, off, name)
     # the sums' order is the shape's alone
     for t, u in zip(first, ag.layer_norm_bwd(dy, h, mean, rstd, weight=w, dh=dh)):
         assert torch.equal(t, u)

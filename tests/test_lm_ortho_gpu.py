@@ -48,7 +48,8 @@ def near(G, got, steps=ag.NEWTON_SCHULZ, what="", eps=EPS):
 
 # one element to many, a row, a column, odd extents, borders of the padding and of both tiles, tall and wide
 SHAPES = [(1, 1), (1, 9), (9, 1), (2, 3), (7, 300), (300, 7), (16, 16), (64, 64), (65, 127), (128, 128), (129, 128), (128, 129),
-          (130, 257), (256, 256), (257, 255), (500, 1003), (1003, 500), (512, 256), (640, 1000), (1000, 1000), (1280, 4100), (4100, 1280)]
+          (130, 257), (256, 256), (257, 255), (500, 1003), (1003, 500), (512, 256), (640, 1000), (1000, 1000), (1280, 4100), (4100, 1280),
+          (100, 5440), (8000, 250), (640, 8192), (1030, 1100), (1024, 2048), (1500, 1600)]
 
 
 @pytest.mark.parametrize("i,shape", list(enumerate(SHAPES)))
@@ -68,7 +69,10 @@ def test_shapes(i, shape, dtype):
 
 
 # a round of the large tiles and more, for all three products, odd numbers of them
-@pytest.mark.parametrize("shape", [(4096, 4224), (4000, 5000), (6016, 6016), (9000, 2100)])
+LARGE = [(2050, 2048), (4096, 4224), (4000, 5000), (6016, 6016), (9000, 2100)]
+
+
+@pytest.mark.parametrize("shape", LARGE)
 def test_large(shape):
     print("newton_schulz", shape, flush=True)
     G = torch.randn(*shape, generator=gen(shape[0])).cuda()
@@ -130,7 +134,11 @@ def test_zeros_infinities_and_nan():
     assert ag.newton_schulz(torch.zeros(5, 0, device="cuda")).shape == (5, 0)
 
 
-@pytest.mark.parametrize("E,R,C", [(2, 64, 100), (5, 300, 130), (7, 129, 513), (16, 1024, 600), (40, 72, 72), (3, 2100, 2050)])
+STACKS = [(2, 64, 100), (5, 300, 130), (7, 129, 513), (16, 1024, 600), (40, 72, 72), (3, 2100, 2050), (3, 200, 4000), (2, 640, 7000),
+          (4, 1100, 1024), (16, 520, 1000)]
+
+
+@pytest.mark.parametrize("E,R,C", STACKS)
 def test_stacks(E, R, C):
     print("stack", E, R, C, flush=True)
     g = gen(E)
