@@ -606,37 +606,70 @@ int64_t cus()
     return n;
 }
 
-// f(TPR, C) with the threads and pieces for rows of `width` <= kNormWidest columns
+// f(TPR, C, workgroups of a CU): the threads and pieces of rows of `width` <= kNormWidest columns.  Few enough threads that all
+// have columns, pieces enough to be in flight, and no more workgroups than it takes: each more walks through memory at a
+// place of its own.  us, 65536 rows up to 2000 columns, 2^27 values beyond:
+//   forward, 8 | 4 workgroups a CU (16 | 32 threads ... where narrower rows leave lanes idle): 100 columns 11.9 | 12.5 (64 threads
+//   30), 200 19.0 | 19.9 (64: 29), 500 46.2 | 46.1 (256: 102), 1000 109.9 | 98.6 (256: 123), 2000 217 | 205 (64 threads of
+//   four pieces 233 | 275), 4096 211 | 193 (512 threads 198 | 200); 8192 512 threads, 2 a CU 194.5, 256 of four pieces 263,
+//   4 a CU 193; 14336 512 of four pieces, 2 a CU 208, 1024 of two 222 (1 a CU 218)
 template <typename F>
-auto by_width(int64_t width, F f)
+auto forward_by_width(int64_t width, F f)
 {
     using std::integral_constant;
-#define AG_NORM(TPR, C) return f(integral_constant<int, TPR>(), integral_constant<int, C>())
+#define AG_NORM(TPR, C, PER) return f(integral_constant<int, TPR>(), integral_constant<int, C>(), PER)
     if (width <= 128)
-        AG_NORM(16, 1);
+        AG_NORM(16, 1, 8);
     if (width <= 256)
-        AG_NORM(32, 1);
+        AG_NORM(32, 1, 8);
     if (width <= 512)
-        AG_NORM(64, 1);
+        AG_NORM(64, 1, 8);
     if (width <= 1024)
-        AG_NORM(64, 2);
+        AG_NORM(64, 2, 4);
     if (width <= 2048)
-        AG_NORM(256, 1);
+        AG_NORM(256, 1, 4);
     if (width <= 4096)
-        AG_NORM(256, 2);
+        AG_NORM(256, 2, 4);
     if (width <= 8192)
-        AG_NORM(512, 2);
-    AG_NORM(1024, 2);
+        AG_NORM(512, 2, 2);
+    AG_NORM(512, 4, 2);
+}
+
+// The same for the gradients, whose rows of partial sums are one for each workgroup.  With dh | without, us, 1, 2, 4 workgroups
+// a CU: 100 columns 21 19 21 | 19 18 19, 500 62 50 52 | 54 41 43, 1000 107 108 116 | 94 82 91, 2000 64 threads of four pieces
+// 205 226 230 | 150 166 174 (256 threads 297 215 235 | 234 180 173), 4096 256 threads 207 216 228 | 168 169 178 (512 threads
+// 207 213 226 | 188 164 181), 8192 200 216 245 | 157 173 192 (256 of four pieces 205 222 255 | 158 176 194), 14336 215 239 282 |
+// 173 195 240 (512 of four pieces 223 248 293 | 176 194 246)
+template <typename F>
+auto backward_by_width(int64_t width, F f)
+{
+    using std::integral_constant;
+    if (width <= 128)
+        AG_NORM(16, 1, 2);
+    if (width <= 256)
+        AG_NORM(32, 1, 2);
+    if (width <= 512)
+        AG_NORM(64, 1, 2);
+    if (width <= 1024)
+        AG_NORM(64, 2, 2);
+    if (width <= 2048)
+        AG_NORM(64, 4, 1);
+    if (width <= 4096)
+        AG_NORM(256, 2, 1);
+    if (width <= 8192)
+        AG_NORM(512, 2, 1);
+    AG_NORM(1024, 2, 1);
 #undef AG_NORM
 }
 
-// workgroups for the rows of a backward pass
-int64_t row_parts(int64_t rows, int tpr)
+int64_t row_workgroups(int64_t rows, int tpr, int per_cu)
 {
-    const int rpw = std::max(1, 256 / tpr);
-    return std::min((rows + rpw - 1) / rpw, cus() * (tpr > 256 ? 1 : 2));
+    const int at_a_time = std::max(1, 256 / tpr);
+    return std::min((rows + at_a_time - 1) / at_a_time, cus() * per_cu);
 }
 
+// Gradients for rows that few workgroups read twice rather than another launch join their sums, us: 256 rows of 256 columns
+// 13.2 | 15.9, 4096 14.3 | 16.0, 8192 11.6 | 23.4; 128 x 4096 11.5 | 16.0
 bool few_rows(int64_t rows, int64_t width) { return in_registers(width) && width <= 8192 && rows <= 256; }
 
 // rows of partial sums
@@ -648,7 +681,7 @@ int64_t bwd_parts(int64_t rows, int64_t width)
         return std::min<int64_t>((rows + 31) / 32, 32);
     if (few_rows(rows, width))
         return 0;
-    return by_width(width, [&](auto tpr, auto) { return row_parts(rows, decltype(tpr)::value); });
+    return backward_by_width(width, [&](auto tpr, auto, int per) { return row_workgroups(rows, decltype(tpr)::value, per); });
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -689,10 +722,9 @@ extern "C" int layer_norm(const void* x, const void* residual, const void* weigh
     if (!in_registers(width))
         norm_wide_kernel<<<dim3((unsigned)std::min(rows, cus() * 2)), dim3(1024), 0, s>>>(a);
     else
-        by_width(width, [&](auto tpr, auto c) {
-            constexpr int T = decltype(tpr)::value, C = decltype(c)::value, rpw = kThreads<T> / T;
-            const int64_t grid = std::min((rows + rpw - 1) / rpw, cus() * (T > 256 ? 2 : 8));
-            norm_kernel<T, C><<<dim3((unsigned)grid), dim3(kThreads<T>), 0, s>>>(a);
+        forward_by_width(width, [&](auto tpr, auto c, int per) {
+            constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
+            norm_kernel<T, C><<<dim3((unsigned)row_workgroups(rows, T, per)), dim3(kThreads<T>), 0, s>>>(a);
         });
     NORM_HIP("launch layer_norm");
     return AG_OK;
@@ -736,7 +768,7 @@ extern "C" int layer_norm_bwd(const void* dy, const void* h, const float* mean, 
             norm_cols_kernel<<<dim3((unsigned)((width + 255) / 256), (unsigned)parts), dim3(256), 0, s>>>(
                 a, (rows + parts - 1) / parts);
     } else if (few_rows(rows, width) && sums && rows > 0) {
-        by_width(width, [&](auto tpr, auto c) {
+        backward_by_width(width, [&](auto tpr, auto c, int) {
             constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
             if constexpr (T < 1024) {
                 const int row_wgs = dx ? (int)((rows * T + kThreads<T> - 1) / kThreads<T>) : 0;
@@ -750,9 +782,9 @@ extern "C" int layer_norm_bwd(const void* dy, const void* h, const float* mean, 
         NORM_HIP("launch layer_norm_bwd");
         return AG_OK;
     } else if (rows > 0) {
-        by_width(width, [&](auto tpr, auto c) {
+        backward_by_width(width, [&](auto tpr, auto c, int per) {
             constexpr int T = decltype(tpr)::value, C = decltype(c)::value;
-            const dim3 grid((unsigned)row_parts(rows, T)), block(kThreads<T>);
+            const dim3 grid((unsigned)row_workgroups(rows, T, per)), block(kThreads<T>);
             if (dx && dh)
                 norm_bwd_kernel<T, C, true><<<grid, block, 0, s>>>(a);
             else

@@ -1019,7 +1019,7 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         double gain = 1.0;
         for (int32_t i = step + 1; i < steps; ++i)
             gain *= std::fabs((double)coefficients[3 * i]);
-        return gain > 16.0;
+        return gain > 8.0;
     };
     bool kept = g_type == AG_TYPE_F32 && keeps(-1);
     float* const scale = reinterpret_cast<float*>(ws + o.scale);
