@@ -80,10 +80,12 @@ __device__ __forceinline__ bf16x8 take8(const __bf16* p, int n)
     return v;
 }
 
+// The stores leave the L2 caches to what is read, us: forward 16384 x 4096 99.5 | 96.1 so, 16384 x 8192 194 | 189, gradients
+// 8192 x 14336 151 | 148, 65536 x 200 28.7 | 25.5 (forward 19.2 | 19.4).
 __device__ __forceinline__ void give8(__bf16* p, int n, bf16x8 v)
 {
     if (n >= 8) {
-        *reinterpret_cast<bf16x8_any*>(p) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<bf16x8_any*>(p));
         return;
     }
 #pragma unroll
@@ -375,7 +377,7 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int64_t firs
         r.rstd = a.rstd[row];
     };
     const int64_t step = workgroups * RPW;
-    constexpr bool AHEAD = TPR < 1024;                 // those have no registers for a second row
+    constexpr bool AHEAD = TPR < 1024 || !DH;          // the others have no registers for a second row
     auto compute = [&](Row& r, Row& next, int64_t row) {
         if constexpr (!AHEAD)
             fetch(r, row);
@@ -606,13 +608,13 @@ int64_t cus()
     return n;
 }
 
-// f(TPR, C, workgroups of a CU): the threads and pieces of rows of `width` <= kNormWidest columns.  Few enough threads that all
-// have columns, pieces enough to be in flight, and no more workgroups than it takes: each more walks through memory at a
-// place of its own.  us, 65536 rows up to 2000 columns, 2^27 values beyond:
-//   forward, 8 | 4 workgroups a CU (16 | 32 threads ... where narrower rows leave lanes idle): 100 columns 11.9 | 12.5 (64 threads
-//   30), 200 19.0 | 19.9 (64: 29), 500 46.2 | 46.1 (256: 102), 1000 109.9 | 98.6 (256: 123), 2000 217 | 205 (64 threads of
-//   four pieces 233 | 275), 4096 211 | 193 (512 threads 198 | 200); 8192 512 threads, 2 a CU 194.5, 256 of four pieces 263,
-//   4 a CU 193; 14336 512 of four pieces, 2 a CU 208, 1024 of two 222 (1 a CU 218)
+// f(TPR, C, workgroups a CU): the threads and pieces of rows of `width` <= kNormWidest columns.  As few threads as have
+// columns each, pieces enough to be in flight, and no more workgroups than that takes: each walks through memory at a place
+// of its own.  us for 65536 rows up to 2000 columns, 2^27 values beyond; the first is what is taken:
+//    100 columns, 16 threads 11.9, 4 workgroups a CU 12.5, 64 threads 30;    200, 32 threads 19.0, 19.9, 64 threads 29
+//    500, 64 threads 46.2, 4 a CU 46.1, 256 threads 102;    1000, 64 of two pieces 98.6, 8 a CU 110, 256 threads 123
+//   2000, 256 threads 205, 8 a CU 217, 64 of four pieces 275;    4096, 256 of two 193, 8 a CU 211, 512 threads 200
+//   8192, 512 of two 194, 4 a CU 214, 256 of four 193 at 4;    14336, 512 of four 208, 4 a CU 255, 1024 of two 218
 template <typename F>
 auto forward_by_width(int64_t width, F f)
 {
@@ -635,11 +637,12 @@ auto forward_by_width(int64_t width, F f)
     AG_NORM(512, 4, 2);
 }
 
-// The same for the gradients, whose rows of partial sums are one for each workgroup.  With dh | without, us, 1, 2, 4 workgroups
-// a CU: 100 columns 21 19 21 | 19 18 19, 500 62 50 52 | 54 41 43, 1000 107 108 116 | 94 82 91, 2000 64 threads of four pieces
-// 205 226 230 | 150 166 174 (256 threads 297 215 235 | 234 180 173), 4096 256 threads 207 216 228 | 168 169 178 (512 threads
-// 207 213 226 | 188 164 181), 8192 200 216 245 | 157 173 192 (256 of four pieces 205 222 255 | 158 176 194), 14336 215 239 282 |
-// 173 195 240 (512 of four pieces 223 248 293 | 176 194 246)
+// The same for the gradients, whose partial sums are a row for each workgroup.  us at 1 | 2 | 4 workgroups a CU, with dh; without:
+//    100 columns 21 | 19 | 21; 19 | 18 | 19    500 62 | 50 | 52; 54 | 41 | 43    1000 107 | 108 | 116; 94 | 82 | 91
+//   2000, 64 threads of four pieces 205 | 226 | 230; 150 | 166 | 174, 256 threads 297 | 215 | 235; 234 | 180 | 173
+//   4096, 256 threads of two 207 | 216 | 228; 168 | 169 | 178, 512 threads 207 | 213 | 226; 188 | 164 | 181
+//   8192, 512 of two 200 | 216 | 245; 157 | 173 | 192, 256 of four 205 | 222 | 255; 158 | 176 | 194
+//  14336, 1024 of two 215 | 239 | 282; 173 | 195 | 240, 512 of four 223 | 248 | 293; 176 | 194 | 246
 template <typename F>
 auto backward_by_width(int64_t width, F f)
 {
