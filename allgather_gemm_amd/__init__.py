@@ -1,5 +1,5 @@
 """Python binding of libaggemm (include/aggemm.h): chunked AllGather fused with a bf16 GEMM, TGATHER,
-and a language model's operators around the gathered product, on one MI355X.
+and a language model's operators around the gathered product (products, norms and updates), on one MI355X.
 
 Argument marshalling only: every step of the path runs in the library's gfx950 kernels.  Tensors
 are torch CUDA (HIP) tensors; the library is given their device pointers and the current stream.

@@ -16,7 +16,10 @@ constexpr int64_t kMostWorkgroups = (1 << 24) - 8;
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Group { kGroupRows = 1, kGroupK = 2 };     // 0: no groups
-enum Epi { kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3, kEpiScaled = 4, kEpiGram = 5, kEpiSquare = 6, kEpiUpdate = 7 };
+// kEpiGram, kEpiSquare, kEpiUpdate: fp16 factors, X X^T, A A and B X of newton_schulz (lm_ortho.hip)
+enum Epi {
+    kEpiLinear = 0, kEpiStat = 1, kEpiGrad = 2, kEpiSum = 3, kEpiScaled = 4, kEpiGram = 5, kEpiSquare = 6, kEpiUpdate = 7
+};
 // kTile128: four stages, one workgroup a CU; kTileShort: 128 x 128 with one stage, a workgroup for each tile and
 // four of them on a CU, no groups
 enum Tile { kTile256 = 0, kTile128 = 1, kTile32 = 2, kTileShort = 3 };

@@ -5,15 +5,20 @@
 //
 // Products by fp16 matrix instructions with fp32 sums: the iterates' singular values stay below a bound that the
 // coefficients give (checked by the entry point), so fp16 with a fixed scale holds them, with three bits more than bf16.
-// What a rounding of X does is not the same everywhere: an error e among X's small left and right singular directions comes
+// What a rounding of X does is not the same everywhere: an error among X's small left and right singular directions comes
 // out multiplied by the remaining steps' a's (3.4445^4 after the first of five), any other by about one.  Through A, and
 // through B's own rounding, what is off reaches those directions only times X, which is small there; a rounding of X is in
-// them as it is.  So the iterates are kept as two fp16, value and remainder, as long as the remaining gain is large: the
-// products take the value alone, and a times the remainder is added to B X (B times it, but for what does not grow).  (Error of 1024 x 1024 with singular values i^-1.5, of the result's norm: with one fp16 1.2e-2,
-// with bf16 9e-2, so 2.0e-3, of which 1.66e-3 is the result's own rounding to bf16.)
+// them as it is.  So the iterates are kept as two fp16, value and remainder, while the remaining gain is above 8: the products
+// take the value alone, and a times the remainder is added to B X (B times it, but for what does not grow).  Error of the
+// result's norm for a 4096 x 4096 momentum of shared directions and noise: 6.5e-3 without remainders, 1.96e-3 with them down to
+// a gain of 16, 1.77e-3 to 8, 1.74e-3 to 3, of which 1.66e-3 is the result's own rounding to bf16; they take 2.5 % of the time.
 //
 // A and A A are symmetric: their tiles at and below the diagonal are computed, and each is stored on both sides of it.  All
 // extents are padded to whole tiles of 128 with zeros, which the steps keep.
+//
+// Five steps of 4096 x 4096 take 1.35 ms, 1.0 PFLOP/s of the products that are computed, of 14336 x 4096 3.65 ms, 1.08: matrix
+// instructions at the clock that the power leaves (busy 0.51-0.54 of the cycles in A A and X X^T, 0.61 in B X, 0.71 in the longer
+// X X^T).  Small matrices wait for their launches, two or three a step of 5 to 10 us.
 #include "../../include/aggemm.h"
 #include "ag_internal.hpp"
 #include "lm_tile.hpp"
@@ -356,8 +361,7 @@ __global__ __launch_bounds__(NT, 1) void ortho128_kernel(OrthoArgs a)
 // The parts of a 64 x 64 tile's reduction: each workgroup leaves its sums in memory and counts itself; the last one adds
 // them all up, in the parts' order whoever came last, and has the tile from there on (true).  Nobody waits.  The sums are
 // stored through the caches and counted when they have arrived, so no cache has to be written back (a release fence
-// does that with the whole L2: 25 us for 512 x 4096 in six parts, which takes 16 in one and 10 so).  The reader's
-// caches hold nothing of them: no one has read them in this launch.
+// does that with the whole L2: X X^T of 512 x 4096 in six parts took 25 us with it, 15 without, as long as in one part).
 __device__ __forceinline__ bool join_parts(const OrthoArgs& a, int64_t tile, int part, f32x16& x)
 {
     constexpr int kWriteThrough = 1 | 16;              // cache policy bits sc0 | sc1
@@ -399,7 +403,8 @@ __device__ __forceinline__ bool join_parts(const OrthoArgs& a, int64_t tile, int
 // 64 x 64 tiles, a workgroup for each, of matrices so small that a launch mostly waits: for its code, its first loads, LDS.
 // Everything about where a tile lies is one workgroup index each and 32 bits; a step's fragments are all read while the
 // step before multiplies; four steps are on their way.  H = 2: steps of 128, one workgroup a CU; H = 1: of 64, two.
-// PARTS: of a tile's reduction.
+// PARTS: of a tile's reduction.  X X^T of 1024 x 1024 7.4 us, of 1024 x 8192 26.5 (0.165 a step of 64); as product_tile() has
+// it, with the tiles' general order, 11.9 and 34.3.
 template <int EPI, int H, bool PARTS>
 __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a)
 {
@@ -497,7 +502,9 @@ __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a
 // ------------------------------------------------------------------------------------------- few rows
 // X = B X with B = a I + b A + c A A formed on the way, for MP = 128 or 256 rows (padded), whose products take less than a
 // launch: a workgroup holds all of A in LDS, makes 64 rows of B out of it and multiplies them with blocks of 64 columns of X,
-// the next block on its way meanwhile.  What every workgroup of the same 64 rows does again is 64 MP MP products.
+// the next block on its way meanwhile.  What every workgroup of the same 64 rows does again is 64 MP MP products.  Five steps
+// so | by a launch for B, us: 64 x 64 49 | 66, 128 x 512 59 | 72, 128 x 4096 80 | 95, 256 x 512 72 | 79, 256 x 8192 121 | 121,
+// 25 of 72 x 5440 254 | 300.
 template <int MP>
 __global__ __launch_bounds__(NT, MP == 256 ? 1 : 2) void ortho_thin_kernel(OrthoArgs a)
 {
@@ -795,7 +802,13 @@ void bounds(const float* q, double top, double* x, double* b)
         *b = std::max(*b, std::fabs(A - B * B / (4 * C)));
 }
 
-// A launch: its tiles, and how many of the last ones go in quarters.
+// A launch: its tiles, and how many of the last ones go in quarters.  The least by a model of their times, whose constants are
+// measured; 64 | 128 | 192 | 256 wide, us:  X X^T (A A alike)  1024 x 4096 16 | 28 | 46 | 77,  2048 x 2048 26 | 19 | 29 | 46,
+// 2048 x 5632 73 | 41 | 65 | 109,  4096 x 4096 139 | 99 | 75 | 96,  6016 x 6016 579 | 267 | 255 | 226,  16 of 1024 x 2048
+// 102 | 52 | 71 | 55;  B X  1024 x 4096 19.6 | 16.3 | - | 33,  2048 x 5632 84 | 65 | - | 55,  4096 x 4096 226 | 162 | - | 120,
+// 16 of 1024 x 2048 134 | 107 | - | 80.  (192 x 192 is 253 tiles of 4096 x 4096, a round; a column operand's swizzle has no
+// such width.)  In parts | in one, five steps: 100 x 5440 84 | 129, 250 x 8000 121 | 188, 640 x 8192 215 | 250; 512 x 4096, in
+// one, 149.
 struct OrthoTiles {
     int size;
     int64_t rows, cols, all, cut;

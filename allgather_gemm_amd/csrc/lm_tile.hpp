@@ -1,5 +1,5 @@
 // lm_tile.hpp -- the tiled matrix product behind the language-model operators (gemm_bias_act,
-// gemm_grouped, gemm_xent and their gradients), with what follows the product in its epilogue.
+// gemm_grouped, gemm_xent and their gradients; newton_schulz), with what follows the product in its epilogue.
 //
 // One kernel template computes out = X * Y^T tile by tile with v_mfma_f32_32x32x16_bf16 and fp32
 // sums, where each operand lies in memory in one of two ways:

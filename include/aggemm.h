@@ -1,6 +1,7 @@
 /*
  * aggemm.h -- C ABI of libaggemm: chunked AllGather fused with a bf16 GEMM, TGATHER, and a language
- * model's operators around the gathered product, on one AMD Instinct MI355X (gfx950).
+ * model's operators around the gathered product (the products, the norms before them, the updates
+ * after them), on one AMD Instinct MI355X (gfx950).
  *
  * Pages this library implements:
  *   [AGMM]  "Triton第四课：基于对称内存融合 AllGather 与 MatMul，提速1.56倍" (the fused
@@ -200,8 +201,9 @@ int ag_gemm_noalloc(const void *const *shards, int32_t N, int64_t M, int64_t K, 
 /* ------------------------------------------------------------------ language-model operators
  *
  * The products of a language model's block and head around the gathered A, with what follows them
- * fused in, and their gradients.  All matrices are bf16, every sum and softmax statistic fp32, outputs
- * rounded once (nearest even).  The conventions above hold, with two additions:
+ * fused in, the norm in front of them, their gradients, and what an optimiser makes of those.  All
+ * matrices are bf16 (newton_schulz takes fp32 too), every sum and statistic fp32, outputs rounded once
+ * (nearest even).  The conventions above hold, with two additions:
  *   - They keep nothing in the library.  A call that needs scratch memory takes `work`, a 16-byte
  *     aligned device buffer of at least `work_bytes`, what the matching ..._workspace() returns for
  *     the same extents (0: `work` may be NULL).  Calls on different streams with different workspaces
@@ -312,10 +314,10 @@ int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float
  *   G (E, R, C) in g_type; out (E, R, C) bf16, may be G's buffer where that is bf16; coefficients: steps x 3 floats on the
  *   HOST, read during the call.
  * Every singular value s of X becomes s (a + b s^2 + c s^4), step by step.  The products take fp16 of X, A and
- * a I + b A + c A A, with fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.  Coefficients whose X could
- * have a singular value above 3.5 on the way, or whose |a + b t + c t^2| could exceed 28 (t: the squares), return
- * AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  A matrix
- * with an infinity or NaN gives NaN throughout.
+ * a I + b A + c A A, with fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.
+ * Coefficients under which X could have a singular value above 3.5 on the way, or |a + b t + c t^2| (t: the squares) could
+ * exceed 28, return AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or
+ * 2^26 in all.  A matrix with an infinity or NaN gives NaN throughout, one of zeros (with eps > 0) zeros.
  */
 #define AG_TYPE_BF16  0
 #define AG_TYPE_F32   1
