@@ -403,12 +403,12 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int64_t firs
             h[c] = piece(c).fit(r.h[c]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = (value(h[c], e) - r.mean) * r.rstd, d = value(dy[c], e);
+                const float off = value(h[c], e) - r.mean, d = value(dy[c], e);
                 const float g = d * value(w[c], e);
                 s1 += g;
-                s2 = fmaf(g, xh, s2);
+                s2 = fmaf(g, off, s2);                 // times rstd at the end: past the row g is 0, but mean rstd may be infinite
                 if constexpr (SUMS) {
-                    dw[c][e] = fmaf(d, xh, dw[c][e]);
+                    dw[c][e] = fmaf(d, off * r.rstd, dw[c][e]);
                     db[c][e] += d;
                     asm volatile("" : "+v"(dw[c][e]), "+v"(db[c][e]));   // added now, not behind the sums over the row
                 }
@@ -418,7 +418,7 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int64_t firs
         if constexpr (!AHEAD)
             fetch_more();
         const float2 s = row_sum<TPR>(s1, s2, s_sum, turn);
-        const float m1 = s.x * inv, m2 = s.y * inv;
+        const float m1 = s.x * inv, m2 = s.y * inv * r.rstd;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             // g and xh again from what is packed: kept, they are sixteen registers for each piece
@@ -529,43 +529,43 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdArgs a)
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t at = row * a.width;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        auto values = [&](int col, int n, float* g, float* xh) {
+        auto values = [&](int col, int n, float* g, float* off) {
             float w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 w[e] = 1.0f;
             load8(a.dy + at + col, n, g);
-            load8(a.h + at + col, n, xh);
+            load8(a.h + at + col, n, off);
             if (a.w)
                 load8(a.w + col, n, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 g[e] *= w[e];
-                xh[e] = (xh[e] - mean) * rstd;
+                off[e] -= mean;
             }
         };
         float s1 = 0.0f, s2 = 0.0f;
         for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
-            float g[8], xh[8];
-            values(col, min(a.width - col, 8), g, xh);
+            float g[8], off[8];
+            values(col, min(a.width - col, 8), g, off);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s1 += g[e];
-                s2 = fmaf(g[e], xh[e], s2);
+                s2 = fmaf(g[e], off[e], s2);
             }
         }
         const float2 s = row_sum<TPR>(s1, s2, s_sum, turn);
-        const float m1 = s.x / count, m2 = s.y / count;
+        const float m1 = s.x / count, m2 = s.y / count * rstd;
         for (int col = threadIdx.x * 8; col < a.width; col += TPR * 8) {
             const int n = min(a.width - col, 8);
-            float g[8], xh[8], dh[8] = {};
-            values(col, n, g, xh);
+            float g[8], off[8], dh[8] = {};
+            values(col, n, g, off);
             if (a.dh)
                 load8(a.dh + at + col, n, dh);
             bf16x8 o;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = (__bf16)fmaf(rstd, g[e] - m1 - xh[e] * m2, dh[e]);
+                o[e] = (__bf16)fmaf(rstd, g[e] - m1 - off[e] * rstd * m2, dh[e]);
             give8(a.dx + at + col, n, o);
         }
     }

@@ -247,3 +247,64 @@ def test_graph_and_streams():
         torch.cuda.synchronize()
         for t, u in zip(out, step()):
             assert torch.equal(t, u), i
+
+
+@pytest.mark.parametrize("width", [9, 100, 1003, 4097, 20001])
+def test_mean_times_rstd_past_fp32(width):
+    """A constant row's gradient is finite though its mean times its rstd is not: nothing past the row's end takes part."""
+    g = gen(13)
+    x = torch.full((300, width), 2.0 ** 110, dtype=BF16, device="cuda")
+    w, dy = normal(g, width), normal(g, 300, width)
+    mean, rstd = torch.empty(2, 300, device="cuda")
+    ag.layer_norm(x, eps=1e-12, mean=mean, rstd=rstd)
+    assert bool((mean == 2.0 ** 110).all()) and bool(torch.isinf(mean * rstd).all())
+    for rows in (300, 2):
+        got = ag.layer_norm_bwd(dy[:rows], x[:rows], mean[:rows], rstd[:rows], weight=w)
+        for name, t, (want, off) in zip(("dx", "dw", "db"), got, backward(dy[:rows], x[:rows], mean[:rows], rstd[:rows], w, None)):
+            near(t, want, off, name)
+
+
+# more than 2^32 values, for every way through memory
+@pytest.mark.parametrize("rows,width", [(45000000, 100), (1100000, 4096), (260000, 17000)])
+def test_offsets_past_32_bits(rows, width):
+    print("norm", rows, width, flush=True)
+    g = gen(14)
+    n = 300
+    x = torch.zeros(rows, width, dtype=BF16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[-n:], dy[-n:] = normal(g, n, width), normal(g, n, width)
+    mean, rstd = torch.empty(2, rows, device="cuda")
+    y = ag.layer_norm(x, eps=EPS, mean=mean, rstd=rstd)
+    at = [t[-n:] for t in (y, mean, rstd)]
+    for name, got, (want, off) in zip(("y", "mean", "rstd"), at, forward(x[-n:], None, None, EPS)):
+        near(got, want, off, name)
+    assert bool((y[:n] == 0).all()) and bool((y[-2 * n:-n] == 0).all())
+    del y
+    dx, dw, db = ag.layer_norm_bwd(dy, x, mean, rstd)
+    for name, t, (want, off) in zip(("dx", "dw", "db"), (dx[-n:], dw, db), backward(dy[-n:], x[-n:], at[1], at[2], None, None)):
+        near(t, want, off, name)
+    assert bool((dx[:n] == 0).all()) and bool((dx[-2 * n:-n] == 0).all())
+
+
+def test_two_streams_at_once():
+    g = gen(15)
+    sets = []
+    for rows, width in ((5000, 1504), (256, 4096)):
+        x, res, w, dy = normal(g, rows, width), normal(g, rows, width), normal(g, width), normal(g, rows, width)
+
+        def step(x=x, res=res, w=w, dy=dy):
+            h = torch.empty_like(x)
+            mean, rstd = torch.empty(2, x.shape[0], device="cuda")
+            y = ag.layer_norm(x, weight=w, residual=res, h=h, mean=mean, rstd=rstd)
+            return (y, h) + ag.layer_norm_bwd(dy, h, mean, rstd, weight=w)
+        sets.append((step, step(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(5):
+        got = []
+        for step, want, stream in sets:
+            with torch.cuda.stream(stream):
+                got.append([step() for _ in range(3)])
+        torch.cuda.synchronize()
+        for (step, want, stream), outs in zip(sets, got):
+            for out in outs:
+                assert all(torch.equal(t, u) for t, u in zip(out, want)), i
