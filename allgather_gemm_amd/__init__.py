@@ -585,7 +585,7 @@ def newton_schulz(G: torch.Tensor, coefficients=NEWTON_SCHULZ, eps: float = 1e-7
     """G (R, C) or each matrix of G (E, R, C), bf16 or fp32, made nearly orthogonal: X = G / (|G| + eps), then for each step's
     (a, b, c) X = a X + (b A + c A A) X with A = X X^T (from the right where R > C).  out: bf16, G's shape; it may be G
     itself where that is bf16.  Written in place where given; the result has no gradient function.  Coefficients under which
-    X could grow past fp16 are refused (aggemm.h has the bounds)."""
+    X could leave fp16's range are refused (aggemm.h has the bounds)."""
     if G.dim() not in (2, 3):
         raise ValueError("G must have 2 or 3 dimensions")
     if G.dtype not in (torch.bfloat16, torch.float32):

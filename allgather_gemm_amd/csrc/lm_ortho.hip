@@ -1012,12 +1012,12 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         return AG_EINVAL;
     if (ortho_too_large(E, R, C))
         return AG_EUNSUPPORTED;
-    // stored values: X, A and B of every step within fp16
+    // stored values: X, A and B of every step within fp16, and not all of X down where it has few bits
     double top = 1.0;
     for (int32_t i = 0; i < steps; ++i) {
         double x, b;
         bounds(coefficients + 3 * i, top, &x, &b);
-        if (top > 3.5 || b > 28.0)
+        if (top > 3.5 || top < 0.015625 || b > 28.0)
             return AG_EUNSUPPORTED;
         top = x;
     }

@@ -288,7 +288,8 @@ int gemm_xent_bwd(const float *dloss, const void *A, const void *B, const int64_
  *   r = 1 / sqrt(mean((h - m)^2) + eps),  y = (h - m) r weight + bias.
  *   x, residual, y, h (rows, width); weight, bias (width); mean, rstd (rows) fp32: m and r.
  * residual, weight (then 1), bias (then 0), h, mean and rstd may be NULL; h needs a residual and may be the same buffer as
- * x or residual.  eps >= 0.  width > 2^21 or rows > 2^30 return AG_EUNSUPPORTED.  Rows may have any length.
+ * x or residual.  eps >= 0.  width > 2^21 or rows > 2^30 return AG_EUNSUPPORTED.  Rows may have any length; nothing is written
+ * for rows of none.
  */
 int layer_norm(const void *x, const void *residual, const void *weight, const void *bias, int64_t rows, int64_t width,
                float eps, void *y, void *h, float *mean, float *rstd, void *stream);
@@ -315,9 +316,10 @@ int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float
  *   HOST, read during the call.
  * Every singular value s of X becomes s (a + b s^2 + c s^4), step by step.  The products take fp16 of X, A and
  * a I + b A + c A A, with fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.
- * Coefficients under which X could have a singular value above 3.5 on the way, or |a + b t + c t^2| (t: the squares) could
- * exceed 28, return AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or
- * 2^26 in all.  A matrix with an infinity or NaN gives NaN throughout, one of zeros (with eps > 0) zeros.
+ * Coefficients under which X could have a singular value above 3.5 on the way, could have none above 2^-6, or
+ * |a + b t + c t^2| (t: the squares) could exceed 28, return AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than
+ * 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  A matrix with an infinity or NaN gives NaN throughout, one of zeros
+ * (with eps > 0) zeros.
  */
 #define AG_TYPE_BF16  0
 #define AG_TYPE_F32   1

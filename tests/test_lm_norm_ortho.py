@@ -81,9 +81,9 @@ def test_schulz_refusals():
     for kw in (dict(C=(1 << 20) + 1), dict(E=65536), dict(R=1 << 19, C=1 << 19), dict(E=60000, R=8192, C=8192)):
         assert schulz(**kw) == ag.AG_EUNSUPPORTED, kw
         assert ag.lib().newton_schulz_workspace(kw.get("E", 1), kw.get("R", 64), kw.get("C", 96)) == 0
-    # iterates that could leave fp16: by their size, by that of b t + c t^2, or at an extremum inside the range
+    # iterates that could leave fp16: downwards, by their size, by that of b t + c t^2, or at an extremum inside the range
     for steps in ([10.0, 0.0, 0.0] * 2, [1.0, -40.0, 0.0], [1.0, 0.0, 30.0], [3.5, 3.5, 3.5] * 2, [2.0, 120.0, -125.0],
-                  [20.0, -36.0, 16.0] * 2):
+                  [20.0, -36.0, 16.0] * 2, [0.015, 0.0, 0.0] * 2, [0.0, 0.0, 0.0] * 2):
         assert schulz(steps=steps) == ag.AG_EUNSUPPORTED, steps
     for kw in (dict(E=0), dict(R=0), dict(C=0)):
         assert schulz(**kw) == ag.AG_OK

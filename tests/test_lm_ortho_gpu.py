@@ -189,3 +189,51 @@ def test_graph_and_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ag.newton_schulz(G)), i
+
+
+def test_offsets_past_32_bits():
+    """A stack of more than 2^32 elements, its first and last matrix the only ones that are not zeros."""
+    E, n = 140, 5600
+    print("stack", E, n, n, flush=True)
+    G = torch.zeros(E, n, n, dtype=BF16, device="cuda")
+    for e in (0, E - 1):
+        G[e] = torch.randn(n, n, generator=gen(20 + e)).to(BF16).cuda()
+    out = ag.newton_schulz(G)
+    for e in (0, E - 1):
+        near(G[e], out[e])
+    assert bool((out[1] == 0).all()) and bool((out[E - 2] == 0).all())
+
+
+def test_two_streams_at_once():
+    """Products in parts, whose counts live in each call's own workspace, and large ones beside them."""
+    sets = []
+    for i, shape in enumerate(((640, 8192), (100, 5440), (1100, 1024))):
+        G = torch.randn(*shape, generator=gen(30 + i)).cuda()
+        sets.append((G, ag.newton_schulz(G), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(5):
+        got = []
+        for G, want, stream in sets:
+            got.append([ag.newton_schulz(G, stream=stream) for _ in range(3)])
+        torch.cuda.synchronize()
+        for (G, want, stream), outs in zip(sets, got):
+            assert all(torch.equal(out, want) for out in outs), (i, tuple(G.shape))
+
+
+@pytest.mark.parametrize("shape", [(640, 8192), (250, 8000), (72, 72)])
+def test_parts_in_a_graph(shape):
+    g = gen(13)
+    G = torch.randn(*shape, generator=g).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        ag.newton_schulz(G)
+        with torch.cuda.graph(graph, stream=side):
+            out = ag.newton_schulz(G)
+    for i in range(4):
+        G.copy_(torch.randn(*shape, generator=g))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ag.newton_schulz(G)), i
