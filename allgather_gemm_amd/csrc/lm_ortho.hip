@@ -17,8 +17,8 @@
 // extents are padded to whole tiles of 128 with zeros, which the steps keep.
 //
 // Five steps of 4096 x 4096 take 1.35 ms, 1.0 PFLOP/s of the products that are computed, of 14336 x 4096 3.65 ms, 1.08: matrix
-// instructions at the clock that the power leaves (busy 0.51-0.54 of the cycles in A A and X X^T, 0.61 in B X, 0.71 in the longer
-// X X^T).  Small matrices wait for their launches, two or three a step of 5 to 10 us.
+// instructions at the clock that the power leaves (busy 0.51-0.54 of the cycles in A A and X X^T, 0.58-0.61 in B X, 0.70 in
+// the longer X X^T).  Small matrices wait for their launches, two or three a step of 5 to 10 us.
 #include "../../include/aggemm.h"
 #include "ag_internal.hpp"
 #include "lm_tile.hpp"
