@@ -308,3 +308,20 @@ def test_two_streams_at_once():
         for (step, want, stream), outs in zip(sets, got):
             for out in outs:
                 assert all(torch.equal(t, u) for t, u in zip(out, want)), i
+
+
+@pytest.mark.parametrize("rows,width", [(33, 1003), (256, 4096), (700, 203), (700, 1003), (600, 4097), (520, 9001), (300, 20001), (9, 7)])
+def test_gradient_added_in_place(rows, width):
+    """The C entry point with dx in dh's buffer, every kernel that has a dh, odd row ends."""
+    g = gen(16)
+    h, w, dy, dh = normal(g, rows, width), normal(g, width), normal(g, rows, width), normal(g, rows, width)
+    mean, rstd = torch.empty(2, rows, device="cuda")
+    ag.layer_norm(h, eps=EPS, mean=mean, rstd=rstd)
+    want = ag.layer_norm_bwd(dy, h, mean, rstd, weight=w, dh=dh)
+    got = dh, torch.empty_like(w), torch.empty_like(w)
+    n = ag.lib().layer_norm_bwd_workspace(rows, width)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    rc = ag.lib().layer_norm_bwd(*(t.data_ptr() for t in (dy, h, mean, rstd, w, dh)), rows, width, *(t.data_ptr() for t in got),
+                                 work.data_ptr() if n else None, n, torch.cuda.current_stream().cuda_stream)
+    assert rc == ag.AG_OK
+    assert all(torch.equal(t, u) for t, u in zip(got, want))
