@@ -33,7 +33,8 @@ struct OrthoArgs : TileArgs {
     float alpha, beta;       // out = alpha sums + beta addend, plus `unit` on the diagonal (kEpiSquare)
     float unit;
     float square_alpha, square_beta;   // B out of A A and A, where X = B X forms it (ortho_thin_kernel)
-    const float* scale;      // the first step's rest of the norm, a factor for each matrix: squared in A, once in X (null: 1)
+    const float* scale;      // for each matrix what X is stored in, see in_units()
+    float now, next;         // X comes in units of min(1, scale now), or (0) of scale; it goes in those of `next`, or (0) of 1
     const _Float16* add;     // addend: A (kEpiSquare); X's remainder, or null (kEpiUpdate)
     _Float16 *hi, *lo;       // the result and (unless null) its remainder
     int64_t ldo, stride;     // of addend and result: rows, matrices
@@ -53,6 +54,16 @@ namespace {
 
 constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;   // stored = true x this
 constexpr int PAD = 128;
+
+// X is stored in units of f: at the start of scale = 2^k / (|G| + eps) <= 2 with |G| in [1/2, 1) 2^k, after a step of
+// min(1, scale g) with g the most that the steps so far can have multiplied a singular value by.  Where eps does not count that is
+// 1, X itself; where |G| is far below eps, X keeps its bits so (as X itself G of 1e-8 eps came out off by 0.4, of 1e-9 as
+// zeros).  A is always that of X itself: where f is small, next to nothing beside a I.  A scale of NaN stays one.
+__device__ __forceinline__ float in_units(float scale, float g)
+{
+    const float f = scale * g;
+    return f > 1.0f ? 1.0f : f;
+}
 
 // A wave's block of 32 rows and FN * 32 columns of 16 bits in its LDS slab, laid out as half_slab_at() has it; three blocks
 // side by side take rows of four, of which `units` 16-byte units are there.
@@ -160,9 +171,9 @@ __device__ __forceinline__ void after_sums(const OrthoArgs& a, const Where& w, A
 {
     typedef Slab<FN> S;
     const uint32_t fr = lane & 31, fh = lane >> 5;
-    const float r = a.scale ? a.scale[w.g] : 1.0f;
-    const float alpha = a.alpha * (EPI == kEpiGram ? r * r : EPI == kEpiUpdate ? r : 1.0f);
-    const float beta = a.beta * (EPI == kEpiUpdate ? r : 1.0f);
+    const float f = EPI == kEpiSquare ? 1.0f : a.now == 0.0f ? w.scale : in_units(w.scale, a.now);
+    const float r = EPI == kEpiGram ? f * f : EPI == kEpiUpdate && a.next != 0.0f ? f / in_units(w.scale, a.next) : f;
+    const float alpha = a.alpha * r, beta = a.beta * (EPI == kEpiUpdate ? r : 1.0f);
     const bool keep = EPI == kEpiUpdate && a.lo, add = EPI == kEpiSquare || (EPI == kEpiUpdate && a.add);
     if (col0 >= a.N)
         return;
@@ -324,7 +335,7 @@ __device__ __forceinline__ void ortho_body(const OrthoArgs& a)
     for (int t = vid; t < whole; t += G) {
         int e, tm, tn;
         tile(t, e, tm, tn);
-        const Where w = {(int64_t)tm * BM, (int64_t)tn * BM, a.M, a.K, 0, e * a.M, tn, e, 0, false};
+        const Where w = {(int64_t)tm * BM, (int64_t)tn * BM, a.M, a.K, 0, e * a.M, tn, e, 0, false, EPI == kEpiSquare ? 1.0f : a.scale[e]};
         product_tile<BM, BM, 2, 2, S, false, TB, EPI>(a, l, w);
     }
     if constexpr (QUARTERS) {
@@ -334,7 +345,7 @@ __device__ __forceinline__ void ortho_body(const OrthoArgs& a)
             const int64_t m0 = (int64_t)tm * BM + (t >> 1 & 1) * (BM / 2), n0 = (int64_t)tn * BM + (t & 1) * (BM / 2);
             if (m0 >= a.M || n0 >= a.N || (EPI != kEpiUpdate && n0 > m0))
                 continue;
-            const Where w = {m0, n0, a.M, a.K, 0, e * a.M, tn, e, 0, false};
+            const Where w = {m0, n0, a.M, a.K, 0, e * a.M, tn, e, 0, false, EPI == kEpiSquare ? 1.0f : a.scale[e]};
             product_tile<BM / 2, BM / 2, 2, 2, 4, false, TB, EPI>(a, lq, w);
         }
     }
@@ -420,6 +431,7 @@ __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a
     }
     if (!TB && tn > tm)
         return;
+    const float scale = EPI == kEpiSquare ? 1.0f : a.scale[e];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
     const uint32_t lda = (uint32_t)a.lda * 2, ldb = (uint32_t)a.ldb * 2, r = tid >> 3, p = tid & 7;
     const uint32_t va = r * lda + ((p ^ swz(r)) * 16);
@@ -495,7 +507,7 @@ __global__ __launch_bounds__(NT, H == 1 ? 2 : 1) void ortho64_kernel(OrthoArgs a
     if constexpr (PARTS)
         if (!join_parts(a, ((int64_t)e * a.tiles_m + tm) * a.tiles_n + tn, part, acc))
             return;
-    const Where w = {tm * 64, tn * 64, a.M, a.K, 0, 0, tn, e, 0, false};
+    const Where w = {tm * 64, tn * 64, a.M, a.K, 0, 0, tn, e, 0, false, scale};
     after_sums<EPI, 1, 1, 2>(a, w, [&](int) { return &acc; }, s0 + wave * 2 * Slab<1>::BYTES, tm * 64 + wm * 32, tn * 64 + wn * 32, lane);
 }
 
@@ -520,6 +532,7 @@ __global__ __launch_bounds__(NT, MP == 256 ? 1 : 2) void ortho_thin_kernel(Ortho
     const uint32_t fr = lane & 31, fh = lane >> 5, wave_off = wave * 1024;
     const int blocks = (int)(a.N / 64), sharers = (int)(gridDim.x / (a.E * KS));      // workgroups of the same rows
     const int first = (int)blockIdx.x % sharers, rb = (int)blockIdx.x / sharers % KS, e = (int)blockIdx.x / sharers / KS;
+    const float scale = a.scale[e];
     char* const stage[4] = {sT0, sT1, KS > 2 ? sT2 : sT0, KS > 2 ? sT3 : sT1};
 
     Side<MP, false> sa;
@@ -632,7 +645,7 @@ __global__ __launch_bounds__(NT, MP == 256 ? 1 : 2) void ortho_thin_kernel(Ortho
                 acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, bf), __builtin_bit_cast(f16x8, af), acc, 0, 0, 0);
             }
         stage_barrier();                               // read: the block after the next may come there
-        const Where w = {rb * 64, b * 64, a.M, a.K, 0, 0, 0, e, 0, false};
+        const Where w = {rb * 64, b * 64, a.M, a.K, 0, 0, 0, e, 0, false, scale};
         after_sums<kEpiUpdate, 1, 1, 2>(a, w, [&](int) { return &acc; }, slab, rb * 64 + wm * 32, (int64_t)b * 64 + wn * 32, lane);
     };
     for (int b = first; b < blocks; b += 2 * sharers) {
@@ -686,8 +699,8 @@ struct StartArgs {
     _Float16 *hi, *lo;       // lo may be null
 };
 
-// X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G.  `scale` gets the
-// rest of the norm.
+// X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G.  `scale` gets what
+// is left of 1 / (|G| + eps).
 template <typename T, bool TURN>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs a)
 {
@@ -703,14 +716,15 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs 
     if ((threadIdx.x & 63) == 0)
         s_sum[threadIdx.x >> 6] = sum;
     barrier_after_lds_write();
-    const double norm = sqrt((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3])) + (double)a.eps;
+    const double size = sqrt((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3])), norm = size + (double)a.eps;
     const bool fine = norm > 0.0 && norm < (double)INFINITY;
     int k = 0;
-    const double part = fine ? frexp(norm, &k) : (double)NAN;           // norm = part 2^k, part in [1/2, 1)
+    if (fine)
+        frexp(size > 0.0 ? size : norm, &k);
     const int tiles = (int)(a.np / 64);
     const int64_t i0 = blockIdx.x / tiles * 64, j0 = (int64_t)(blockIdx.x % tiles) * 64;
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        a.scale[e] = (float)(1.0 / part);
+        a.scale[e] = fine ? fmaxf((float)ldexp(1.0 / norm, k), 0x1p-126f) : NAN;
     if (blockIdx.x == 0 && e == 0)
         for (int64_t i = threadIdx.x; i < a.counts; i += 256)
             a.done[i] = 0;
@@ -1044,6 +1058,8 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
     else
         launch_start<__bf16>(G, o, st, E, s);
     ORTHO_HIP(hipGetLastError(), "launch newton_schulz start");
+    double grown = 0.0;
+    top = 1.0;
     int64_t cur = o.x0, next = o.x1;
     const int64_t xs = o.mp * o.np, as = o.mp * o.mp;
     for (int32_t i = 0; i < steps; ++i) {
@@ -1067,7 +1083,8 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         };
         OrthoArgs p = product(cur, o.np, cur, o.np, o.mp, o.mp, o.np, xs);
         p.alpha = kScaleA / (kScaleX * kScaleX);
-        p.scale = i == 0 ? scale : nullptr;
+        p.scale = scale;
+        p.now = (float)grown;
         p.hi = half(o.a);
         p.sums = reinterpret_cast<float*>(ws + o.sums);
         p.done = reinterpret_cast<uint32_t*>(ws + o.done);
@@ -1089,7 +1106,12 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.unit = a * kScaleB;
         p.alpha = 1.0f / kScaleB;
         p.beta = a;
-        p.scale = i == 0 ? scale : nullptr;
+        p.scale = scale;
+        p.now = (float)grown;
+        double b_most;
+        bounds(coefficients + 3 * i, top, &top, &b_most);
+        grown = std::min(std::max(1.0, (i ? grown : 1.0) * b_most), 0x1p127);
+        p.next = i + 1 < steps ? (float)grown : 0.0f;
         p.add = kept ? half(o.lo) : nullptr;
         p.hi = half(next);
         p.lo = keep ? half(o.lo) : nullptr;

@@ -883,6 +883,7 @@ struct Where {
     int64_t m0, n0, M, K, k_first, grow0;
     int tn, g, split;
     bool zero;                                         // rows past the last group
+    float scale = 1.0f;                                // newton_schulz: OrthoArgs::scale of the tile's matrix
 };
 
 struct OrthoArgs;
