@@ -52,7 +52,7 @@ struct OrthoArgs : TileArgs {
 
 namespace {
 
-constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;   // stored = true x this
+constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f;   // stored = true x this; B: scale_b()
 constexpr int PAD = 128;
 
 // X is stored in units of f: at the start of scale = 2^k / (|G| + eps) <= 2 with |G| in [1/2, 1) 2^k, after a step of
@@ -816,6 +816,16 @@ void bounds(const float* q, double top, double* x, double* b)
         *b = std::max(*b, std::fabs(A - B * B / (4 * C)));
 }
 
+// What B is stored times: 2048, or more where B is small (a last step that only scales: as 2048 times itself it came out off by
+// 1e-2 for a = 1e-9, as zeros for 1e-11).
+float scale_b(double most)
+{
+    float s = 2048.0f;
+    while (most * s < 1024.0 && s < 0x1p110f)
+        s *= 2.0f;
+    return s;
+}
+
 // A launch: its tiles, and how many of the last ones go in quarters.  The least by a model of their times, whose constants are
 // measured; 64 | 128 | 192 | 256 wide, us:  X X^T (A A alike)  1024 x 4096 16 | 28 | 46 | 77,  2048 x 2048 26 | 19 | 29 | 46,
 // 2048 x 5632 73 | 41 | 65 | 109,  4096 x 4096 139 | 99 | 75 | 96,  6016 x 6016 579 | 267 | 255 | 226,  16 of 1024 x 2048
@@ -1065,6 +1075,9 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
     for (int32_t i = 0; i < steps; ++i) {
         const float a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
         const bool keep = i + 1 < steps && keeps(i);
+        double most;
+        bounds(coefficients + 3 * i, top, &top, &most);
+        const float by = scale_b(most);
         auto product = [&](int64_t A, int64_t lda, int64_t B, int64_t ldb, int64_t M, int64_t N, int64_t K, int64_t strideB) {
             OrthoArgs p = {};
             p.A = reinterpret_cast<const __bf16*>(ws + A);
@@ -1089,13 +1102,13 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.sums = reinterpret_cast<float*>(ws + o.sums);
         p.done = reinterpret_cast<uint32_t*>(ws + o.done);
         ORTHO_HIP(launch_ortho<kEpiGram>(p, s), "launch newton_schulz X X^T");
-        const float square_alpha = c * (kScaleB / (kScaleA * kScaleA)), square_beta = b * (kScaleB / kScaleA);
+        const float square_alpha = c * (by / (kScaleA * kScaleA)), square_beta = b * (by / kScaleA);
         const bool thin = o.mp <= 256;
         if (!thin) {
             p = product(o.a, o.mp, o.a, o.mp, o.mp, o.mp, o.mp, as);
             p.alpha = square_alpha;
             p.beta = square_beta;
-            p.unit = a * kScaleB;
+            p.unit = a * by;
             p.add = half(o.a);
             p.hi = half(o.b);
             ORTHO_HIP(launch_ortho<kEpiSquare>(p, s), "launch newton_schulz A A");
@@ -1103,14 +1116,12 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p = product(thin ? o.a : o.b, o.mp, cur, o.np, o.mp, o.np, o.mp, xs);
         p.square_alpha = square_alpha;
         p.square_beta = square_beta;
-        p.unit = a * kScaleB;
-        p.alpha = 1.0f / kScaleB;
+        p.unit = a * by;
+        p.alpha = 1.0f / by;
         p.beta = a;
         p.scale = scale;
         p.now = (float)grown;
-        double b_most;
-        bounds(coefficients + 3 * i, top, &top, &b_most);
-        grown = std::min(std::max(1.0, (i ? grown : 1.0) * b_most), 0x1p127);
+        grown = std::min(std::max(1.0, (i ? grown : 1.0) * most), 0x1p127);
         p.next = i + 1 < steps ? (float)grown : 0.0f;
         p.add = kept ? half(o.lo) : nullptr;
         p.hi = half(next);

@@ -1,4 +1,4 @@
-"""newton_schulz where a factor far from one stands before X or a step: norms far below eps."""
+"""newton_schulz where a factor far from one stands before X or a step: norms far below eps, small coefficients."""
 import pytest
 import torch
 
@@ -54,3 +54,15 @@ def test_eps_without_a_matrix():
     """Zeros over any eps."""
     for eps in (1e-38, 1e-7, 1.0, 3e38):
         assert bool((ag.newton_schulz(torch.zeros(5, 70, device="cuda"), eps=eps) == 0).all()), eps
+
+
+@pytest.mark.parametrize("shape", SHAPES[:5])
+def test_small_last_steps(shape):
+    """A last step that makes X small: out = B X with a B that fp16 of a fixed scale would not hold."""
+    G = torch.randn(*shape, generator=gen(sum(shape) + 1)).cuda()
+    s, n = spectrum(G)
+    for a in (1e-6, 1e-9, 1e-11, 1e-20, 1e-30):
+        for steps in ([(a, 0.0, 0.0)], [(a, -a, 0.3 * a)], [(2.0, -1.5, 0.5)] * 2 + [(-a, a, 0.0)]):
+            o, most = off(ag.newton_schulz(G, coefficients=steps), exact(G, steps)), bound(s, n, steps, True)
+            print("newton_schulz", shape, steps[-1], "%.2e of %.2e" % (o, most), flush=True)
+            assert o <= most, (shape, steps[-1], o, most)
