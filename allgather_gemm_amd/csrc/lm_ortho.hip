@@ -826,6 +826,24 @@ float scale_b(double most)
     return s;
 }
 
+// Whether a step that hardly scales X, where a is next to nothing, leaves X, A and B bits enough in fp16.  For m equal singular
+// values of norm `low` in all, t = low^2 / m: A and B are off by 2^-25 in each entry where these are small (2 sqrt(m) of that in a
+// matrix of m rows), so A of 2^-36 sqrt(m) and B of 2^-24 sqrt(m) / by; X of 2^-37 in each of m n entries.  At most
+// 2^-7 of what they are part of is taken, of which half at most is in the norm.  (0, 1, 0) twice, taken for up to 227 rows, comes out
+// off by 5e-4 for 64, 4e-4 for 256, 1e-2 for 1024 and 0.5 for 2048 x 4096; (1/8, 1/2, 0) twice and (0, 1, 0), just taken for 2048 x
+// 4096, by 2.6e-3.  The
+// largest of the three terms stands for their sum, so that a polynomial may cross zero.  most: bound of B; `low` becomes what it
+// is after the step.
+bool leaves_bits(const float* q, double most, double m, double n, double* low)
+{
+    const double t = *low * *low / m, b = std::fabs((double)q[1]), c = std::fabs((double)q[2]);
+    const double size = std::max(std::fabs((double)q[0]), std::max(b * t, c * t * t)), by = scale_b(most);
+    if (size > 0 && (size < std::sqrt(m) * (0x1p-29 * (b + 2 * c * t) + 0x1p-17 / by) || *low < std::sqrt(m * n) * 0x1p-30))
+        return false;
+    *low = std::min(1.0, *low * size);
+    return true;
+}
+
 // A launch: its tiles, and how many of the last ones go in quarters.  The least by a model of their times, whose constants are
 // measured; 64 | 128 | 192 | 256 wide, us:  X X^T (A A alike)  1024 x 4096 16 | 28 | 46 | 77,  2048 x 2048 26 | 19 | 29 | 46,
 // 2048 x 5632 73 | 41 | 65 | 109,  4096 x 4096 139 | 99 | 75 | 96,  6016 x 6016 579 | 267 | 255 | 226,  16 of 1024 x 2048
@@ -1037,11 +1055,12 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
     if (ortho_too_large(E, R, C))
         return AG_EUNSUPPORTED;
     // stored values: X, A and B of every step within fp16, and not all of X down where it has few bits
-    double top = 1.0;
+    double top = 1.0, low = 1.0;
     for (int32_t i = 0; i < steps; ++i) {
         double x, b;
         bounds(coefficients + 3 * i, top, &x, &b);
-        if (top > 3.5 || top < 0.015625 || b > 28.0)
+        if (top > 3.5 || top < 0.015625 || b > 28.0 ||
+            !leaves_bits(coefficients + 3 * i, b, (double)std::min(R, C), (double)std::max(R, C), &low))
             return AG_EUNSUPPORTED;
         top = x;
     }

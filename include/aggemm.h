@@ -317,8 +317,10 @@ int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float
  * Every singular value s of X becomes s (a + b s^2 + c s^4), step by step.  The products take fp16 of X, A and
  * a I + b A + c A A, with fp32 sums, and what X loses by that is kept beside it where later steps would enlarge it.
  * Coefficients under which X could have a singular value above 3.5 on the way, could have none above 2^-6, or
- * |a + b t + c t^2| (t: the squares) could exceed 28, return AG_EUNSUPPORTED, as do R or C > 2^20, E > 65535, and more than
- * 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  A matrix with an infinity or NaN gives NaN throughout, one of zeros
+ * |a + b t + c t^2| (t: the squares) could exceed 28, return AG_EUNSUPPORTED, as do those whose a's vanish, so that what is left
+ * of R singular values of one size falls where fp16 has no bits ((0, 1, 0) twice is taken for up to 227 rows), R or C > 2^20,
+ * E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  (Where |G| is far below eps, a step whose a is 0
+ * gives zeros.)  A matrix with an infinity or NaN gives NaN throughout, one of zeros
  * (with eps > 0) zeros.
  */
 #define AG_TYPE_BF16  0

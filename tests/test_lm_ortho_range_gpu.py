@@ -1,4 +1,5 @@
-"""newton_schulz where a factor far from one stands before X or a step: norms far below eps, small coefficients."""
+"""newton_schulz where a factor far from one stands before X or a step: norms far below eps, small coefficients, none before
+X itself."""
 import pytest
 import torch
 
@@ -66,3 +67,15 @@ def test_small_last_steps(shape):
             o, most = off(ag.newton_schulz(G, coefficients=steps), exact(G, steps)), bound(s, n, steps, True)
             print("newton_schulz", shape, steps[-1], "%.2e of %.2e" % (o, most), flush=True)
             assert o <= most, (shape, steps[-1], o, most)
+
+
+@pytest.mark.parametrize("shape", SHAPES[:4])
+def test_steps_without_a(shape):
+    """Steps in which X is hardly scaled, as far as they are taken: B is next to nothing but A."""
+    G = torch.randn(*shape, generator=gen(sum(shape) + 2)).cuda()
+    s, n = spectrum(G)
+    for steps in ([(0.0, 1.0, 0.0)], [(0.0, 0.0, 1.0)], [(1e-4, 1.0, 0.0)] * 2, [(0.0, 2.0, 0.0), (1.5, -0.5, 0.0)],
+                  [(0.0, 1.0, 0.0)] * 2)[:5 if len(s) <= 256 else 4]:
+        o, most = off(ag.newton_schulz(G, coefficients=steps), exact(G, steps)), bound(s, n, steps, True)
+        print("newton_schulz", shape, steps, "%.2e of %.2e" % (o, most), flush=True)
+        assert o <= most, (shape, steps, o, most)
