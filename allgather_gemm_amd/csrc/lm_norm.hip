@@ -680,8 +680,11 @@ int64_t bwd_parts(int64_t rows, int64_t width)
 {
     if (rows <= 0 || width <= 0)
         return 0;
+    // Eight threads have a column in each part.  Rows too wide for registers are few; of narrow ones there may be 2^30: then a
+    // thread adds 2^17 of them up, as many as where rows of 8 columns are in registers (in 32 parts it was 2^22, and a dbias of
+    // 2^27 gradients of one sign came out 0.8 % small).
     if (!in_registers(width))
-        return std::min<int64_t>((rows + 31) / 32, 32);
+        return std::min<int64_t>((rows + 31) / 32, width < 8 ? 1024 : 32);
     if (few_rows(rows, width))
         return 0;
     return backward_by_width(width, [&](auto tpr, auto, int per) { return row_workgroups(rows, decltype(tpr)::value, per); });
