@@ -844,21 +844,35 @@ bool leaves_bits(const float* q, double most, double m, double n, double* low)
     return true;
 }
 
-// A launch: its tiles, and how many of the last ones go in quarters.  The least by a model of their times, whose constants are
-// measured; 64 | 128 | 192 | 256 wide, us:  X X^T (A A alike)  1024 x 4096 16 | 28 | 46 | 77,  2048 x 2048 26 | 19 | 29 | 46,
-// 2048 x 5632 73 | 41 | 65 | 109,  4096 x 4096 139 | 99 | 75 | 96,  6016 x 6016 579 | 267 | 255 | 226,  16 of 1024 x 2048
-// 102 | 52 | 71 | 55;  B X  1024 x 4096 19.6 | 16.3 | - | 33,  2048 x 5632 84 | 65 | - | 55,  4096 x 4096 226 | 162 | - | 120,
-// 16 of 1024 x 2048 134 | 107 | - | 80.  (192 x 192 is 253 tiles of 4096 x 4096, a round; a column operand's swizzle has no
-// such width.)  In parts | in one, five steps: 100 x 5440 84 | 129, 250 x 8000 121 | 188, 640 x 8192 215 | 250; 512 x 4096, in
-// one, 149.
+// A launch: its tiles, and how many of the last ones go in quarters.  The least by a model of their times: rounds of a tile on
+// each CU, whose time is (step + crowd * share of the CUs that have one) for 64 of the reduction, plus a start.  Quarters are
+// tiles of half the width, one a CU as well (the workgroup keeps its LDS), so they pay up to a round or two of them; 64 x 64 tiles
+// go two a CU and one after the other.  Constants from a sweep of 50 stacks, which they meet to 5 %; what is chosen is within 1 %
+// of the best on average.  64 | 128 | 192 | 256 wide, q: the last ones in quarters, us:
+//   X X^T  1024 x 4096 16 | 28 | 46 | 77,  2048 x 2048 26 | 20 | 30 | 44,  3200 x 3200 - | 61, q 57 | 47 | 67,  3840 x 3840 - | 71,
+//          q 103 | 61 | 82,  4096 x 4096 - | 96, q 93 | 71 | 91,  4608 x 4608 - | 122, q 140 | 138 | 104,  5760 x 5760 - | 221,
+//          q 220 | 188 | 253, q 198,  6400 x 6400 - | 288, q 345 | 301 | 339, q 259,  7168 x 7168 - | 433, q 422 | 339 | 375, q 363,
+//          8192 x 8192 - | 587, q 578 | 508 | 553, q 487;  16 of 1024 x 2048 102 | 62, q 55 | 72 | 57,  28 of 512 x 512 22 | 20, q 17 | - | 21
+//   A A    16 of 1024 x 1024 - | 44, q 38 | 51 | 40,  else like X X^T of a square
+//   B X    1024 x 4096 20 | 16 | - | 33,  2048 x 5632 84 | 66, q 79 | - | 58,  3200 x 3200 - | 92, q 96 | - | 79,  4096 x 4096
+//          226 | 148 | - | 119,  4608 x 4608 - | 223, q 223 | - | 253, q 195,  6400 x 6400 - | 549, q 585 | - | 513, q 455,
+//          8192 x 8192 - | 1110 | - | 862;  16 of 1024 x 2048 134 | 114 | - | 84,  8 of 512 x 512 10 | 11 | - | 23
+// (192 x 192 is 253 tiles of 4096 x 4096, a round; a column operand's swizzle has no such width.)  In parts | in one, five steps:
+// 100 x 5440 84 | 129, 250 x 8000 121 | 188, 640 x 8192 215 | 250; 512 x 4096, in one, 149.
 struct OrthoTiles {
     int size;
     int64_t rows, cols, all, cut;
     int splits, split_steps;         // workgroups of a tile, steps of 128 that each takes
 };
 
+struct TilePrice {
+    double step, crowd, start;
+};
+
 OrthoTiles plan_tiles(int epi, int64_t E, int64_t M, int64_t N, int64_t K)
 {
+    constexpr TilePrice k128 = {0.28, 0.22, 6.5}, k192 = {0.32, 0.58, 17}, k256 = {0.86, 0.74, 15.5};
+    constexpr TilePrice kQuarter128 = {0.11, 0.11, 3}, kQuarter256 = {0.26, 0.24, 3.5};
     const bool lower = epi != kEpiUpdate;
     int cus = 0;
     if (device_cus(&cus) != hipSuccess || cus <= 0)
@@ -866,17 +880,11 @@ OrthoTiles plan_tiles(int epi, int64_t E, int64_t M, int64_t N, int64_t K)
     const double steps = (double)(K / 64);
     OrthoTiles best = {};
     double least = 1e30;
-    auto tile_us = [&](int size, double fill) {
-        switch (size) {
-        case 64: return (fill > 1 ? 0.36 : 0.16) * steps + (fill > 1 ? 4 : 5.5);
-        case 128: return 0.44 * steps + 5.5;
-        case 192: return (0.7 + 0.35 * fill) * steps + 7;
-        default: return (1.0 + 0.7 * fill) * steps + 14;
-        }
-    };
-    auto rounds = [&](int size, int64_t tiles) {
-        const int64_t room = size == 64 ? 2 * cus : cus, full = tiles / room, rest = tiles % room;
-        return full * tile_us(size, size == 64 ? 2 : 1) + (rest ? tile_us(size, full ? 1 : (double)rest / cus) : 0);
+    // inside: how much of the tiles is
+    auto rounds = [&](const TilePrice& p, int64_t tiles, double inside) {
+        const int64_t rest = tiles % cus;
+        return tiles / cus * ((p.step + p.crowd) * steps + p.start) +
+               (rest ? (p.step + p.crowd * inside * rest / cus) * steps + p.start : 0);
     };
     for (const int size : {64, 128, 192, 256}) {
         if (size == 192 && !lower)
@@ -885,12 +893,21 @@ OrthoTiles plan_tiles(int epi, int64_t E, int64_t M, int64_t N, int64_t K)
         t.all = E * (lower ? t.rows * (t.rows + 1) / 2 : t.rows * t.cols);
         if (size == 64 && t.all > 8 * cus)             // (offsets of 32 bits)
             continue;
-        double us = rounds(size, t.all) + (size == 128 ? 2.5 : 0);
-        if (size == 64 && epi == kEpiGram)             // what the tiles read between them
-            us = std::max(us, 5.5 + 256.0 * t.all * K / 11e6);
+        const TilePrice& price = size == 128 ? k128 : size == 192 ? k192 : k256;
+        const double launch = size == 128 ? 1 : 0;
+        double us;
+        if (size == 64) {
+            const double pairs = (double)t.all / (2 * cus);
+            us = t.all <= cus ? 0.16 * steps + 5.5 : lower ? 3 + pairs * (0.31 * steps + 8) : 3.5 + pairs * (0.39 * steps + 3.7);
+            if (epi == kEpiGram)                       // what the tiles read between them
+                us = std::max(us, 5.5 + 256.0 * t.all * K / 18e6);
+        } else {
+            const double area = E * (lower ? M * (M + (double)size) / 2 : (double)M * N) / (size * size);
+            us = launch + rounds(price, t.all, std::min(1.0, area / t.all));
+        }
         const int64_t rest = t.all % cus;
         if ((size == 128 || size == 256) && t.all > cus && rest) {
-            const double cut = rounds(size, t.all - rest) + rounds(size / 2, 4 * rest) + (size == 128 ? 2.5 : 0);
+            const double cut = launch + rounds(price, t.all - rest, 1) + rounds(size == 128 ? kQuarter128 : kQuarter256, 4 * rest, 1);
             if (cut < us) {
                 us = cut;
                 t.cut = rest;

@@ -10,9 +10,9 @@ pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
 
 # X X^T and A A in 128 x 128 tiles of which the last go in quarters, wide and tall, in stacks; 256 x 256 ones without quarters;
-# B X in 256 x 256 tiles with quarters, turned; two 64 x 64 tiles a CU, turned
+# B X in 256 x 256 tiles with quarters, turned; two 64 x 64 tiles a CU, turned; 128 x 128 ones without quarters, turned
 WAYS = [(1, 2880, 2900), (1, 3000, 2870), (16, 2048, 1024), (16, 1000, 2040), (1, 3400, 4000), (64, 396, 393), (1, 4928, 4928),
-        (1, 8448, 2112), (16, 2059, 301), (8, 349, 268), (8, 268, 349)]
+        (1, 8448, 2112), (16, 2059, 301), (8, 349, 268), (8, 268, 349), (1, 2496, 832)]
 
 
 @pytest.mark.parametrize("i,stack", list(enumerate(WAYS)), ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else "")
