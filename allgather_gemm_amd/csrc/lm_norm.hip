@@ -221,7 +221,11 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a)
 }
 
 // Rows wider than kNormWidest: a workgroup of 1024 threads a row, three times over it.  A thread sees the same columns each
-// time, and where h is kept reads the sum back from there (h may be x's or residual's own buffer).
+// time, and where h is kept reads the sum back from there (h may be x's or residual's own buffer).  With residual and h, us, beside
+// what a copy of as many bytes takes: 6554 x 20480 286 (216), 6500 x 20001 382 (209), 1024 x 131072 308 (216), 128 x 2^20, which half
+// of the CUs have, 505 (216); gradients with dh 332, 468, 359 and 543.  (8192 x 16384 in registers: 193 and 211, 216.)  Rows of
+// fewer than 8 columns come here too and keep one thread of the 1024 at work: right, and slow, 13.2 ms for 2^20 rows of 4 where 8
+// columns take 0.09.  They wait for a kernel of their own.
 __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a)
 {
     constexpr int TPR = 1024;
@@ -671,8 +675,16 @@ int64_t row_workgroups(int64_t rows, int tpr, int per_cu)
     return std::min((rows + at_a_time - 1) / at_a_time, cus() * per_cu);
 }
 
-// Gradients for rows that few workgroups read twice rather than another launch join their sums, us: 256 rows of 256 columns
-// 13.2 | 15.9, 4096 14.3 | 16.0, 8192 11.6 | 23.4; 128 x 4096 11.5 | 16.0
+// Gradients for rows that few workgroups read twice rather than another launch join their sums.  With dh, us, in one launch | two,
+// called one after the other from Python, where two launches cost the host 16:
+//    256 columns  64 rows 11.8 | 16.1, 128 12.0 | 16.0, 256 13.6 | 16.1, 320 16.6 | 16.1;   1024, 256 rows 14.0 | 16.2, 320 16.8 | 16.2
+//   4096, 256 rows 14.6 | 16.1, 320 17.5 | 16.2;   8192, 256 rows 11.8 | 24.2, 320 13.2 | 25.1;   14336, 320 rows 17.6 | 33.9
+// The sides cross near 290 rows up to 4096 columns: the limit.  On the device alone (replayed in a graph) they cross earlier where
+// rows are narrow and a column's sum, 32 rows at a time, is what takes long, and later where they are wide:
+//    256 columns  64 rows 5.0 | 5.8, 128 8.1 | 6.0, 256 14.0 | 6.5;   1024, 64 rows 5.5 | 6.4, 256 14.2 | 6.4;   2000, 160 rows 9.8 | 10.0
+//   4096, 256 rows 15.0 | 15.2;   8192, 384 rows 19.6 | 24.6;   14336, 256 rows 14.7 | 31.8, 448 23.1 | 35.3
+// One rule serves both, for the sums' order is to be the shape's alone.  Rows past 8192 columns, where a kernel of 1024 threads would
+// join in, go the other way, at the figures above.
 bool few_rows(int64_t rows, int64_t width) { return in_registers(width) && width <= 8192 && rows <= 256; }
 
 // rows of partial sums

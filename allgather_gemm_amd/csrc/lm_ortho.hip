@@ -4,7 +4,7 @@
 //   X = B X.
 //
 // Products by fp16 matrix instructions with fp32 sums: the iterates' singular values stay below a bound that the
-// coefficients give (checked by the entry point), so fp16 with a fixed scale holds them, with three bits more than bf16.
+// coefficients give (checked by the entry point), so fp16 with a scale known beforehand holds them, with three bits more than bf16.
 // What a rounding of X does is not the same everywhere: an error among X's small left and right singular directions comes
 // out multiplied by the remaining steps' a's (3.4445^4 after the first of five), any other by about one.  Through A, and
 // through B's own rounding, what is off reaches those directions only times X, which is small there; a rounding of X is in
@@ -16,9 +16,10 @@
 // A and A A are symmetric: their tiles at and below the diagonal are computed, and each is stored on both sides of it.  All
 // extents are padded to whole tiles of 128 with zeros, which the steps keep.
 //
-// Five steps of 4096 x 4096 take 1.35 ms, 1.0 PFLOP/s of the products that are computed, of 14336 x 4096 3.65 ms, 1.08: matrix
-// instructions at the clock that the power leaves (busy 0.51-0.54 of the cycles in A A and X X^T, 0.58-0.61 in B X, 0.70 in
-// the longer X X^T).  Small matrices wait for their launches, two or three a step of 5 to 10 us.
+// Five steps of 4096 x 4096 take 1.34 to 1.40 ms, 1.0 PFLOP/s of the products that are computed, of 14336 x 4096 3.6 to 3.85 ms, 1.06.
+// Matrix instructions run in 0.50-0.54 of the cycles in A A and X X^T, 0.57-0.60 in B X, 0.69 in the longer X X^T, at 1.8 to 1.9 GHz;
+// in the rest the one wave of a SIMD waits (0.17-0.24 of its cycles), reads fragments, starts a tile or stores one.  Small matrices
+// wait for their launches, two or three a step of 5 to 10 us.
 #include "../../include/aggemm.h"
 #include "ag_internal.hpp"
 #include "lm_tile.hpp"
@@ -699,7 +700,8 @@ struct StartArgs {
     _Float16 *hi, *lo;       // lo may be null
 };
 
-// X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G.  `scale` gets what
+// X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G but elements below 2^-28 of
+// its norm (fp16's subnormals: by 2^-37 of the norm at most).  `scale` gets what
 // is left of 1 / (|G| + eps).
 template <typename T, bool TURN>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs a)
@@ -954,7 +956,7 @@ Ortho plan_ortho(int64_t E, int64_t R, int64_t C)
     o.done = region(o.counts * 4);
     o.x0 = region(E * o.mp * o.np * 2);
     o.x1 = region(E * o.mp * o.np * 2);
-    o.lo = region(E * o.mp * o.np * 2);
+    o.lo = region(E * o.mp * o.np * 2);                // (whether a remainder is kept the coefficients say, which are not known here)
     o.a = region(E * o.mp * o.mp * 2);
     o.b = region(E * o.mp * o.mp * 2);
     o.bytes = at;
