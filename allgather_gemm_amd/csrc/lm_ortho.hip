@@ -701,8 +701,7 @@ struct StartArgs {
 };
 
 // X from G, 64 x 64 elements a workgroup: scaled by a power of two, which rounds nothing in a bf16 G but elements below 2^-28 of
-// its norm (fp16's subnormals: by 2^-37 of the norm at most).  `scale` gets what
-// is left of 1 / (|G| + eps).
+// its norm (fp16's subnormals: by 2^-37 of the norm at most).  `scale` gets what is left of 1 / (|G| + eps).
 template <typename T, bool TURN>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs a)
 {
@@ -830,12 +829,11 @@ float scale_b(double most)
 
 // Whether a step that hardly scales X, where a is next to nothing, leaves X, A and B bits enough in fp16.  For m equal singular
 // values of norm `low` in all, t = low^2 / m: A and B are off by 2^-25 in each entry where these are small (2 sqrt(m) of that in a
-// matrix of m rows), so A of 2^-36 sqrt(m) and B of 2^-24 sqrt(m) / by; X of 2^-37 in each of m n entries.  At most
-// 2^-7 of what they are part of is taken, of which half at most is in the norm.  (0, 1, 0) twice, taken for up to 227 rows, comes out
-// off by 5e-4 for 64, 4e-4 for 256, 1e-2 for 1024 and 0.5 for 2048 x 4096; (1/8, 1/2, 0) twice and (0, 1, 0), just taken for 2048 x
-// 4096, by 2.6e-3.  The
-// largest of the three terms stands for their sum, so that a polynomial may cross zero.  most: bound of B; `low` becomes what it
-// is after the step.
+// matrix of m rows), so A of 2^-36 sqrt(m) and B of 2^-24 sqrt(m) / by; X of 2^-37 in each of m n entries.  At most 2^-7 of what
+// they are part of is taken, of which about half is in the result's norm.  (0, 1, 0) twice, taken for up to 227 rows, comes out off by
+// 5e-4 for 64, 4e-4 for 256, 1e-2 for 1024 and 0.5 for 2048 x 4096; (1/8, 1/2, 0) twice and (0, 1, 0), just taken for 2048 x 4096,
+// by 2.6e-3.  The largest of the three terms stands for their sum, so that a polynomial may cross zero.  most: bound of B; `low`
+// becomes what it is after the step.
 bool leaves_bits(const float* q, double most, double m, double n, double* low)
 {
     const double t = *low * *low / m, b = std::fabs((double)q[1]), c = std::fabs((double)q[2]);

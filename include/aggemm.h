@@ -290,7 +290,8 @@ int gemm_xent_bwd(const float *dloss, const void *A, const void *B, const int64_
  * residual, weight (then 1), bias (then 0), h, mean and rstd may be NULL; h needs a residual and may be the same buffer as
  * x or residual.  eps >= 0.  width > 2^21 or rows > 2^30 return AG_EUNSUPPORTED.  Rows may have any length (those of fewer than 8
  * columns take over a hundred times as long as longer ones would, those of more than 16384 half as long again); nothing is written
- * for rows of none.  Means and variances are fp32: differences whose squares add up to more than that holds give an r of 0.
+ * for rows of none.  Sums are fp32: a row whose values add up to more than that holds gives NaN, one whose squared differences do
+ * an r of 0.
  */
 int layer_norm(const void *x, const void *residual, const void *weight, const void *bias, int64_t rows, int64_t width,
                float eps, void *y, void *h, float *mean, float *rstd, void *stream);
@@ -322,9 +323,9 @@ int layer_norm_bwd(const void *dy, const void *h, const float *mean, const float
  * Coefficients under which X could have a singular value above 3.5 on the way, could have none above 2^-6, or
  * |a + b t + c t^2| (t: the squares) could exceed 28, return AG_EUNSUPPORTED, as do those whose a's vanish, so that what is left
  * of R singular values of one size falls where fp16 has no bits ((0, 1, 0) twice is taken for up to 227 rows), R or C > 2^20,
- * E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  (Where |G| is far below eps, a step whose a is 0
- * gives zeros.)  A matrix with an infinity or NaN gives NaN throughout, one of zeros
- * (with eps > 0) zeros.
+ * E > 65535, and more than 2^21 tiles of 128 x 128 in a matrix or 2^26 in all.  Where |G| is far below eps, a step whose a is 0
+ * gives zeros, and steps whose a's are far below the largest |a + b t + c t^2| leave X fewer bits.  A matrix with an infinity or NaN
+ * gives NaN throughout, one of zeros (with eps > 0) zeros.
  */
 #define AG_TYPE_BF16  0
 #define AG_TYPE_F32   1
