@@ -725,7 +725,7 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const T* G, StartArgs 
     const int tiles = (int)(a.np / 64);
     const int64_t i0 = blockIdx.x / tiles * 64, j0 = (int64_t)(blockIdx.x % tiles) * 64;
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        a.scale[e] = fine ? fmaxf((float)ldexp(1.0 / norm, k), 0x1p-126f) : NAN;
+        a.scale[e] = fine ? fmaxf((float)ldexp(1.0 / norm, k), 0x1p-149f) : NAN;
     if (blockIdx.x == 0 && e == 0)
         for (int64_t i = threadIdx.x; i < a.counts; i += 256)
             a.done[i] = 0;
@@ -1157,7 +1157,9 @@ extern "C" int newton_schulz(const void* G, int32_t g_type, int64_t E, int64_t R
         p.beta = a;
         p.scale = scale;
         p.now = (float)grown;
-        grown = std::min(std::max(1.0, (i ? grown : 1.0) * most), 0x1p127);
+        grown = std::max(1.0, (i ? grown : 1.0) * most);
+        if (grown > 0x1p127)                           // from here on X itself, whatever the scale
+            grown = INFINITY;
         p.next = i + 1 < steps ? (float)grown : 0.0f;
         p.add = kept ? half(o.lo) : nullptr;
         p.hi = half(next);

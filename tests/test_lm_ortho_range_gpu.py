@@ -33,6 +33,19 @@ def test_norms_far_below_eps(shape):
         assert o <= most, (shape, norm, eps, o, most)
 
 
+@pytest.mark.parametrize("shape", SHAPES[:4])
+def test_largest_eps(shape):
+    """A norm of 1 beside eps of 3e38, in steps that bring the result back into bf16's range, and steps enough to bring any back."""
+    G = torch.randn(*shape, generator=gen(sum(shape) + 3))
+    G = (G / torch.linalg.vector_norm(G)).cuda()
+    s, n = spectrum(G)
+    for steps in (ag.NEWTON_SCHULZ * 2, ag.NEWTON_SCHULZ * 4):
+        o, most = off(ag.newton_schulz(G, coefficients=steps, eps=3e38), exact(G, steps, 3e38)), bound(s, n, steps, True, 3e38)
+        print("newton_schulz", shape, len(steps), "%.2e of %.2e" % (o, most), flush=True)
+        assert o <= most, (shape, len(steps), o, most)
+    assert bool(torch.isfinite(ag.newton_schulz(G, coefficients=ag.NEWTON_SCHULZ * 30, eps=3e38)).all())
+
+
 def test_stack_of_all_norms():
     """Each matrix of a stack as it is alone, whatever the others' norms; zeros stay zeros."""
     g = gen(1)
